@@ -53,6 +53,7 @@
 #ifndef FG_H
 #define FG_H
 
+#include <stddef.h>
 #include <stdint.h>
 #include <hip/hip_runtime_api.h>
 
@@ -71,7 +72,8 @@ enum {
                             (M x K or N x K bytes, per expert) of
                             2^31 bytes or more, or N > 4194296 (the
                             kernels address these with 32-bit byte
-                            offsets) */
+                            offsets); the row operators' limits are
+                            stated at their declarations */
   FG_EUNSUPPORTED = -2,  /* current device is not gfx950 */
   FG_ELAUNCH = -3,       /* the kernel launch failed (hipGetLastError) */
   FG_EDEVICE = -4        /* a HIP runtime query failed */
@@ -259,6 +261,119 @@ int fg_quant_act_1x128_pow2(const float* x, void* q, float* sa, int batch, int M
                             hipStream_t stream);
 int fg_quant_weight_128x128_pow2(const float* w, void* q, float* sb, int G, int N, int K,
                                  hipStream_t stream);
+
+/*
+ * Row operators: what turns a batch of tokens into the grouped GEMMs' operands
+ * and their outputs back into tokens, and low-rank adapters beside a dense
+ * projection. Conventions as above (device pointers, asynchronous, capturable,
+ * no allocation, bitwise reproducible, nothing is written where a call has no
+ * output). The zwzgs.cn DeepGEMM page's MoE layouts ("Features > layouts",
+ * "Applications > MoE") define the rows these calls produce and consume; the
+ * page takes the routing itself for granted.
+ *
+ * T tokens have k choices each: slot t * k + j is token t's choice j.
+ */
+enum { FG_BF16 = 0, FG_FP32 = 1 };                      /* element types */
+enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 };    /* router scores */
+
+/*
+ * Router: each token's k best of E experts.
+ *   logits [T][E] bf16 or fp32. An expert with logit -inf or NaN is masked.
+ *   score  s = softmax over the unmasked experts, or 1 / (1 + exp(-logit)).
+ *   bias   [E] fp32 or NULL: experts are ranked by s + bias; without it by the
+ *          logits (the order of s). Equal ranks go to the lower index; a rank
+ *          of -inf or NaN is masked too. The bias is no part of the weights.
+ *   ids    [T][k] int32, best first; -1 where fewer than k experts are left.
+ *   w      [T][k] fp32: scale * s, or with renorm scale * s / (sum of the
+ *          token's chosen s) (0 if that sum is 0); 0 where the id is -1.
+ * 1 <= k <= min(E, 64), E <= 1024. T == 0 returns FG_OK.
+ */
+int fg_route_topk(const void* logits, int dtype, const float* bias, int32_t* ids, float* w, int T, int E, int k,
+                  int score, int renorm, float scale, hipStream_t stream);
+
+/*
+ * Gradient of fg_route_topk's w with respect to the logits, the choice taken
+ * as given: ids as it returned them (distinct per token; -1 is skipped), dw
+ * [T][k] fp32, dlogits [T][E] in the logits' type, written in full (0 for
+ * masked experts). The other arguments as in the forward call.
+ */
+int fg_route_topk_grad(const void* logits, int dtype, const int32_t* ids, const float* dw, void* dlogits, int T,
+                       int E, int k, int score, int renorm, float scale, hipStream_t stream);
+
+/*
+ * Plans: the stable sort of the slots by expert (or of tokens by adapter, with
+ * k = 1) into a row layout.
+ *   ids   [T][k] int32; a slot whose id is outside [0, G) gets no row.
+ *   rows  [T][k] int32 out: the slot's row, -1 if it has none.
+ *   slots [rows] int32 out: the row's slot, -1 if it has none.
+ * Contiguous: expert g's slots are rows offsets[g] ..., and every segment
+ *   starts at a multiple of `align` rows (128 for the grouped GEMM; 16, 32 or
+ *   64 for fg_adapters). slots and m_indices have fg_plan_capacity rows, the
+ *   most any ids can need; m_indices is the row's expert or -1, as
+ *   fg_grouped_contiguous reads it; offsets [G + 1], offsets[G] the rows in use.
+ * Masked: row g * M_max + r holds expert g's r-th slot; slots past M_max get no
+ *   row. slots has G * M_max entries; masked_m [G] as fg_grouped_masked reads it.
+ * ws: fg_plan_workspace bytes of scratch (4-byte aligned), free again when the
+ *   call's work on the stream is done; NULL where that is 0. G <= 1024.
+ */
+int fg_plan_capacity(int T, int k, int G, int align, int* rows);
+int fg_plan_workspace(int T, int k, int G, size_t* bytes);
+int fg_plan_contiguous(const int32_t* ids, int32_t* rows, int32_t* slots, int32_t* m_indices, int32_t* offsets,
+                       void* ws, int T, int k, int G, int align, hipStream_t stream);
+int fg_plan_masked(const int32_t* ids, int32_t* rows, int32_t* slots, int32_t* masked_m, void* ws, int T, int k,
+                   int G, int M_max, hipStream_t stream);
+
+/*
+ * Dispatch: every slot's token row, times w[slot] if w is given, quantised as
+ * fg_quant_act_1x128 (scales = FG_SCALES_FP32) or fg_quant_act_1x128_pow2
+ * (FG_SCALES_POW2) would, into the slot's row of the grouped GEMM's A operand.
+ *   x [T][H] bf16 or fp32, rows [T][k] of a plan (a row outside [0, G * M) is
+ *   skipped; rows must be distinct), w [T][k] fp32 or NULL, Q [G][M][H] E4M3,
+ *   sa [G][H/128][M]. Contiguous plan: G = 1 and M = its capacity; masked: G
+ *   and M_max. H % 128 == 0; x and Q 16-byte aligned. Inputs must be finite.
+ */
+int fg_dispatch_quant(const void* x, int dtype, const int32_t* rows, const float* w, void* Q, float* sa, int T,
+                      int k, int H, int G, int M, int scales, hipStream_t stream);
+
+/*
+ * Combine: out[t] = base[t] + sum_j w[t][j] * y[rows[t][j]], in fp32, rounded
+ * once. y [n_rows][N], base [T][N] or NULL, out [T][N] (may be base), all bf16
+ * or all fp32 and 16-byte aligned; w [T][k] fp32 or NULL (all ones: the
+ * gradient of dispatch's copies). A row outside [0, n_rows) adds nothing.
+ * N % 8 == 0. A masked plan's y is its [G * M_max][N].
+ */
+int fg_combine(const void* y, int dtype, const int32_t* rows, const float* w, const void* base, void* out, int T,
+               int k, int N, int n_rows, hipStream_t stream);
+
+/*
+ * Gradient of fg_combine: dw[t][j] = <dout[t], y[row]> (fp32; 0 where the slot
+ * has no row) and dy[row] = w[t][j] * dout[t], in y's type (dy NULL: only dw).
+ * base's gradient is dout itself. The _quant form writes dy as the backward
+ * GEMM's operand, as fg_dispatch_quant(dout, w) would (N % 128 == 0; y has
+ * G * M rows; dout and y must be finite). Rows without a slot are not written.
+ */
+int fg_combine_grad(const void* dout, const void* y, int dtype, const int32_t* rows, const float* w, void* dy,
+                    float* dw, int T, int k, int N, int n_rows, hipStream_t stream);
+int fg_combine_grad_quant(const void* dout, const void* y, int dtype, const int32_t* rows, const float* w, void* Q,
+                          float* sq, float* dw, int T, int k, int N, int G, int M, int scales, hipStream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection:
+ *   out[t] = D[t] + scales[a] * (x[t] . A[a]^T) . B[a]^T, a = the token's adapter,
+ * in fp32, rounded once; out[t] = D[t] for a token without one.
+ *   D, out [T][N] bf16 (out may be D), x [T][K] bf16, A [L][R][K] bf16,
+ *   B [L][N][R] bf16, scales [L] fp32; rows, slots, m_indices: the contiguous
+ *   plan of the tokens' adapter ids (k = 1, G = L), cap its rows and align its
+ *   alignment, a multiple of 16. A tile has 64 rows if 64 divides align, else
+ *   32 or 16: 64 suits prompts (many tokens per adapter), 16 decode.
+ *   R % 8 == 0, 8 <= R <= 128 (smaller adapters are padded with zeros);
+ *   K % 128 == 0, N % 8 == 0; tensors 16-byte aligned.
+ *   ws: fg_adapters_workspace bytes, 16-byte aligned.
+ */
+int fg_adapters_workspace(int R, int K, int cap, int align, size_t* bytes);
+int fg_adapters(const void* D, const void* x, const void* A, const void* B, const float* scales, const int32_t* rows,
+                const int32_t* slots, const int32_t* m_indices, void* out, void* ws, int T, int L, int R, int K, int N,
+                int cap, int align, hipStream_t stream);
 
 /* Static, human-readable description of a return code. */
 const char* fg_strerror(int code);

@@ -52,6 +52,19 @@ def _declare(L):
     L.fg_gemm_fp8_nt_swiglu_quant.argtypes = [vp, fp, vp, fp, vp, fp, fp, i, i, i, i, vp]
     L.fg_grouped_contiguous_swiglu_quant.argtypes = [vp, fp, vp, fp, vp, fp, fp, ip, i, i, i, i, i, vp]
     L.fg_grouped_masked_swiglu_quant.argtypes = [vp, fp, vp, fp, vp, fp, fp, ip, i, i, i, i, i, vp]
+    sz, f = ctypes.POINTER(ctypes.c_size_t), ctypes.c_float
+    L.fg_route_topk.argtypes = [vp, i, fp, ip, fp, i, i, i, i, i, f, vp]
+    L.fg_route_topk_grad.argtypes = [vp, i, ip, fp, vp, i, i, i, i, i, f, vp]
+    L.fg_plan_capacity.argtypes = [i, i, i, i, ipp]
+    L.fg_plan_workspace.argtypes = [i, i, i, sz]
+    L.fg_plan_contiguous.argtypes = [ip, ip, ip, ip, ip, vp, i, i, i, i, vp]
+    L.fg_plan_masked.argtypes = [ip, ip, ip, ip, vp, i, i, i, i, vp]
+    L.fg_dispatch_quant.argtypes = [vp, i, ip, fp, vp, fp, i, i, i, i, i, i, vp]
+    L.fg_combine.argtypes = [vp, i, ip, fp, vp, vp, i, i, i, i, vp]
+    L.fg_combine_grad.argtypes = [vp, vp, i, ip, fp, vp, fp, i, i, i, i, vp]
+    L.fg_combine_grad_quant.argtypes = [vp, vp, i, ip, fp, vp, fp, fp, i, i, i, i, i, i, vp]
+    L.fg_adapters_workspace.argtypes = [i, i, i, i, sz]
+    L.fg_adapters.argtypes = [vp, vp, vp, vp, fp, ip, ip, ip, vp, vp, i, i, i, i, i, i, i, vp]
     L.fg_strerror.argtypes = [i]
     L.fg_strerror.restype = ctypes.c_char_p
     for name in ENTRY_POINTS:
@@ -66,7 +79,10 @@ ENTRY_POINTS = ("fg_gemm_fp8_nt", "fg_grouped_contiguous", "fg_grouped_masked",
                 "fg_grouped_masked_pow2", "fg_quant_act_1x128_pow2",
                 "fg_quant_weight_128x128_pow2", "fg_gemm_fp8_nt_swiglu_quant",
                 "fg_grouped_contiguous_swiglu_quant", "fg_grouped_masked_swiglu_quant",
-                "fg_strerror")
+                "fg_route_topk", "fg_route_topk_grad", "fg_plan_capacity", "fg_plan_workspace",
+               "fg_plan_contiguous", "fg_plan_masked", "fg_dispatch_quant", "fg_combine",
+               "fg_combine_grad", "fg_combine_grad_quant", "fg_adapters_workspace", "fg_adapters",
+               "fg_strerror")
 
 
 def load(path):
@@ -109,8 +125,12 @@ def _call(fn, dev, *args):
     launches on the current device, on the stream passed last) and raises
     FGError on a nonzero return code."""
     torch = _torch()
-    with torch.cuda.device(dev):
-        _check(getattr(lib(), fn)(*args), fn)
+    if torch.cuda.current_device() == dev.index:
+        code = getattr(lib(), fn)(*args)
+    else:
+        with torch.cuda.device(dev):
+            code = getattr(lib(), fn)(*args)
+    _check(code, fn)
 
 
 def _fp8(t, name, shape, device=None):
@@ -384,3 +404,312 @@ def _quant_weight(fn, w, q, sb):
     _dev(sb, "sb", sb_shape, torch.float32, w.device)
     _call(fn, w.device, _ptr(w), _ptr(q), _ptr(sb), G, N, K, _stream(w))
     return q, sb
+
+
+# ---------------------------------------------------------------- row operators
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _elem(t, name):
+    """fg.h element type of an activation tensor."""
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float32:
+        return 1
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _score(score):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    return SCORES[score]
+
+
+def _new(t, name, shape, dtype, dev):
+    """An output: the caller's, checked, or a new one."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=dev)
+    _dev(t, name, shape, dtype, dev)
+    return t
+
+
+def route_topk(logits, k, score="softmax", bias=None, renorm=False, scale=1.0, ids=None, w=None):
+    """Each token's k best experts from router logits [T, E] (bf16 or fp32; -inf or NaN
+    masks an expert): (ids [T, k] int32, best first, -1 where fewer are left, w [T, k]
+    fp32). score: "softmax" or "sigmoid"; bias [E] fp32 is added to the scores for the
+    ranking only; renorm divides the chosen scores by their sum; scale multiplies w.
+    Ties go to the lower index."""
+    torch = _torch()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    dev = logits.device
+    dt, sc = _elem(logits, "logits"), _score(score)
+    if not 1 <= k <= min(E, 64):
+        raise ValueError(f"k must be in 1 .. min(E, 64), got {k} for E = {E}")
+    _dev(logits, "logits", (T, E))
+    if bias is not None:
+        _dev(bias, "bias", (E,), torch.float32, dev)
+    ids = _new(ids, "ids", (T, k), torch.int32, dev)
+    w = _new(w, "w", (T, k), torch.float32, dev)
+    _call("fg_route_topk", dev, _ptr(logits), dt, _opt_ptr(bias), _ptr(ids), _ptr(w), T, E, k, sc, int(bool(renorm)),
+          scale, _stream(logits))
+    return ids, w
+
+
+def route_topk_grad(logits, ids, dw, score="softmax", renorm=False, scale=1.0, dlogits=None):
+    """Gradient of route_topk's w [T, k] with respect to its logits, the choice ids taken as
+    given; the other arguments as in the forward call. Returns dlogits, in logits' type."""
+    torch = _torch()
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and ids [T, k]")
+    T, E = logits.shape
+    k = ids.shape[1]
+    dev = logits.device
+    dt, sc = _elem(logits, "logits"), _score(score)
+    _dev(logits, "logits", (T, E))
+    _dev(ids, "ids", (T, k), torch.int32, dev)
+    _dev(dw, "dw", (T, k), torch.float32, dev)
+    dlogits = _new(dlogits, "dlogits", (T, E), logits.dtype, dev)
+    _call("fg_route_topk_grad", dev, _ptr(logits), dt, _ptr(ids), _ptr(dw), _ptr(dlogits), T, E, k, sc,
+          int(bool(renorm)), scale, _stream(logits))
+    return dlogits
+
+
+class Plan:
+    """Where each (token, choice) slot's row is in a grouped GEMM's layout; made by
+    plan_contiguous or plan_masked, or from tensors of the same meaning.
+
+    rows [T, k] int32: the slot's row, -1 if none; slots int32: each row's slot t * k + j,
+    -1 if none. Contiguous: m_indices (per row, as grouped_contiguous takes it), offsets
+    [G + 1], align. Masked: masked_m [G], M_max; row g * M_max + r is row r of expert g."""
+    __slots__ = ("layout", "rows", "slots", "m_indices", "offsets", "align", "masked_m", "M_max", "G")
+
+    def __init__(self, layout, rows, slots, m_indices, offsets, align, masked_m, M_max, G):
+        self.layout, self.rows, self.slots, self.G = layout, rows, slots, G
+        self.m_indices, self.offsets, self.align = m_indices, offsets, align
+        self.masked_m, self.M_max = masked_m, M_max
+
+    @classmethod
+    def contiguous(cls, rows, slots, m_indices, offsets, align):
+        torch = _torch()
+        _plan_rows(rows, slots)
+        _dev(m_indices, "m_indices", (slots.shape[0],), torch.int32, rows.device)
+        _dev(offsets, "offsets", (offsets.numel(),), torch.int32, rows.device)
+        if align < 1 or slots.shape[0] % align or offsets.numel() < 2:
+            raise ValueError("a contiguous plan has G + 1 >= 2 offsets and a multiple of align rows")
+        return cls(LAYOUT_CONTIGUOUS, rows, slots, m_indices, offsets, align, None, 0, offsets.numel() - 1)
+
+    @classmethod
+    def masked(cls, rows, slots, masked_m, M_max):
+        torch = _torch()
+        _plan_rows(rows, slots)
+        _dev(masked_m, "masked_m", (masked_m.numel(),), torch.int32, rows.device)
+        if slots.shape[0] != masked_m.numel() * M_max or M_max < 1 or masked_m.numel() < 1:
+            raise ValueError("a masked plan has G * M_max slots")
+        return cls(LAYOUT_MASKED, rows, slots, None, None, 1, masked_m, M_max, masked_m.numel())
+
+    @property
+    def capacity(self):
+        """Rows of the layout (masked: G * M_max)."""
+        return self.slots.shape[0]
+
+    def lead(self):
+        """Leading dimensions of the layout's tensors: (capacity,) or (G, M_max)."""
+        return (self.G, self.M_max) if self.layout == LAYOUT_MASKED else (self.slots.shape[0],)
+
+
+def _plan_rows(rows, slots):
+    torch = _torch()
+    if rows.dim() != 2 or slots.dim() != 1:
+        raise ValueError("rows must be [T, k] and slots [rows]")
+    _dev(rows, "rows", tuple(rows.shape), torch.int32)
+    _dev(slots, "slots", tuple(slots.shape), torch.int32, rows.device)
+
+
+def _plan_args(ids, G):
+    torch = _torch()
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    T, k = ids.shape
+    _dev(ids, "ids", (T, k), torch.int32)
+    if not 1 <= G <= 1024 or k < 1:
+        raise ValueError("G must be in 1 .. 1024 and k at least 1")
+    size = ctypes.c_size_t()
+    _check(lib().fg_plan_workspace(T, k, G, ctypes.byref(size)), "fg_plan_workspace")
+    ws = torch.empty(size.value, dtype=torch.uint8, device=ids.device) if size.value else None
+    return T, k, ws
+
+
+def plan_capacity(T, k, G, align=128):
+    """Rows of a contiguous plan, the most that any ids [T, k] can need; host-only."""
+    rows = ctypes.c_int()
+    _check(lib().fg_plan_capacity(T, k, G, align, ctypes.byref(rows)), "fg_plan_capacity")
+    return rows.value
+
+
+def plan_contiguous(ids, G, align=128):
+    """Stable sort of the slots by expert (ids [T, k] int32; outside [0, G): no row) into the
+    contiguous layout, segments starting at multiples of align rows. Returns a Plan."""
+    torch = _torch()
+    T, k, ws = _plan_args(ids, G)
+    dev = ids.device
+    cap = plan_capacity(T, k, G, align)
+    rows, slots, m_indices, offsets = (torch.empty(n, dtype=torch.int32, device=dev)
+                                       for n in ((T, k), cap, cap, G + 1))
+    _call("fg_plan_contiguous", dev, _ptr(ids), _ptr(rows), _ptr(slots), _ptr(m_indices), _ptr(offsets),
+          _opt_ptr(ws), T, k, G, align, _stream(ids))
+    return Plan(LAYOUT_CONTIGUOUS, rows, slots, m_indices, offsets, align, None, 0, G)
+
+
+def plan_masked(ids, G, M_max):
+    """The same into the masked layout: at most M_max rows per expert, later slots get no row."""
+    torch = _torch()
+    T, k, ws = _plan_args(ids, G)
+    if M_max < 1 or G * M_max > 0x7fffffff:
+        raise ValueError("M_max must be at least 1 and G * M_max below 2^31")
+    dev = ids.device
+    rows, slots, masked_m = (torch.empty(n, dtype=torch.int32, device=dev) for n in ((T, k), G * M_max, G))
+    _call("fg_plan_masked", dev, _ptr(ids), _ptr(rows), _ptr(slots), _ptr(masked_m), _opt_ptr(ws), T, k, G, M_max,
+          _stream(ids))
+    return Plan(LAYOUT_MASKED, rows, slots, None, None, 1, masked_m, M_max, G)
+
+
+def _quant_rows(plan, H, dev, Q, sa):
+    """The sorted E4M3 operand: Q [*lead, H], sa [H/128, capacity] or [G, H/128, M_max]."""
+    torch = _torch()
+    lead = plan.lead()
+    sa_shape = lead[:-1] + (H // 128, lead[-1])
+    if H % 128:
+        raise ValueError("rows must be a multiple of 128 long")
+    if Q is None:
+        Q = torch.empty(lead + (H,), dtype=torch.uint8, device=dev)
+    else:
+        _fp8(Q, "Q", lead + (H,), dev)
+    sa = _new(sa, "sa", sa_shape, torch.float32, dev)
+    G, M = (lead if len(lead) == 2 else (1,) + lead)
+    return Q, sa, G, M
+
+
+def _token_rows(t, name, plan, dev=None):
+    T = plan.rows.shape[0]
+    if t.dim() != 2 or t.shape[0] != T:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{T}, columns]")
+    _dev(t, name, tuple(t.shape), device=plan.rows.device)
+    return t.shape[1]
+
+
+def dispatch_quant(x, plan, w=None, pow2=False, Q=None, sa=None):
+    """Token rows x [T, H] (bf16 or fp32), times w [T, k] if given, into the plan's layout as
+    the grouped GEMM's A operand: E4M3 codes Q ([capacity, H] or [G, M_max, H]) and scales sa
+    ([H/128, capacity] or [G, H/128, M_max]). Rows without a slot are not written."""
+    torch = _torch()
+    dt = _elem(x, "x")
+    H = _token_rows(x, "x", plan)
+    dev = x.device
+    T, k = plan.rows.shape
+    if w is not None:
+        _dev(w, "w", (T, k), torch.float32, dev)
+    Q, sa, G, M = _quant_rows(plan, H, dev, Q, sa)
+    _call("fg_dispatch_quant", dev, _ptr(x), dt, _ptr(plan.rows), _opt_ptr(w), _ptr(Q), _ptr(sa), T, k, H, G, M,
+          int(bool(pow2)), _stream(x))
+    return Q, sa
+
+
+def _sorted_rows(y, plan, dev):
+    if y.dim() != len(plan.lead()) + 1:
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected {plan.lead()} + (N,)")
+    N = y.shape[-1]
+    _dev(y, "y", plan.lead() + (N,), device=dev)
+    if N % 8 or N < 8:
+        raise ValueError("N must be a positive multiple of 8")
+    return N
+
+
+def combine(y, plan, w=None, base=None, out=None):
+    """out[t] = base[t] + sum_j w[t, j] y[row of slot (t, j)]: the experts' rows back in token
+    order ([T, N], y's type). w None: all ones, which is dispatch's gradient. out may be base."""
+    torch = _torch()
+    dev = plan.rows.device
+    dt = _elem(y, "y")
+    N = _sorted_rows(y, plan, dev)
+    T, k = plan.rows.shape
+    if w is not None:
+        _dev(w, "w", (T, k), torch.float32, dev)
+    if base is not None:
+        _dev(base, "base", (T, N), y.dtype, dev)
+    out = _new(out, "out", (T, N), y.dtype, dev)
+    _call("fg_combine", dev, _ptr(y), dt, _ptr(plan.rows), _opt_ptr(w), _opt_ptr(base), _ptr(out), T, k, N,
+          plan.capacity, _stream(y))
+    return out
+
+
+def dispatch_grad(dA, plan, out=None):
+    """Gradient of dispatch's copies with respect to x: the sum of each token's sorted rows."""
+    return combine(dA, plan, out=out)
+
+
+def _combine_grad_args(dout, y, plan, w, dw):
+    torch = _torch()
+    dev = plan.rows.device
+    dt = _elem(y, "y")
+    N = _sorted_rows(y, plan, dev)
+    T, k = plan.rows.shape
+    _dev(dout, "dout", (T, N), y.dtype, dev)
+    _dev(w, "w", (T, k), torch.float32, dev)
+    return dev, dt, N, T, k, _new(dw, "dw", (T, k), torch.float32, dev)
+
+
+def combine_grad(dout, y, plan, w, dy=None, dw=None, with_dy=True):
+    """Gradient of combine: (dy in y's shape and type, rows without a slot not written, or None
+    with with_dy=False; dw [T, k] fp32)."""
+    torch = _torch()
+    dev, dt, N, T, k, dw = _combine_grad_args(dout, y, plan, w, dw)
+    if dy is not None or with_dy:
+        dy = _new(dy, "dy", tuple(y.shape), y.dtype, dev)
+    _call("fg_combine_grad", dev, _ptr(dout), _ptr(y), dt, _ptr(plan.rows), _ptr(w), _opt_ptr(dy), _ptr(dw), T, k, N,
+          plan.capacity, _stream(dout))
+    return dy, dw
+
+
+def combine_grad_quant(dout, y, plan, w, pow2=False, Q=None, sa=None, dw=None):
+    """combine_grad with dy as the backward GEMM's operand: (Q E4M3 codes, sa scales, dw)."""
+    dev, dt, N, T, k, dw = _combine_grad_args(dout, y, plan, w, dw)
+    Q, sa, G, M = _quant_rows(plan, N, dev, Q, sa)
+    _call("fg_combine_grad_quant", dev, _ptr(dout), _ptr(y), dt, _ptr(plan.rows), _ptr(w), _ptr(Q), _ptr(sa),
+          _ptr(dw), T, k, N, G, M, int(bool(pow2)), _stream(dout))
+    return Q, sa, dw
+
+
+def adapters(D, x, A, B, scales, plan, out=None):
+    """Low-rank adapters of many requests beside a shared projection: out[t] = D[t] +
+    scales[a] (x[t] . A[a]^T) . B[a]^T for token t's adapter a, D[t] for a token without one.
+    D [T, N], x [T, K], A [L, R, K], B [L, N, R] bf16, scales [L] fp32; plan: plan_contiguous of
+    the tokens' adapter ids [T, 1] with align 64 (prompts) or 16 (decode). out may be D (in place)."""
+    torch = _torch()
+    if D.dim() != 2 or x.dim() != 2 or A.dim() != 3:
+        raise ValueError("D must be [T, N], x [T, K] and A [L, R, K]")
+    if plan.layout != LAYOUT_CONTIGUOUS or plan.rows.shape[1] != 1 or plan.align % 16:
+        raise ValueError("adapters need a contiguous plan of ids [T, 1] with align a multiple of 16")
+    T, N = D.shape
+    L, R, K = A.shape
+    dev = D.device
+    bf = torch.bfloat16
+    if plan.rows.shape[0] != T or plan.G != L or plan.rows.device != dev:
+        raise ValueError(f"the plan is of {plan.rows.shape[0]} tokens and {plan.G} adapters on "
+                         f"{plan.rows.device}, the call of {T} and {L} on {dev}")
+    if R % 8 or not 8 <= R <= 128 or K % 128 or N % 8:
+        raise ValueError("R must be a multiple of 8 up to 128, K of 128 and N of 8")
+    _dev(D, "D", (T, N), bf, dev)
+    _dev(x, "x", (T, K), bf, dev)
+    _dev(A, "A", (L, R, K), bf, dev)
+    _dev(B, "B", (L, N, R), bf, dev)
+    _dev(scales, "scales", (L,), torch.float32, dev)
+    out = _new(out, "out", (T, N), bf, dev)
+    size = ctypes.c_size_t()
+    _check(lib().fg_adapters_workspace(R, K, plan.capacity, plan.align, ctypes.byref(size)), "fg_adapters_workspace")
+    ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
+    _call("fg_adapters", dev, _ptr(D), _ptr(x), _ptr(A), _ptr(B), _ptr(scales), _ptr(plan.rows), _ptr(plan.slots),
+          _ptr(plan.m_indices), _ptr(out), _ptr(ws), T, L, R, K, N, plan.capacity, plan.align, _stream(D))
+    return out

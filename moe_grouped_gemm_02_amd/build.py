@@ -4,7 +4,8 @@ Run ``python -m moe_grouped_gemm_02_amd.build`` (or call ``build()``). The
 shared object is written next to this file so that it travels with the source
 tree; nothing is installed elsewhere. The GEMM kernels of each layout and scale
 kind are compiled as separate objects (fg_launch.hip with FG_LAUNCH_PART =
-2 * layout + pow2), in parallel, then linked with the host and quantiser code.
+2 * layout + pow2), in parallel, then linked with the host and quantiser code
+and the row operators (routing, sorting, row movement, adapters).
 
 libfg_ceiling.so (fg_ceiling.hip) is a benchmark helper that bench.py loads to
 measure the matrix cores' ceiling on this device; the library does not use it.
@@ -28,9 +29,10 @@ CEILING_LIB = os.path.join(HERE, "libfg_ceiling.so")
 LAUNCH_PARTS = 6   # {dense, contiguous, masked} x {fp32 scales, power-of-two scales}
 # (object name, source, extra flags)
 UNITS = [("fg_host", "fg_host.hip", []), ("fg_host_testing", "fg_host.hip", ["-DFG_TESTING"]),
-         ("fg_quant", "fg_quant.hip", []), ("fg_ceiling", "fg_ceiling.hip", [])] + [
+         ("fg_quant", "fg_quant.hip", []), ("fg_route", "fg_route.hip", []), ("fg_plan", "fg_plan.hip", []),
+         ("fg_rows", "fg_rows.hip", []), ("fg_adapters", "fg_adapters.hip", []), ("fg_ceiling", "fg_ceiling.hip", [])] + [
     (f"fg_launch_{i}", "fg_launch.hip", [f"-DFG_LAUNCH_PART={i}"]) for i in range(LAUNCH_PARTS)]
-HEADERS = ["fg_kernel.hpp", "fg_e4m3.hpp", "fg_tiles.hpp"]
+HEADERS = ["fg_kernel.hpp", "fg_e4m3.hpp", "fg_tiles.hpp", "fg_device.hpp", "fg_wave.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "fg.h"
+#include "fg_device.hpp"
 #include "fg_tiles.hpp"
 
 namespace {
@@ -22,8 +23,10 @@ constexpr int kMaxN = 4194296;
 std::atomic<int> g_dev_state[kMaxDevices];  // 0 unknown, 1 gfx950, -1 other
 std::atomic<int> g_dev_cus[kMaxDevices];
 
+}  // namespace
+
 // Checks that the current device is gfx950; caches its CU count.
-int current_device(int* cus) {
+int fg::current_device(int* cus) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return FG_EDEVICE;
   if (dev < 0 || dev >= kMaxDevices) return FG_EDEVICE;
@@ -40,6 +43,8 @@ int current_device(int* cus) {
   if (cus) *cus = g_dev_cus[dev].load(std::memory_order_relaxed);
   return FG_OK;
 }
+
+namespace {
 
 // ---------------------------------------------------------------- tiles
 struct Tile {
@@ -265,7 +270,8 @@ struct FusedOut {
   float* act = nullptr;
 };
 
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using fg::aligned;
+using fg::current_device;
 
 // pow2: every sa and sb is a power of two, applied by the matrix core as an
 // E8M0 block scale (no separate promotion). fused: write the SiLU-gated,
@@ -508,7 +514,7 @@ int fgt_force_runs(int on) {
 const char* fg_strerror(int code) {
   switch (code) {
     case FG_OK: return "success";
-    case FG_EINVAL: return "invalid argument (null pointer, negative size, K not a multiple of 128, N not a multiple of 8 (256 for the fused epilogue), K < 128, misaligned pointer, G < 1, unknown layout or scale kind, an operand of 2^31 bytes or more, N > 4194296)";
+    case FG_EINVAL: return "invalid argument (null pointer, negative size, K not a multiple of 128, N not a multiple of 8 (256 for the fused epilogue), K < 128, misaligned pointer, G < 1, unknown layout or scale kind, an operand of 2^31 bytes or more, N > 4194296; for the row operators: E, G or L > 1024, k > min(E, 64), rank not a multiple of 8 up to 128, a missing workspace)";
     case FG_EUNSUPPORTED: return "unsupported device (gfx950 required)";
     case FG_ELAUNCH: return "kernel launch failed";
     case FG_EDEVICE: return "HIP device query failed";

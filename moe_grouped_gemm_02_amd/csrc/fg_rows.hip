@@ -1,0 +1,376 @@
+// fg_rows.hip -- token rows into and out of the grouped GEMMs' sorted layouts,
+// and the gradient of the way back.
+//
+// With row = rows[t, j] the sorted row of token t's choice j (none where it is
+// outside the layout, such as -1):
+//
+//   dispatch      Q[row] = e4m3(w[t, j] x[t] / s),  s = amax / 448 of each 1x128 block
+//   combine       out[t] = base[t] + sum_j w[t, j] y[row]
+//   combine_grad  dw[t, j] = <dout[t], y[row]>,  dy[row] = w[t, j] dout[t]
+//
+// in fp32 with one rounding at the end. The gradient of dispatch's copies is
+// combine with all weights one.
+//
+// All are bound by memory traffic. Each goes by tokens, not by sorted rows: a
+// token's row is read from HBM once and used for all its choices, and whole
+// rows of several KB are read or written at each sorted row, so the indirection
+// costs no bandwidth. A lane handles 16 consecutive elements (or 16 bytes), so
+// eight lanes hold a 1x128 block and its largest value takes three DPP steps.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "fg.h"
+#include "fg_device.hpp"
+#include "fg_e4m3.hpp"
+#include "fg_wave.hpp"
+
+namespace {
+
+using namespace fg;
+
+constexpr int kThreads = 256;
+
+// Sorted E4M3 rows: codes [GM][H], scales [G][H/128][M] with GM = G * M rows.
+struct QuantOut {
+  uint8_t* Q;
+  float* sa;
+  int H, M, GM;
+};
+
+// 16 elements of a row starting at element 16 * i.
+template <class R>
+__device__ __forceinline__ void load16(const void* x, long row, int H, int i, float* f) {
+  const u32x4* p = (const u32x4*)((const char*)x + (row * H + 16L * i) * R::kBytes);
+  constexpr int N = 16 / R::kPer16;
+#pragma unroll
+  for (int c = 0; c < N; ++c) R::unpack(p[c], f + c * R::kPer16);
+}
+
+__device__ __forceinline__ float amax16(const float* f) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
+  return m;
+}
+
+// Codes of 16 values of a block with scale s (inv its reciprocal if pow2).
+__device__ __forceinline__ u32x4 encode16(const float* f, float s, bool pow2) {
+  u32x4 q;
+  if (pow2) {
+    const float inv = 1.0f / s;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) q[c] = e4m3x4_mul(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3], inv);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) q[c] = e4m3x4_div(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3], s);
+  }
+  return q;
+}
+
+// Stores unit i (16 codes) of sorted row `row`, and the block's scale from the
+// first of its eight lanes.
+__device__ __forceinline__ void store_unit(const QuantOut& o, int row, int i, u32x4 q, float s) {
+  *(u32x4*)(o.Q + (long)row * o.H + 16L * i) = q;
+  if ((i & 7) == 0) {
+    const int g = row / o.M, r = row - g * o.M;
+    o.sa[((long)g * (o.H >> 7) + (i >> 3)) * o.M + r] = s;
+  }
+}
+
+// Token and unit of this lane when a token has `per` units, lanes taken in order.
+__device__ __forceinline__ bool unit_of(int per, int T, long* t, int* i) {
+  const long b0 = (long)blockIdx.x * kThreads;
+  const long t0 = b0 / per;                       // uniform
+  const unsigned v = (unsigned)(b0 - t0 * per) + threadIdx.x;
+  const unsigned q = v / (unsigned)per;
+  *t = t0 + q;
+  *i = (int)(v - q * (unsigned)per);
+  return *t < T;
+}
+
+template <class R, bool POW2, bool W>
+__global__ __launch_bounds__(kThreads) void dispatch_quant(const void* __restrict__ x,
+                                                           const int32_t* __restrict__ rows,
+                                                           const float* __restrict__ w, QuantOut o, int T, int k) {
+  long t;
+  int i;
+  if (!unit_of(o.H >> 4, T, &t, &i)) return;   // whole groups of eight lanes leave together
+  float f[16];
+  load16<R>(x, t, o.H, i, f);
+  if (!W) {
+    float s = block_scale(group8_max(amax16(f)));
+    if (POW2) s = pow2_up(s);
+    const u32x4 q = encode16(f, s, POW2);
+    for (int j = 0; j < k; ++j) {
+      const int row = rows[t * k + j];
+      if ((unsigned)row < (unsigned)o.GM) store_unit(o, row, i, q, s);
+    }
+  } else {
+    for (int j = 0; j < k; ++j) {
+      const int row = rows[t * k + j];
+      if ((unsigned)row >= (unsigned)o.GM) continue;
+      const float wj = w[t * k + j];
+      float v[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = f[e] * wj;
+      float s = block_scale(group8_max(amax16(v)));
+      if (POW2) s = pow2_up(s);
+      store_unit(o, row, i, encode16(v, s, POW2), s);
+    }
+  }
+}
+
+template <class R, bool W>
+__global__ __launch_bounds__(kThreads) void combine(const void* __restrict__ y, const int32_t* __restrict__ rows,
+                                                    const float* __restrict__ w, const void* __restrict__ base,
+                                                    void* __restrict__ out, int T, int k, int N, int n_rows) {
+  long t;
+  int i;
+  const int per = N / R::kPer16;
+  if (!unit_of(per, T, &t, &i)) return;
+  float acc[R::kPer16];
+  const u32x4* yv = (const u32x4*)y;
+#pragma unroll
+  for (int e = 0; e < R::kPer16; ++e) acc[e] = 0.0f;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    u32x4 v[4];
+    float wj[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int j = j0 + c;
+      const int row = j < k ? rows[t * k + j] : -1;
+      const bool ok = (unsigned)row < (unsigned)n_rows;
+      wj[c] = !ok ? 0.0f : W ? w[t * k + j] : 1.0f;
+      v[c] = ok ? yv[(long)row * per + i] : u32x4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float f[R::kPer16];
+      R::unpack(v[c], f);
+#pragma unroll
+      for (int e = 0; e < R::kPer16; ++e) acc[e] = fmaf(wj[c], f[e], acc[e]);
+    }
+  }
+  if (base) {
+    float f[R::kPer16];
+    R::unpack(((const u32x4*)base)[t * per + i], f);
+#pragma unroll
+    for (int e = 0; e < R::kPer16; ++e) acc[e] += f[e];
+  }
+  ((u32x4*)out)[t * per + i] = R::pack(acc);
+}
+
+// One workgroup per token: its row of dout stays in registers for a unit at a
+// time while the choices' rows of y pass by; JC choices per sweep of the row.
+constexpr int kGradChoices = 8;
+
+// Sums acc[JC] over the workgroup in a fixed order and writes dw.
+__device__ __forceinline__ void reduce_dw(float* acc, float (*part)[kGradChoices], float* dw, int n) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int c = 0; c < kGradChoices; ++c) {
+    const float s = wave_sum(acc[c]);
+    if (lane == 0) part[wave][c] = s;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < n) {
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kThreads / 64; ++v) s += part[v][threadIdx.x];
+    dw[threadIdx.x] = s;
+  }
+  __syncthreads();
+}
+
+template <class R>
+__global__ __launch_bounds__(kThreads) void combine_grad(const void* __restrict__ dout, const void* __restrict__ y,
+                                                         const int32_t* __restrict__ rows,
+                                                         const float* __restrict__ w, void* __restrict__ dy,
+                                                         float* __restrict__ dw, int k, int N, int n_rows) {
+  __shared__ float part[kThreads / 64][kGradChoices];
+  const long t = blockIdx.x;
+  const int per = N / R::kPer16;
+  const u32x4* dv = (const u32x4*)dout + t * per;
+  for (int j0 = 0; j0 < k; j0 += kGradChoices) {
+    const int n = k - j0 < kGradChoices ? k - j0 : kGradChoices;
+    float acc[kGradChoices], wj[kGradChoices];
+    int row[kGradChoices];
+#pragma unroll
+    for (int c = 0; c < kGradChoices; ++c) {
+      const int r = c < n ? rows[t * k + j0 + c] : -1;
+      row[c] = (unsigned)r < (unsigned)n_rows ? r : -1;
+      wj[c] = c < n ? w[t * k + j0 + c] : 0.0f;
+      acc[c] = 0.0f;
+    }
+    for (int i = threadIdx.x; i < per; i += kThreads) {
+      float d[R::kPer16];
+      R::unpack(dv[i], d);
+#pragma unroll
+      for (int c = 0; c < kGradChoices; ++c) {
+        if (row[c] < 0) continue;   // uniform
+        float f[R::kPer16];
+        const long at = (long)row[c] * per + i;
+        R::unpack(((const u32x4*)y)[at], f);
+#pragma unroll
+        for (int e = 0; e < R::kPer16; ++e) {
+          acc[c] = fmaf(d[e], f[e], acc[c]);
+          f[e] = wj[c] * d[e];
+        }
+        if (dy) ((u32x4*)dy)[at] = R::pack(f);
+      }
+    }
+    reduce_dw(acc, part, dw + t * k + j0, n);
+  }
+}
+
+template <class R, bool POW2>
+__global__ __launch_bounds__(kThreads) void combine_grad_quant(const void* __restrict__ dout,
+                                                               const void* __restrict__ y,
+                                                               const int32_t* __restrict__ rows,
+                                                               const float* __restrict__ w, QuantOut o,
+                                                               float* __restrict__ dw, int k) {
+  __shared__ float part[kThreads / 64][kGradChoices];
+  const long t = blockIdx.x;
+  const int per = o.H >> 4;
+  for (int j0 = 0; j0 < k; j0 += kGradChoices) {
+    const int n = k - j0 < kGradChoices ? k - j0 : kGradChoices;
+    float acc[kGradChoices], wj[kGradChoices];
+    int row[kGradChoices];
+#pragma unroll
+    for (int c = 0; c < kGradChoices; ++c) {
+      const int r = c < n ? rows[t * k + j0 + c] : -1;
+      row[c] = (unsigned)r < (unsigned)o.GM ? r : -1;
+      wj[c] = c < n ? w[t * k + j0 + c] : 0.0f;
+      acc[c] = 0.0f;
+    }
+    for (int i = threadIdx.x; i < per; i += kThreads) {   // whole groups of eight lanes
+      float d[16];
+      load16<R>(dout, t, o.H, i, d);
+#pragma unroll
+      for (int c = 0; c < kGradChoices; ++c) {
+        if (row[c] < 0) continue;
+        float f[16];
+        load16<R>(y, row[c], o.H, i, f);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          acc[c] = fmaf(d[e], f[e], acc[c]);
+          f[e] = wj[c] * d[e];
+        }
+        float s = block_scale(group8_max(amax16(f)));
+        if (POW2) s = pow2_up(s);
+        store_unit(o, row[c], i, encode16(f, s, POW2), s);
+      }
+    }
+    reduce_dw(acc, part, dw + t * k + j0, n);
+  }
+}
+
+bool type_ok(int dtype) { return dtype == FG_BF16 || dtype == FG_FP32; }
+
+// Sizes of the E4M3 rows: G x M of them, H columns.
+int check_quant(int dtype, int T, int k, int H, int G, int M, int scales) {
+  if (T < 0 || k < 1 || H < 128 || H % 128 || H > (1 << 24) || G < 1 || M < 1 || !type_ok(dtype)) return FG_EINVAL;
+  if ((scales != FG_SCALES_FP32 && scales != FG_SCALES_POW2) || (long long)G * M > 0x7fffffffLL) return FG_EINVAL;
+  return FG_OK;
+}
+
+int check_rows(int dtype, int T, int k, int N, int n_rows) {
+  if (T < 0 || k < 1 || N < 8 || N % 8 || N > (1 << 24) || n_rows < 0 || !type_ok(dtype)) return FG_EINVAL;
+  return FG_OK;
+}
+
+// Workgroups of kThreads lanes for T tokens of `per` units; 0: too many.
+unsigned unit_grid(int T, int per) {
+  const long long n = ((long long)T * per + kThreads - 1) / kThreads;
+  return n > 0x7fffffffLL ? 0u : (unsigned)n;
+}
+
+template <class R>
+void launch_dispatch(bool pow2, unsigned grid, hipStream_t s, const void* x, const int32_t* rows, const float* w,
+                     const QuantOut& o, int T, int k) {
+  const dim3 g(grid), b(kThreads);
+  if (pow2 && w) hipLaunchKernelGGL((dispatch_quant<R, true, true>), g, b, 0, s, x, rows, w, o, T, k);
+  else if (pow2) hipLaunchKernelGGL((dispatch_quant<R, true, false>), g, b, 0, s, x, rows, w, o, T, k);
+  else if (w) hipLaunchKernelGGL((dispatch_quant<R, false, true>), g, b, 0, s, x, rows, w, o, T, k);
+  else hipLaunchKernelGGL((dispatch_quant<R, false, false>), g, b, 0, s, x, rows, w, o, T, k);
+}
+
+int launched() { return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH; }
+
+}  // namespace
+
+extern "C" {
+
+int fg_dispatch_quant(const void* x, int dtype, const int32_t* rows, const float* w, void* Q, float* sa, int T,
+                      int k, int H, int G, int M, int scales, hipStream_t stream) {
+  const int rc = check_quant(dtype, T, k, H, G, M, scales);
+  if (rc != FG_OK || T == 0) return rc;
+  if (!x || !rows || !Q || !sa || !aligned(x, 16) || !aligned(rows, 4) || !aligned(Q, 16) || !aligned(sa, 4) ||
+      (w && !aligned(w, 4)))
+    return FG_EINVAL;
+  const unsigned grid = unit_grid(T, H / 16);
+  if (grid == 0) return FG_EINVAL;
+  const int st = current_device(nullptr);
+  if (st != FG_OK) return st;
+  const QuantOut o = {static_cast<uint8_t*>(Q), sa, H, M, G * M};
+  const bool pow2 = scales == FG_SCALES_POW2;
+  if (dtype == FG_BF16) launch_dispatch<RowBf16>(pow2, grid, stream, x, rows, w, o, T, k);
+  else launch_dispatch<RowF32>(pow2, grid, stream, x, rows, w, o, T, k);
+  return launched();
+}
+
+int fg_combine(const void* y, int dtype, const int32_t* rows, const float* w, const void* base, void* out, int T,
+               int k, int N, int n_rows, hipStream_t stream) {
+  const int rc = check_rows(dtype, T, k, N, n_rows);
+  if (rc != FG_OK || T == 0) return rc;
+  if ((!y && n_rows) || !rows || !out || !aligned(y, 16) || !aligned(rows, 4) || !aligned(out, 16) ||
+      (w && !aligned(w, 4)) || (base && !aligned(base, 16)))
+    return FG_EINVAL;
+  const unsigned grid = unit_grid(T, dtype == FG_BF16 ? N / 8 : N / 4);
+  if (grid == 0) return FG_EINVAL;
+  const int st = current_device(nullptr);
+  if (st != FG_OK) return st;
+  const dim3 g(grid), b(kThreads);
+  if (dtype == FG_BF16 && w) hipLaunchKernelGGL((combine<RowBf16, true>), g, b, 0, stream, y, rows, w, base, out, T, k, N, n_rows);
+  else if (dtype == FG_BF16) hipLaunchKernelGGL((combine<RowBf16, false>), g, b, 0, stream, y, rows, w, base, out, T, k, N, n_rows);
+  else if (w) hipLaunchKernelGGL((combine<RowF32, true>), g, b, 0, stream, y, rows, w, base, out, T, k, N, n_rows);
+  else hipLaunchKernelGGL((combine<RowF32, false>), g, b, 0, stream, y, rows, w, base, out, T, k, N, n_rows);
+  return launched();
+}
+
+int fg_combine_grad(const void* dout, const void* y, int dtype, const int32_t* rows, const float* w, void* dy,
+                    float* dw, int T, int k, int N, int n_rows, hipStream_t stream) {
+  const int rc = check_rows(dtype, T, k, N, n_rows);
+  if (rc != FG_OK || T == 0) return rc;
+  if (!dout || (!y && n_rows) || !rows || !w || !dw || !aligned(dout, 16) || !aligned(y, 16) || !aligned(rows, 4) ||
+      !aligned(w, 4) || !aligned(dw, 4) || (dy && !aligned(dy, 16)))
+    return FG_EINVAL;
+  const int st = current_device(nullptr);
+  if (st != FG_OK) return st;
+  const dim3 g((unsigned)T), b(kThreads);
+  if (dtype == FG_BF16) hipLaunchKernelGGL((combine_grad<RowBf16>), g, b, 0, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
+  else hipLaunchKernelGGL((combine_grad<RowF32>), g, b, 0, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
+  return launched();
+}
+
+int fg_combine_grad_quant(const void* dout, const void* y, int dtype, const int32_t* rows, const float* w, void* Q,
+                          float* sq, float* dw, int T, int k, int N, int G, int M, int scales, hipStream_t stream) {
+  const int rc = check_quant(dtype, T, k, N, G, M, scales);
+  if (rc != FG_OK || T == 0) return rc;
+  if (!dout || !y || !rows || !w || !Q || !sq || !dw || !aligned(dout, 16) || !aligned(y, 16) || !aligned(rows, 4) ||
+      !aligned(w, 4) || !aligned(Q, 16) || !aligned(sq, 4) || !aligned(dw, 4))
+    return FG_EINVAL;
+  const int st = current_device(nullptr);
+  if (st != FG_OK) return st;
+  const QuantOut o = {static_cast<uint8_t*>(Q), sq, N, M, G * M};
+  const dim3 g((unsigned)T), b(kThreads);
+  const bool pow2 = scales == FG_SCALES_POW2;
+  if (dtype == FG_BF16 && pow2) hipLaunchKernelGGL((combine_grad_quant<RowBf16, true>), g, b, 0, stream, dout, y, rows, w, o, dw, k);
+  else if (dtype == FG_BF16) hipLaunchKernelGGL((combine_grad_quant<RowBf16, false>), g, b, 0, stream, dout, y, rows, w, o, dw, k);
+  else if (pow2) hipLaunchKernelGGL((combine_grad_quant<RowF32, true>), g, b, 0, stream, dout, y, rows, w, o, dw, k);
+  else hipLaunchKernelGGL((combine_grad_quant<RowF32, false>), g, b, 0, stream, dout, y, rows, w, o, dw, k);
+  return launched();
+}
+
+}  // extern "C"
