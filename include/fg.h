@@ -278,7 +278,7 @@ enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 };    /* router scores */
 
 /*
  * Router: each token's k best of E experts.
- *   logits [T][E] bf16 or fp32. An expert with logit -inf or NaN is masked.
+ *   logits [T][E] bf16 or fp32, 16-byte aligned. An expert with logit -inf or NaN is masked.
  *   score  s = softmax over the unmasked experts, or 1 / (1 + exp(-logit)).
  *   bias   [E] fp32 or NULL: experts are ranked by s + bias; without it by the
  *          logits (the order of s). Equal ranks go to the lower index; a rank
@@ -294,7 +294,7 @@ int fg_route_topk(const void* logits, int dtype, const float* bias, int32_t* ids
 /*
  * Gradient of fg_route_topk's w with respect to the logits, the choice taken
  * as given: ids as it returned them (distinct per token; -1 is skipped), dw
- * [T][k] fp32, dlogits [T][E] in the logits' type, written in full (0 for
+ * [T][k] fp32, dlogits [T][E] in the logits' type (16-byte aligned), written in full (0 for
  * masked experts). The other arguments as in the forward call.
  */
 int fg_route_topk_grad(const void* logits, int dtype, const int32_t* ids, const float* dw, void* dlogits, int T,

@@ -17,6 +17,7 @@ Tensor conventions (all on the same CUDA/HIP device, contiguous):
     D   bfloat16                [M, N]        (masked: [G, M_max, N])
 """
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -115,9 +116,18 @@ def _torch():
     return torch
 
 
+_raw_stream = None
+
+
 def _stream(t):
-    torch = _torch()
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    """The current HIP stream of t's device as an address. torch's raw getter takes 0.1 us;
+    a Stream object, where a torch has no such getter, 1.9 us, a third of a small call."""
+    global _raw_stream
+    if _raw_stream is None:
+        torch = _torch()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(t.device.index)
 
 
 def _call(fn, dev, *args):
@@ -143,6 +153,9 @@ def _fp8(t, name, shape, device=None):
 def _dev(t, name, shape, dtype=None, device=None):
     """Checks a tensor argument: on a GPU (on `device` if given), of `dtype`
     (if given), of `shape`, contiguous."""
+    if (t.is_cuda and t.shape == shape and (dtype is None or t.dtype is dtype)
+            and (device is None or t.device == device) and t.is_contiguous()):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if device is not None and t.device != device:
@@ -156,7 +169,7 @@ def _dev(t, name, shape, dtype=None, device=None):
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def gemm_fp8_nt(A, sa, B, sb, D):
@@ -260,7 +273,7 @@ def _fused_outputs(lead, I, M, dev, Q, sq, act, with_act):
 
 
 def _opt_ptr(t):
-    return ctypes.c_void_p(0) if t is None else _ptr(t)
+    return None if t is None else t.data_ptr()
 
 
 def gemm_fp8_nt_swiglu_quant(A, sa, B, sb, Q=None, sq=None, act=None, pow2=False, with_act=False):
@@ -536,17 +549,29 @@ def _plan_args(ids, G):
     _dev(ids, "ids", (T, k), torch.int32)
     if not 1 <= G <= 1024 or k < 1:
         raise ValueError("G must be in 1 .. 1024 and k at least 1")
+    size = _plan_workspace(T, k, G)
+    return T, k, torch.empty(size, dtype=torch.uint8, device=ids.device) if size else None
+
+
+@functools.lru_cache(maxsize=1024)
+def _plan_workspace(T, k, G):
     size = ctypes.c_size_t()
     _check(lib().fg_plan_workspace(T, k, G, ctypes.byref(size)), "fg_plan_workspace")
-    ws = torch.empty(size.value, dtype=torch.uint8, device=ids.device) if size.value else None
-    return T, k, ws
+    return size.value
 
 
+@functools.lru_cache(maxsize=1024)
 def plan_capacity(T, k, G, align=128):
     """Rows of a contiguous plan, the most that any ids [T, k] can need; host-only."""
     rows = ctypes.c_int()
     _check(lib().fg_plan_capacity(T, k, G, align, ctypes.byref(rows)), "fg_plan_capacity")
     return rows.value
+
+
+def _int32_parts(dev, *sizes):
+    """New int32 vectors of these sizes in one allocation."""
+    torch = _torch()
+    return torch.empty(sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes)
 
 
 def plan_contiguous(ids, G, align=128):
@@ -556,8 +581,8 @@ def plan_contiguous(ids, G, align=128):
     T, k, ws = _plan_args(ids, G)
     dev = ids.device
     cap = plan_capacity(T, k, G, align)
-    rows, slots, m_indices, offsets = (torch.empty(n, dtype=torch.int32, device=dev)
-                                       for n in ((T, k), cap, cap, G + 1))
+    m_indices, slots, rows, offsets = _int32_parts(dev, cap, cap, T * k, G + 1)
+    rows = rows.view(T, k)
     _call("fg_plan_contiguous", dev, _ptr(ids), _ptr(rows), _ptr(slots), _ptr(m_indices), _ptr(offsets),
           _opt_ptr(ws), T, k, G, align, _stream(ids))
     return Plan(LAYOUT_CONTIGUOUS, rows, slots, m_indices, offsets, align, None, 0, G)
@@ -570,7 +595,8 @@ def plan_masked(ids, G, M_max):
     if M_max < 1 or G * M_max > 0x7fffffff:
         raise ValueError("M_max must be at least 1 and G * M_max below 2^31")
     dev = ids.device
-    rows, slots, masked_m = (torch.empty(n, dtype=torch.int32, device=dev) for n in ((T, k), G * M_max, G))
+    slots, rows, masked_m = _int32_parts(dev, G * M_max, T * k, G)
+    rows = rows.view(T, k)
     _call("fg_plan_masked", dev, _ptr(ids), _ptr(rows), _ptr(slots), _ptr(masked_m), _opt_ptr(ws), T, k, G, M_max,
           _stream(ids))
     return Plan(LAYOUT_MASKED, rows, slots, None, None, 1, masked_m, M_max, G)
@@ -682,6 +708,13 @@ def combine_grad_quant(dout, y, plan, w, pow2=False, Q=None, sa=None, dw=None):
     return Q, sa, dw
 
 
+@functools.lru_cache(maxsize=1024)
+def _adapters_workspace(R, K, cap, align):
+    size = ctypes.c_size_t()
+    _check(lib().fg_adapters_workspace(R, K, cap, align, ctypes.byref(size)), "fg_adapters_workspace")
+    return size.value
+
+
 def adapters(D, x, A, B, scales, plan, out=None):
     """Low-rank adapters of many requests beside a shared projection: out[t] = D[t] +
     scales[a] (x[t] . A[a]^T) . B[a]^T for token t's adapter a, D[t] for a token without one.
@@ -707,9 +740,7 @@ def adapters(D, x, A, B, scales, plan, out=None):
     _dev(B, "B", (L, N, R), bf, dev)
     _dev(scales, "scales", (L,), torch.float32, dev)
     out = _new(out, "out", (T, N), bf, dev)
-    size = ctypes.c_size_t()
-    _check(lib().fg_adapters_workspace(R, K, plan.capacity, plan.align, ctypes.byref(size)), "fg_adapters_workspace")
-    ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
+    ws = torch.empty(_adapters_workspace(R, K, plan.capacity, plan.align), dtype=torch.uint8, device=dev)
     _call("fg_adapters", dev, _ptr(D), _ptr(x), _ptr(A), _ptr(B), _ptr(scales), _ptr(plan.rows), _ptr(plan.slots),
           _ptr(plan.m_indices), _ptr(out), _ptr(ws), T, L, R, K, N, plan.capacity, plan.align, _stream(D))
     return out

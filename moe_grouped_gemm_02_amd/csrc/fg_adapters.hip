@@ -27,6 +27,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "fg.h"
 #include "fg_device.hpp"
@@ -39,6 +40,7 @@ using namespace fg;
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kMaxRank = 128;
 constexpr int kStepK = 64;
+constexpr size_t kSpareBytes = 64 * 16;
 
 struct AdapterArgs {
   const uint16_t *D, *x, *A, *B;
@@ -46,10 +48,12 @@ struct AdapterArgs {
   const int32_t *rows, *slots, *m_indices;
   uint16_t* out;
   float* ws;              // [parts][cap][16 * TR]
+  uint16_t* spare;        // 64 x 16 bytes that hold nothing
   int T, L, R, K, N, cap;
   int parts;              // parts of K
   int strip;              // columns of one expand workgroup
   int tiles;              // row tiles
+  int copies;             // workgroups of expand that pass tokens through
 };
 
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
@@ -58,26 +62,25 @@ __device__ __forceinline__ f32x4v mfma(u32x4 a, u32x4 b, f32x4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
-// TM: 16-row groups of a tile, TR: 16-column groups of the rank.
-template <int TM, int TR>
-__global__ __launch_bounds__(kThreads) void adapter_shrink(AdapterArgs p) {
-  constexpr int RT = 16 * TM, RC = 16 * TR, RP = RC + 4;
+// TR: 16-column groups of the rank.
+//
+// 16-row tiles (decode: few tokens per adapter, so A is read once and nothing is
+// shared): the four waves split the part's K, each lane's fragments come straight
+// from global memory, two steps under way, and the waves' sums meet in LDS.
+template <int TR>
+__global__ __launch_bounds__(kThreads) void adapter_shrink16(AdapterArgs p) {
+  constexpr int RT = 16, RC = 16 * TR, RP = RC + 4;
   __shared__ float red[kWaves][RT][RP];
-  const int tile = blockIdx.x, r0 = tile * RT;
+  const int r0 = blockIdx.x * RT;
   const int a = p.m_indices[r0];
   if ((unsigned)a >= (unsigned)p.L) return;   // no token in this tile (uniform)
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lrow = lane & 15, q = lane >> 4;
 
   // rows without a token repeat the tile's first one; their sums are not stored
-  const int first = p.slots[r0];
-  const uint16_t* xp[TM];
-#pragma unroll
-  for (int m = 0; m < TM; ++m) {
-    const int s = p.slots[r0 + 16 * m + lrow];
-    const int tok = (unsigned)s < (unsigned)p.T ? s : (unsigned)first < (unsigned)p.T ? first : 0;
-    xp[m] = p.x + (long)tok * p.K + 16 * q;
-  }
+  const int first = p.slots[r0], mine = p.slots[r0 + lrow];
+  const int tok = (unsigned)mine < (unsigned)p.T ? mine : (unsigned)first < (unsigned)p.T ? first : 0;
+  const uint16_t* xp = p.x + (long)tok * p.K + 16 * q;
   const uint16_t* ap[TR];
 #pragma unroll
   for (int c = 0; c < TR; ++c) {
@@ -86,40 +89,49 @@ __global__ __launch_bounds__(kThreads) void adapter_shrink(AdapterArgs p) {
   }
   const int steps = p.K / kStepK;
   const int lanes = p.parts * kWaves, me = blockIdx.y * kWaves + wave;
-  const int s0 = (int)((long)steps * me / lanes), s1 = (int)((long)steps * (me + 1) / lanes);
+  const int s0 = steps * me / lanes, s1 = steps * (me + 1) / lanes;
 
-  f32x4v acc[TR][TM];
+  f32x4v acc[TR];
 #pragma unroll
-  for (int c = 0; c < TR; ++c)
-#pragma unroll
-    for (int m = 0; m < TM; ++m) acc[c][m] = f32x4v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-  for (int s = s0; s < s1; ++s) {
-    u32x4 xf[TM][2], af[TR][2];
-#pragma unroll
-    for (int m = 0; m < TM; ++m) {
-      const u32x4* v = (const u32x4*)(xp[m] + (long)s * kStepK);
-      xf[m][0] = v[0];
-      xf[m][1] = v[1];
-    }
+  for (int c = 0; c < TR; ++c) acc[c] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  struct Step {
+    u32x4 x[2], a[TR][2];
+  };
+  const auto load = [&](Step& f, int s) {
+    const u32x4* v = (const u32x4*)(xp + (long)s * kStepK);
+    f.x[0] = v[0];
+    f.x[1] = v[1];
 #pragma unroll
     for (int c = 0; c < TR; ++c) {
-      const u32x4* v = (const u32x4*)(ap[c] + (long)s * kStepK);
-      af[c][0] = v[0];
-      af[c][1] = v[1];
+      const u32x4* u = (const u32x4*)(ap[c] + (long)s * kStepK);
+      f.a[c][0] = u[0];
+      f.a[c][1] = u[1];
     }
+  };
+  const auto multiply = [&](const Step& f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int c = 0; c < TR; ++c)
-#pragma unroll
-        for (int m = 0; m < TM; ++m) acc[c][m] = mfma(af[c][h], xf[m][h], acc[c][m]);
+      for (int c = 0; c < TR; ++c) acc[c] = mfma(f.a[c][h], f.x[h], acc[c]);
+  };
+  // Loads are issued unconditionally (past the end the last step again): behind a
+  // branch the compiler could not count them and would wait for the step ahead too.
+  Step f[2];
+  if (s0 < s1) {
+    const int last = s1 - 1;
+    load(f[0], s0);
+    for (int s = s0; s < s1; s += 2) {
+      load(f[1], s + 1 < last ? s + 1 : last);
+      multiply(f[0]);
+      if (s + 1 < s1) {
+        load(f[0], s + 2 < last ? s + 2 : last);
+        multiply(f[1]);
+      }
+    }
   }
-  // lane holds ranks 16 c + 4 q + v of row 16 m + lrow
+  // lane holds ranks 16 c + 4 q + v of row lrow
 #pragma unroll
-  for (int c = 0; c < TR; ++c)
-#pragma unroll
-    for (int m = 0; m < TM; ++m) *(f32x4v*)&red[wave][16 * m + lrow][16 * c + 4 * q] = acc[c][m];
+  for (int c = 0; c < TR; ++c) *(f32x4v*)&red[wave][lrow][16 * c + 4 * q] = acc[c];
   __syncthreads();
   for (int i = tid; i < RT * RC / 4; i += kThreads) {
     const int row = i / (RC / 4), col = 4 * (i - row * (RC / 4));
@@ -131,111 +143,359 @@ __global__ __launch_bounds__(kThreads) void adapter_shrink(AdapterArgs p) {
   }
 }
 
-template <int TM, int TR>
-__global__ __launch_bounds__(kThreads) void adapter_expand(AdapterArgs p) {
-  constexpr int RT = 16 * TM, RC = 16 * TR;
-  constexpr int KF = TR == 1 ? 1 : TR / 2;        // 32-deep fragments of the rank
-  constexpr int HP = (TR == 1 ? 32 : RC) + 8;     // bf16 of one LDS row (+16 bytes against bank conflicts)
-  constexpr int HL = TR == 1 ? 1 : 2;             // hi (and lo) planes
-  __shared__ __attribute__((aligned(16))) uint16_t hs[HL][RT][HP];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lrow = lane & 15, q = lane >> 4;
-  const int n_lo = blockIdx.y * p.strip, n_hi = n_lo + p.strip < p.N ? n_lo + p.strip : p.N;
-  if ((int)blockIdx.x >= p.tiles) {
-    // tokens without an adapter pass through (launched only where out is not D)
-    const int t0 = ((int)blockIdx.x - p.tiles) * 16;
-    for (int t = t0; t < t0 + 16 && t < p.T; ++t) {
-      if ((unsigned)p.rows[t] < (unsigned)p.cap) continue;
-      for (int n = n_lo + 8 * tid; n < n_hi; n += 8 * kThreads)
-        *(u32x4*)(p.out + (long)t * p.N + n) = *(const u32x4*)(p.D + (long)t * p.N + n);
-    }
-    return;
-  }
+// 16 bytes per lane from global memory straight into LDS at lds_at + 16 * lane
+// (no register in between; counted by vmcnt like any load).
+__device__ __forceinline__ void dma16(const void* src, uint32_t lds_at) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :: "v"(src), "s"(lds_at) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// shrink for 64-row tiles: wave w owns rows 16 w .. 16 w + 15 over the whole part
+// of K, so nothing is summed across waves and A, used by all four, is worth
+// staging. A ring of kStages LDS stages of 64 k (x rows and A rows, one 128-byte
+// line each) is filled by direct global-to-LDS loads kStages - 1 steps ahead. One
+// barrier per step both publishes a stage and frees the one before it. A row's
+// 16-byte chunk c sits at position c ^ (row & 7), which spreads the 16 rows that a
+// quarter wave reads over the banks.
+constexpr int kStages = 3;
+
+template <int TR>
+__global__ __launch_bounds__(kThreads) void adapter_shrink64(AdapterArgs p) {
+  constexpr int RT = 64, RC = 16 * TR;
+  constexpr int AI = TR > 2 ? TR / 2 : 1;           // A loads per wave and stage
+  constexpr int kStageBytes = RT * 128 + RC * 128;
+  __shared__ __attribute__((aligned(128))) uint8_t ring[kStages * kStageBytes];
   const int r0 = blockIdx.x * RT;
   const int a = p.m_indices[r0];
-  if ((unsigned)a >= (unsigned)p.L) return;
-  const float scale = p.scales[a];
-  for (int i = tid; i < RT * RC / 4; i += kThreads) {
-    const int row = i / (RC / 4), col = 4 * (i - row * (RC / 4));
-    f32x4v h = {0.f, 0.f, 0.f, 0.f};
-    if ((unsigned)p.slots[r0 + row] < (unsigned)p.T && col < p.R) {
-      for (int c = 0; c < p.parts; ++c) h += *(const f32x4v*)(p.ws + ((long)c * p.cap + r0 + row) * RC + col);
-      h *= scale;
-    }
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      hi[e] = bf16_pair(h[2 * e], h[2 * e + 1]);
-      lo[e] = bf16_pair(h[2 * e] - bf16_lo(hi[e]), h[2 * e + 1] - bf16_hi(hi[e]));
-    }
-    *(u32x2v*)&hs[0][row][col] = u32x2v{hi[0], hi[1]};
-    if (TR == 1) *(u32x2v*)&hs[0][row][16 + col] = u32x2v{lo[0], lo[1]};
-    else *(u32x2v*)&hs[HL - 1][row][col] = u32x2v{lo[0], lo[1]};
-  }
-  __syncthreads();
-  u32x4 hf[HL][KF][TM];
-#pragma unroll
-  for (int e = 0; e < HL; ++e)
-#pragma unroll
-    for (int f = 0; f < KF; ++f)
-#pragma unroll
-      for (int m = 0; m < TM; ++m) hf[e][f][m] = *(const u32x4*)&hs[e][16 * m + lrow][32 * f + 8 * q];
-  int tok[TM];
-#pragma unroll
-  for (int m = 0; m < TM; ++m) tok[m] = p.slots[r0 + 16 * m + lrow];
+  if ((unsigned)a >= (unsigned)p.L) return;   // no token in this tile (uniform)
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lrow = lane & 15, q = lane >> 4;
+  const int steps = p.K / kStepK;
+  const int part = blockIdx.y, s0 = steps * part / p.parts, s1 = steps * (part + 1) / p.parts;
 
-  // Columns in pairs of 16-wide sub-tiles: sub-tile e's operand row i is column
-  // 8 (i / 4) + 4 e + i % 4, so a lane's results of the pair are the eight
-  // consecutive columns 8 q .. 8 q + 7 and D moves in 16-byte pieces.
+  // a load instruction covers eight rows; its lanes fetch their row's chunks in swizzled order
+  const int first = p.slots[r0];
+  const int chunk = 8 * ((lane & 7) ^ (lane >> 3));   // in elements
+  const uint16_t *xp[2], *ap[AI];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = p.slots[r0 + 16 * wave + 8 * i + (lane >> 3)];
+    // rows without a token repeat the tile's first one; their sums are not stored
+    const int tok = (unsigned)s < (unsigned)p.T ? s : (unsigned)first < (unsigned)p.T ? first : 0;
+    xp[i] = p.x + (long)tok * p.K + (long)s0 * kStepK + chunk;
+  }
+  int arow[AI];
+#pragma unroll
+  for (int i = 0; i < AI; ++i) {
+    arow[i] = 8 * ((wave * AI + i) % (2 * TR));       // waves without a share repeat another's load
+    const int r = arow[i] + (lane >> 3) < p.R ? arow[i] + (lane >> 3) : p.R - 1;
+    ap[i] = p.A + ((long)a * p.R + r) * p.K + (long)s0 * kStepK + chunk;
+  }
+  const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)ring;
+  // Issues the loads of one step into a stage; past the end the last step again, so that every
+  // wave always has the same number of loads under way.
+  int to_go = s1 - s0 - 1;
+  const auto issue = [&](int stage) {
+    const uint32_t at = lds0 + stage * kStageBytes;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) dma16(xp[i], at + (16 * wave + 8 * i) * 128);
+#pragma unroll
+    for (int i = 0; i < AI; ++i) dma16(ap[i], __builtin_amdgcn_readfirstlane(at + (RT + arow[i]) * 128));
+    const int adv = to_go > 0 ? kStepK : 0;
+    --to_go;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) xp[i] += adv;
+#pragma unroll
+    for (int i = 0; i < AI; ++i) ap[i] += adv;
+  };
+  f32x4v acc[TR];
+#pragma unroll
+  for (int c = 0; c < TR; ++c) acc[c] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  if (s0 < s1) {   // uniform over the workgroup
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    int stage = 0;
+    for (int s = s0; s < s1; ++s) {
+      // this stage's loads are the oldest; the later stages' stay under way
+      wait_vm<(kStages - 2) * (2 + AI)>();
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the last step's LDS reads are done
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      issue(stage == 0 ? kStages - 1 : stage - 1);
+      const uint8_t* st = ring + stage * kStageBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = ((4 * h + q) ^ (lrow & 7)) << 4;
+        const u32x4 xf = *(const u32x4*)(st + (16 * wave + lrow) * 128 + at);
+#pragma unroll
+        for (int c = 0; c < TR; ++c)
+          acc[c] = mfma(*(const u32x4*)(st + (RT + 16 * c + lrow) * 128 + at), xf, acc[c]);
+      }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    wait_vm<0>();   // nothing may land in LDS after the workgroup has ended
+  }
+  const int row = r0 + 16 * wave + lrow;
+  if ((unsigned)p.slots[row] >= (unsigned)p.T) return;
+  float* out = p.ws + ((long)blockIdx.y * p.cap + row) * RC + 4 * q;
+#pragma unroll
+  for (int c = 0; c < TR; ++c) *(f32x4v*)(out + 16 * c) = acc[c];
+}
+
+// A lane's fragments of h: row `row` of the tile, its parts summed, scaled and
+// split into hi and lo. TR == 1: one fragment, hi in the lanes of k 0 .. 15, lo in
+// the others.
+template <int TR>
+struct HFrags {
+  static constexpr int KF = TR == 1 ? 1 : TR / 2;   // 32-deep fragments of the rank
+  static constexpr int HL = TR == 1 ? 1 : 2;        // hi (and lo)
+  u32x4 f[HL][KF];
+};
+template <int TR>
+__device__ __forceinline__ void load_h(const AdapterArgs& p, int row, bool real, float scale, int q, HFrags<TR>& h) {
+  constexpr int RC = 16 * TR;
+#pragma unroll
+  for (int k = 0; k < HFrags<TR>::KF; ++k) {
+    const int r = TR == 1 ? 8 * (q & 1) : 32 * k + 8 * q;
+    f32x4v v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const float* src = p.ws + (long)row * RC + r;   // inside the workspace whether or not it was written
+#pragma unroll 4
+    for (int c = 0; c < p.parts; ++c) {
+      v[0] += *(const f32x4v*)src;
+      v[1] += *(const f32x4v*)(src + 4);
+      src += (long)p.cap * RC;
+    }
+    if (!real || r >= p.R) v[0] = v[1] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    u32x4 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = v[e >> 1][2 * (e & 1)] * scale, y = v[e >> 1][2 * (e & 1) + 1] * scale;
+      hi[e] = bf16_pair(x, y);
+      lo[e] = bf16_pair(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
+    }
+    if (TR == 1) {
+      h.f[0][0] = q < 2 ? hi : lo;
+    } else {
+      h.f[0][k] = hi;
+      h.f[HFrags<TR>::HL - 1][k] = lo;
+    }
+  }
+}
+
+// Tokens without an adapter pass through: workgroup `block` of the launch's first
+// p.copies takes 16 tokens, each wave four, all its loads under way before the
+// first store.
+__device__ __forceinline__ void copy_tokens(const AdapterArgs& p, int block) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long t0 = ((long)block * kWaves + wave) * 4;
+  long tok[4];
+  bool pass[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {   // past the last token: the last one, not stored
+    tok[i] = t0 + i < p.T ? t0 + i : p.T - 1;
+    pass[i] = (unsigned)p.rows[tok[i]] >= (unsigned)p.cap && t0 + i < p.T;
+  }
+  if (!(pass[0] || pass[1] || pass[2] || pass[3])) return;
+  for (int n = 8 * lane; n < p.N; n += 8 * 64) {
+    u32x4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *(const u32x4*)(p.D + tok[i] * p.N + n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (pass[i]) *(u32x4*)(p.out + tok[i] * p.N + n) = v[i];
+  }
+}
+
+// Columns go in pairs of 16-wide sub-tiles: sub-tile e's operand row i is column
+// 8 (i / 4) + 4 e + i % 4 of the pair's 32, so a lane's results of the pair are the
+// eight consecutive columns 8 q .. 8 q + 7 and D moves in 16-byte pieces.
+__device__ __forceinline__ int pair_row(int i, int e) { return 8 * (i >> 2) + 4 * e + (i & 3); }
+
+// out = D + the pair's products, for one lane's eight columns.
+__device__ __forceinline__ u32x4 add_pair(u32x4 d, const f32x4v* acc) {
+  float v[8];
+  RowBf16::unpack(d, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] += acc[e >> 2][e & 3];
+  return RowBf16::pack(v);
+}
+
+// Expand for 16-row tiles: each wave has its own columns, 32 at a time, and B's
+// fragments come straight from global memory (B is read once).
+template <int TR>
+__global__ __launch_bounds__(kThreads) void adapter_expand16(AdapterArgs p) {
+  using H = HFrags<TR>;
+  if ((int)blockIdx.x < p.copies) return copy_tokens(p, blockIdx.x);
+  const int job = blockIdx.x - p.copies, strip = job / p.tiles, r0 = (job - strip * p.tiles) * 16;
+  const int a = p.m_indices[r0];
+  if ((unsigned)a >= (unsigned)p.L) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lrow = lane & 15, q = lane >> 4;
+  const int n_lo = strip * p.strip, n_hi = n_lo + p.strip < p.N ? n_lo + p.strip : p.N;
+  const int tok = p.slots[r0 + lrow];
+  const bool real = (unsigned)tok < (unsigned)p.T;
+  const int first = p.slots[r0];
+  const uint16_t* drow = p.D + (long)(real ? tok : (unsigned)first < (unsigned)p.T ? first : 0) * p.N;
+  H h;
+  load_h<TR>(p, r0 + lrow, real, p.scales[a], q, h);
   const uint16_t* Ba = p.B + (long)a * p.N * p.R;
-  const int brow = 8 * (lrow >> 2) + (lrow & 3);
   for (int n0 = n_lo + 32 * wave; n0 < n_hi; n0 += 32 * kWaves) {
-    u32x4 bf[2][KF];
+    u32x4 bf[2][H::KF];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int f = 0; f < KF; ++f) {
-        const int n = n0 + brow + 4 * e;
+      for (int f = 0; f < H::KF; ++f) {
+        const int n = n0 + pair_row(lrow, e);
         const int r = TR == 1 ? 8 * (q & 1) : 32 * f + 8 * q;
-        bf[e][f] = n < p.N && r < p.R ? *(const u32x4*)(Ba + (long)n * p.R + r) : u32x4{0u, 0u, 0u, 0u};
+        // loads are not predicated: outside B and D any valid piece is read and dropped
+        bf[e][f] = *(const u32x4*)(Ba + (long)(n < n_hi ? n : n_hi - 1) * p.R + (r < p.R ? r : 0));
+        if (r >= p.R) bf[e][f] = u32x4{0u, 0u, 0u, 0u};
       }
     const int col = n0 + 8 * q;
-    u32x4 d[TM];
+    const bool ok = real && col < n_hi;
+    const u32x4 d = *(const u32x4*)(drow + (col < n_hi ? col : n_lo));
+    f32x4v acc[2] = {};
 #pragma unroll
-    for (int m = 0; m < TM; ++m) {
-      const bool ok = (unsigned)tok[m] < (unsigned)p.T && col < p.N;
-      d[m] = ok ? *(const u32x4*)(p.D + (long)tok[m] * p.N + col) : u32x4{0u, 0u, 0u, 0u};
-    }
+    for (int l = H::HL - 1; l >= 0; --l)   // the small halves first
 #pragma unroll
-    for (int m = 0; m < TM; ++m) {
-      f32x4v acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      for (int f = 0; f < H::KF; ++f)
 #pragma unroll
-      for (int h = HL - 1; h >= 0; --h)   // the small halves first
-#pragma unroll
-        for (int f = 0; f < KF; ++f)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) acc[e] = mfma(bf[e][f], hf[h][f][m], acc[e]);
-      float v[8];
-      RowBf16::unpack(d[m], v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += acc[e >> 2][e & 3];
-      if ((unsigned)tok[m] < (unsigned)p.T && col < p.N)
-        *(u32x4*)(p.out + (long)tok[m] * p.N + col) = RowBf16::pack(v);
-    }
+        for (int e = 0; e < 2; ++e) acc[e] = mfma(bf[e][f], h.f[l][f], acc[e]);
+    if (ok) *(u32x4*)(p.out + (long)tok * p.N + col) = add_pair(d, acc);
   }
+}
+
+// Expand for 64-row tiles: wave w owns rows 16 w .. 16 w + 15, and B, used by all
+// four waves, goes through LDS: 128 columns at a time, which are one contiguous
+// piece of global memory, loaded straight into one of two LDS buffers while the
+// other is in use. With B fetched by each wave on its own (half-line pieces of 16
+// rows per instruction) its loads took 22 us of 55 at T = 8192, N = 4096, R = 64.
+// A row's 16-byte chunk c sits at c ^ key(n) where the chunks per row are a power of
+// two, key(n) spreading the rows that eight neighbouring lanes read over the banks.
+constexpr int kCols = 128;
+
+__device__ __forceinline__ int swizzle_key(int n, int chunks) {
+  return (chunks & (chunks - 1)) ? 0 : ((n & 3) | ((n >> 1) & 4)) & (chunks - 1);
+}
+
+template <int TR>
+__global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
+  using H = HFrags<TR>;
+  constexpr int NI = TR;                       // loads per wave and buffer: 128 columns x 2 TR chunks / 256
+  __shared__ __attribute__((aligned(128))) uint8_t ring[2][NI * kThreads * 16];
+  if ((int)blockIdx.x < p.copies) return copy_tokens(p, blockIdx.x);
+  const int job = blockIdx.x - p.copies, strip = job / p.tiles, r0 = (job - strip * p.tiles) * 64;
+  const int a = p.m_indices[r0];
+  if ((unsigned)a >= (unsigned)p.L) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lrow = lane & 15, q = lane >> 4;
+  const int n_lo = strip * p.strip, n_hi = n_lo + p.strip < p.N ? n_lo + p.strip : p.N;
+  const int chunks = p.R >> 3;                 // 16-byte chunks of a row of B
+  const uint16_t* Ba = p.B + (long)a * p.N * p.R;
+  const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)&ring[0][0];
+  // this lane's LDS chunks hold row bn of the buffer's 128, chunk bc of it
+  int bn[NI], bc[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int g = (i * kWaves + wave) * 64 + lane;
+    bn[i] = g / chunks;
+    bc[i] = (g - bn[i] * chunks) ^ swizzle_key(bn[i], chunks);
+  }
+  const auto issue = [&](int buffer, int n0) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      // rows past the buffer's 128 (R below 16 TR) or past N repeat a valid one; nothing reads them
+      const int n = n0 + (bn[i] < kCols ? bn[i] : kCols - 1);
+      dma16(Ba + (long)(n < p.N ? n : p.N - 1) * p.R + 8 * bc[i],
+            lds0 + buffer * (NI * kThreads * 16) + (i * kWaves + wave) * 1024);
+    }
+  };
+  issue(0, n_lo);
+  const int tok = p.slots[r0 + 16 * wave + lrow];
+  const bool real = (unsigned)tok < (unsigned)p.T;
+  const uint16_t* drow = p.D + (long)(real ? tok : 0) * p.N;
+  uint16_t* orow = p.out + (long)(real ? tok : 0) * p.N;
+  uint16_t* spare = p.spare + 8 * lane;
+  H h;
+  load_h<TR>(p, r0 + 16 * wave + lrow, real, p.scales[a], q, h);
+  constexpr int NG = kCols / 32;
+  int cc[H::KF];   // this lane's chunk of a row of B in each fragment
+#pragma unroll
+  for (int f = 0; f < H::KF; ++f) {
+    const int c = TR == 1 ? q & 1 : 4 * f + q;
+    cc[f] = c < chunks ? c : 0;
+  }
+  u32x4 d[2][NG];
+  const auto load_d = [&](u32x4* v, int n0) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int col = n0 + 32 * g + 8 * q;
+      v[g] = *(const u32x4*)(drow + (col < n_hi ? col : n_lo));
+    }
+  };
+  load_d(d[0], n_lo);
+  // Loads and stores count down in order, so a wait for a load also waits for every
+  // store before it. Each round therefore issues the next round's loads before its
+  // own NG stores and leaves just those under way when it waits; for the count to be
+  // exact no store is skipped: lanes without an output write to spare memory.
+  wait_vm<0>();
+  const auto round = [&](auto odd, int n0) {
+    constexpr int B = decltype(odd)::value;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the other buffer's reads are done
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const int next = n0 + kCols < n_hi ? n0 + kCols : n_lo;   // the last round loads its first columns again
+    issue(B ^ 1, next);
+    load_d(d[B ^ 1], next);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      f32x4v acc[2] = {};
+#pragma unroll
+      for (int f = 0; f < H::KF; ++f) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int n = 32 * g + pair_row(lrow, e);
+          // ranks past R: any chunk, dropped (a predicated read would be a branch and a wait of its own)
+          u32x4 b = *(const u32x4*)(ring[B] + ((n * chunks + (cc[f] ^ swizzle_key(n, chunks))) << 4));
+          if (cc[f] != (TR == 1 ? q & 1 : 4 * f + q)) b = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int l = H::HL - 1; l >= 0; --l) acc[e] = mfma(b, h.f[l][f], acc[e]);
+        }
+      }
+      const int col = n0 + 32 * g + 8 * q;
+      *(u32x4*)(real && col < n_hi ? orow + col : spare) = add_pair(d[B][g], acc);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm<NG>();
+  };
+  for (int n0 = n_lo; n0 < n_hi; n0 += 2 * kCols) {
+    round(std::integral_constant<int, 0>{}, n0);
+    if (n0 + kCols < n_hi) round(std::integral_constant<int, 1>{}, n0 + kCols);
+  }
+  wait_vm<0>();   // nothing may land in LDS after the workgroup has ended
 }
 
 // 16-column groups of the rank as compiled: 1, 2, 4 or 8.
 int rank_groups(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
-// Rows of one tile: 64 where the plan's segments allow it, else 32 or 16.
-int tile_rows(int align) { return align % 64 == 0 ? 64 : align % 32 == 0 ? 32 : 16; }
+// Rows of one tile: 64 where the plan's segments allow it, else 16.
+int tile_rows(int align) { return align % 64 == 0 ? 64 : 16; }
 
 // Parts of K: enough workgroups to fill the chip, at least one step of K a wave.
-int k_parts(int tiles, int K) {
+// Every part is one more partial h for each expand workgroup to read: with 16-row
+// tiles, 64 tokens of 64 adapters (K 7168, N 4096, R 16), 2 / 4 / 8 parts take 8.6 /
+// 5.8 / 5.6 us in shrink and 5.6 / 6.2 / 8.3 us in expand, so those stop at 256
+// workgroups. With 64-row tiles (T 8192, L 8, R 64) 2, 4 and 8 parts take 27.9, 27.4
+// and 34 us in shrink.
+int k_parts(int tiles, int rt, int K) {
   const int most = K / (kStepK * kWaves) > 1 ? K / (kStepK * kWaves) : 1;
+  const long fill = rt == 64 ? 512 : 256;
   int parts = 1;
-  while (parts < 8 && 2 * parts <= most && (long)tiles * parts < 512) parts *= 2;
+  while (parts < 16 && 2 * parts <= most && (long)tiles * parts < fill) parts *= 2;
   return parts;
 }
 
@@ -246,24 +506,15 @@ int sizes(int R, int K, int cap, int align) {
   return FG_OK;
 }
 
-template <int TM, int TR>
-void launch(const AdapterArgs& p, hipStream_t s) {
-  hipLaunchKernelGGL((adapter_shrink<TM, TR>), dim3(p.tiles, p.parts), dim3(kThreads), 0, s, p);
-}
-template <int TM, int TR>
-void launch_expand(const AdapterArgs& p, hipStream_t s) {
-  const unsigned copies = p.out != p.D ? (unsigned)((p.T + 15L) / 16) : 0u;
-  hipLaunchKernelGGL((adapter_expand<TM, TR>), dim3(p.tiles + copies, (p.N + p.strip - 1) / p.strip), dim3(kThreads), 0,
-                     s, p);
-}
-
-template <int TM>
-void launch_rank(const AdapterArgs& p, int tr, bool expand, hipStream_t s) {
-  switch (tr) {
-    case 1: expand ? launch_expand<TM, 1>(p, s) : launch<TM, 1>(p, s); break;
-    case 2: expand ? launch_expand<TM, 2>(p, s) : launch<TM, 2>(p, s); break;
-    case 4: expand ? launch_expand<TM, 4>(p, s) : launch<TM, 4>(p, s); break;
-    default: expand ? launch_expand<TM, 8>(p, s) : launch<TM, 8>(p, s); break;
+template <int TR>
+void launch(const AdapterArgs& p, bool wide, hipStream_t s) {
+  const dim3 g1(p.tiles, p.parts), g2(p.copies + p.tiles * ((p.N + p.strip - 1) / p.strip)), b(kThreads);
+  if (wide) {
+    hipLaunchKernelGGL(adapter_shrink64<TR>, g1, b, 0, s, p);
+    hipLaunchKernelGGL(adapter_expand64<TR>, g2, b, 0, s, p);
+  } else {
+    hipLaunchKernelGGL(adapter_shrink16<TR>, g1, b, 0, s, p);
+    hipLaunchKernelGGL(adapter_expand16<TR>, g2, b, 0, s, p);
   }
 }
 
@@ -273,7 +524,7 @@ extern "C" {
 
 int fg_adapters_workspace(int R, int K, int cap, int align, size_t* bytes) {
   if (!bytes || sizes(R, K, cap, align) != FG_OK) return FG_EINVAL;
-  *bytes = (size_t)k_parts(cap / tile_rows(align), K) * cap * (16 * rank_groups(R)) * sizeof(float);
+  *bytes = kSpareBytes + (size_t)k_parts(cap / tile_rows(align), tile_rows(align), K) * cap * (16 * rank_groups(R)) * sizeof(float);
   return FG_OK;
 }
 
@@ -299,25 +550,31 @@ int fg_adapters(const void* D, const void* x, const void* A, const void* B, cons
   p.slots = slots;
   p.m_indices = m_indices;
   p.out = static_cast<uint16_t*>(out);
-  p.ws = static_cast<float*>(ws);
+  p.spare = static_cast<uint16_t*>(ws);
+  p.ws = static_cast<float*>(ws) + kSpareBytes / sizeof(float);
   p.T = T;
   p.L = L;
   p.R = R;
   p.K = K;
   p.N = N;
   p.cap = cap;
-  const int rt = tile_rows(align), tr = rank_groups(R);
+  const int rt = tile_rows(align);
   p.tiles = cap / rt;
-  p.parts = k_parts(p.tiles, K);
-  // columns of an expand workgroup: long strips read h once for more of D, short ones fill the chip
+  p.parts = k_parts(p.tiles, rt, K);
+  p.copies = out != D ? (int)((T + 15L) / 16) : 0;
+  // columns of an expand workgroup: long strips load h less often, short ones fill the
+  // chip (64-row tiles, T 8192, N 4096: 256 / 512 / 1024 / 2048 / 4096 columns take 47 /
+  // 40 / 38-45 / 39 / 56 us)
   p.strip = 1024;
-  while (p.strip > 128 && (long)p.tiles * ((N + p.strip - 1) / p.strip) < 512) p.strip /= 2;
-  for (int e = 0; e < 2; ++e) {
-    if (rt == 64) launch_rank<4>(p, tr, e, stream);
-    else if (rt == 32) launch_rank<2>(p, tr, e, stream);
-    else launch_rank<1>(p, tr, e, stream);
-    if (hipGetLastError() != hipSuccess) return FG_ELAUNCH;
+  while (p.strip > 128 && (long)p.tiles * ((N + p.strip - 1) / p.strip) < (rt == 64 ? 512 : 1024)) p.strip /= 2;
+  if ((long)p.copies + (long)p.tiles * ((N + p.strip - 1) / p.strip) > 0x7fffffffL) return FG_EINVAL;
+  switch (rank_groups(R)) {
+    case 1: launch<1>(p, rt == 64, stream); break;
+    case 2: launch<2>(p, rt == 64, stream); break;
+    case 4: launch<4>(p, rt == 64, stream); break;
+    default: launch<8>(p, rt == 64, stream); break;
   }
+  if (hipGetLastError() != hipSuccess) return FG_ELAUNCH;
   return FG_OK;
 }
 

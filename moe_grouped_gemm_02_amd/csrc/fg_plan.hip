@@ -119,10 +119,18 @@ __global__ __launch_bounds__(kThreads) void plan_place(PlanArgs p) {
     for (int i = tid; i < parts * G; i += kThreads) {
       const int g = i % G;
       int before = 0, all = 0;
-      for (int c = i / G; c < chunks; c += parts) {
-        const int n = p.hist[(long)c * G + g];
-        all += n;
-        before += c < (int)blockIdx.x ? n : 0;
+      for (int c0 = i / G; c0 < chunks; c0 += 8 * parts) {
+        int n[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int c = c0 + u * parts;
+          n[u] = c < chunks ? p.hist[(long)c * G + g] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          all += n[u];
+          before += c0 + u * parts < (int)blockIdx.x ? n[u] : 0;
+        }
       }
       atomicAdd(&total[g], all);
       atomicAdd(&base[g], before);
@@ -223,7 +231,9 @@ int plan(PlanArgs p, void* ws, hipStream_t stream) {
     hipLaunchKernelGGL((plan_place<kChunk / kThreads>), dim3(chunks), dim3(kThreads), lds, stream, p);
   } else {
     p.hist = nullptr;
-    hipLaunchKernelGGL((plan_place<kOneBlock / kThreads>), dim3(1), dim3(kThreads), lds, stream, p);
+    if (p.S <= kThreads) hipLaunchKernelGGL((plan_place<1>), dim3(1), dim3(kThreads), lds, stream, p);
+    else if (p.S <= 4 * kThreads) hipLaunchKernelGGL((plan_place<4>), dim3(1), dim3(kThreads), lds, stream, p);
+    else hipLaunchKernelGGL((plan_place<kOneBlock / kThreads>), dim3(1), dim3(kThreads), lds, stream, p);
   }
   return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
 }

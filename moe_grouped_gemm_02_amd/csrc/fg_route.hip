@@ -20,10 +20,11 @@
 //     sigmoid                  dl = g s (1 - s)
 //     sigmoid, renormalised    dl = (g - <g, p>) / (sum of the chosen s) * s (1 - s), chosen only
 //
-// One wave holds one token: lane i has experts [i * V, (i + 1) * V). Each of
-// the k rounds is a wave-wide maximum over 32-bit order keys on the DPP path,
-// a ballot that finds the lowest lane holding it, and that lane clearing its
-// lowest such key; no LDS and no barrier. All sums are fp32 in a fixed order.
+// A group of L = 64 or 16 lanes holds a token: lane i of it has experts
+// [i * V, (i + 1) * V). Each of the k rounds is a maximum over the group's 32-bit
+// order keys on the DPP path, a ballot that finds the lowest lane holding it, and
+// that lane clearing its lowest such key and noting the choice in LDS; no
+// barrier, since a group lies within one wave. All sums are fp32 in a fixed order.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -38,36 +39,79 @@ using namespace fg;
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
-constexpr int kWaves = 4;   // tokens per workgroup
+constexpr int kThreads = 256;
+constexpr int kPackTokens = 2048;   // from here on four tokens share a wave
 
-// Lane's V logits of one row (NaN and everything past E as -inf).
+// V consecutive elements of a row move in pieces of up to 16 bytes where V
+// divides E (a lane then has V experts or none, and pieces are aligned).
 template <class R, int V>
-__device__ __forceinline__ void load_logits(const void* logits, long row, int E, int lane, float* l) {
+struct Pieces {
+  static constexpr int kBytes = V * R::kBytes < 16 ? V * R::kBytes : 16;
+  static constexpr int kEach = kBytes / R::kBytes, kCount = V / kEach;
+  struct alignas(kBytes) Piece {
+    uint8_t b[kBytes];
+  };
+};
+
+// V consecutive logits from expert e0 of a row; experts past E and NaN as -inf.
+template <class R, int V>
+__device__ __forceinline__ void load_logits(const void* logits, long row, int E, int e0, float* l) {
+  using P = Pieces<R, V>;
+  if (E % V == 0) {
+    const int at = e0 < E ? e0 : E - V;
+    const auto* src = (const typename P::Piece*)((const char*)logits + (row * E + at) * R::kBytes);
+    typename P::Piece raw[P::kCount];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    float v = -INFINITY;
-    if (e < E) v = R::load1(logits, row * E + e);
-    l[i] = v > -INFINITY ? v : -INFINITY;
+    for (int c = 0; c < P::kCount; ++c) raw[c] = src[c];
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = R::load1(raw, i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      // loads are not predicated: past the row's end its last logit is read and dropped
+      const int e = e0 + i < E ? e0 + i : E - 1;
+      l[i] = R::load1(logits, row * E + e);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = e0 + i < E && l[i] > -INFINITY ? l[i] : -INFINITY;
+}
+
+template <class R, int V>
+__device__ __forceinline__ void store_row(void* out, long row, int E, int e0, const float* v) {
+  using P = Pieces<R, V>;
+  if (E % V == 0) {
+    typename P::Piece raw[P::kCount];
+#pragma unroll
+    for (int i = 0; i < V; ++i) R::store1(raw, i, v[i]);
+    auto* dst = (typename P::Piece*)((char*)out + (row * E + e0) * R::kBytes);
+    if (e0 < E) {
+#pragma unroll
+      for (int c = 0; c < P::kCount; ++c) dst[c] = raw[c];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e0 + i < E) R::store1(out, row * E + e0 + i, v[i]);
   }
 }
 
 // Scores of the lane's V logits.
-template <int V>
+template <int L, int V>
 __device__ __forceinline__ void scores(const float* l, int softmax, float* s) {
   if (softmax) {
-    uint32_t m = 0;
+    float m = l[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = umax(m, order_key(l[i]));
-    m = wave_max_u32(m);
-    const float top = __uint_as_float((m >> 31) ? (m & 0x7fffffffu) : ~m);
+    for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+    const uint32_t u = group_max_u32<L>(order_key(m));
+    const float top = __uint_as_float((u >> 31) ? (u & 0x7fffffffu) : ~u);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       s[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
       sum += s[i];
     }
-    sum = wave_sum(sum);
+    sum = group_sum<L>(sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = s[i] == 0.0f ? 0.0f : s[i] / sum;   // a row with nothing eligible has sum 0
   } else {
@@ -76,123 +120,124 @@ __device__ __forceinline__ void scores(const float* l, int softmax, float* s) {
   }
 }
 
-template <class R, int V>
-__global__ __launch_bounds__(64 * kWaves) void route_topk(const void* __restrict__ logits,
-                                                          const float* __restrict__ bias,
-                                                          int32_t* __restrict__ ids, float* __restrict__ w,
-                                                          int T, int E, int k, int softmax, int renorm,
-                                                          float scale) {
-  const long t = (long)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (t >= T) return;
-  const int lane = threadIdx.x & 63;
-  float l[V], s[V];
+template <class R, int L, int V>
+__global__ __launch_bounds__(kThreads) void route_topk(const void* __restrict__ logits,
+                                                       const float* __restrict__ bias, int32_t* __restrict__ ids,
+                                                       float* __restrict__ w, int T, int E, int k, int softmax,
+                                                       int renorm, float scale) {
+  __shared__ int32_t best_id[kThreads / L][kMaxTopK];
+  __shared__ float best_s[kThreads / L][kMaxTopK];
+  const int group = threadIdx.x / L, lane = threadIdx.x % L;
+  const long t = (long)blockIdx.x * (kThreads / L) + group;
+  const long row = t < T ? t : T - 1L;   // groups past the last token repeat it and store nothing
+  float l[V], s[V], b[V];
   uint32_t key[V];
-  load_logits<R, V>(logits, t, E, lane, l);
-  scores<V>(l, softmax, s);
+  load_logits<R, V>(logits, row, E, lane * V, l);
+  if (bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = bias[lane * V + i < E ? lane * V + i : E - 1];
+  }
+  scores<L, V>(l, softmax, s);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    float rank = l[i];
-    if (bias && e < E && l[i] > -INFINITY) rank = s[i] + bias[e];
+    const float rank = bias && l[i] > -INFINITY ? s[i] + b[i] : l[i];
     key[i] = rank > -INFINITY ? order_key(rank) : 0u;
   }
-  int id = -1;        // lane j ends with the j-th choice
-  float chosen = 0.0f;
+  for (int j = lane; j < k; j += L) {
+    best_id[group][j] = -1;
+    best_s[group][j] = 0.0f;
+  }
+  float sum = 0.0f;   // of this lane's chosen scores
   for (int j = 0; j < k; ++j) {
-    uint32_t m = 0;
+    uint32_t m = key[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = umax(m, key[i]);
-    const uint32_t best = wave_max_u32(m);
-    if (best == 0u) break;   // nothing eligible is left
-    const int lead = __builtin_ctzll(__ballot(m == best));
-    int at = 0;
-    float sc = 0.0f;
-    bool open = lane == lead;
+    for (int i = 1; i < V; ++i) m = umax(m, key[i]);
+    const uint32_t best = group_max_u32<L>(m);
+    // the group's lowest lane with the best key; its lowest expert among equals
+    unsigned long long same = __ballot(m == best);
+    if (L == 16) same = (same >> (threadIdx.x & 48)) & 0xffffu;
+    if (__builtin_ctzll(same | (1ull << 63)) == lane && best != 0u) {
+      int at = 0;
+      float sc = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (open && key[i] == best) {
-        key[i] = 0u;
-        at = i;
-        sc = s[i];
-        open = false;
+      for (int i = V - 1; i >= 0; --i) {
+        at = key[i] == best ? i : at;
+        sc = key[i] == best ? s[i] : sc;
       }
-    }
-    const int e = lead * V + __builtin_amdgcn_readlane(at, lead);
-    const float se = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(sc), lead));
-    if (lane == j) {
-      id = e;
-      chosen = se;
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = i == at ? 0u : key[i];
+      best_id[group][j] = lane * V + at;
+      best_s[group][j] = sc;
+      sum += sc;
     }
   }
-  if (renorm) {
-    const float sum = wave_sum(chosen);
-    chosen = sum > 0.0f ? chosen / sum : 0.0f;
-  }
-  if (lane < k) {
-    ids[t * k + lane] = id;
-    w[t * k + lane] = chosen * scale;
+  if (renorm) sum = group_sum<L>(sum);
+  if (t >= T) return;
+  // the group's own LDS writes, in order within its wave
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  for (int j = lane; j < k; j += L) {
+    const float c = best_s[group][j];
+    ids[t * k + j] = best_id[group][j];
+    w[t * k + j] = (renorm ? (sum > 0.0f ? c / sum : 0.0f) : c) * scale;
   }
 }
 
-template <class R, int V>
-__global__ __launch_bounds__(64 * kWaves) void route_topk_grad(const void* __restrict__ logits,
-                                                               const int32_t* __restrict__ ids,
-                                                               const float* __restrict__ dw,
-                                                               void* __restrict__ dlogits, int T, int E, int k,
-                                                               int softmax, int renorm, float scale) {
-  const long t = (long)blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (t >= T) return;
-  const int lane = threadIdx.x & 63;
+template <class R, int L, int V>
+__global__ __launch_bounds__(kThreads) void route_topk_grad(const void* __restrict__ logits,
+                                                            const int32_t* __restrict__ ids,
+                                                            const float* __restrict__ dw,
+                                                            void* __restrict__ dlogits, int T, int E, int k,
+                                                            int softmax, int renorm, float scale) {
+  const int group = threadIdx.x / L, lane = threadIdx.x % L;
+  const long t = (long)blockIdx.x * (kThreads / L) + group;
+  const long row = t < T ? t : T - 1L;
   float l[V], s[V], g[V];
   bool hit[V];
-  load_logits<R, V>(logits, t, E, lane, l);
-  scores<V>(l, softmax, s);
-  const int my_id = lane < k ? ids[t * k + lane] : -1;
-  const float my_g = lane < k ? dw[t * k + lane] * scale : 0.0f;
+  load_logits<R, V>(logits, row, E, lane * V, l);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     g[i] = 0.0f;
     hit[i] = false;
   }
+#pragma unroll 8
   for (int j = 0; j < k; ++j) {
-    const int e = __builtin_amdgcn_readlane(my_id, j);
-    const float ge = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_g), j));
+    const int at = ids[row * k + j] - lane * V;
+    const float ge = dw[row * k + j] * scale;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (e == lane * V + i) {
-        g[i] += ge;
-        hit[i] = true;
-      }
+      g[i] += at == i ? ge : 0.0f;
+      hit[i] = hit[i] || at == i;
     }
   }
+  scores<L, V>(l, softmax, s);
   float total = 1.0f;
   if (renorm) {   // shares p of the chosen scores; g - <g, p>
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) c += hit[i] ? s[i] : 0.0f;
-    total = wave_sum(c);
+    total = group_sum<L>(c);
     float d = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) d += hit[i] && total > 0.0f ? g[i] * (s[i] / total) : 0.0f;
-    d = wave_sum(d);
+    d = group_sum<L>(d);
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] = hit[i] ? g[i] - d : 0.0f;
   } else if (softmax) {
     float d = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) d += g[i] * s[i];
-    d = wave_sum(d);
+    d = group_sum<L>(d);
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] -= d;
   }
+  if (t >= T) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
     float out = 0.0f;
     if (total > 0.0f) out = g[i] * (renorm ? s[i] / total : s[i]);
-    if (!softmax) out *= 1.0f - s[i];
-    if (e < E) R::store1(dlogits, t * E + e, out);
+    g[i] = softmax ? out : out * (1.0f - s[i]);
   }
+  store_row<R, V>(dlogits, t, E, lane * V, g);
 }
 
 int check(const void* logits, int dtype, int T, int E, int k, int score) {
@@ -200,26 +245,34 @@ int check(const void* logits, int dtype, int T, int E, int k, int score) {
   if ((dtype != FG_BF16 && dtype != FG_FP32) || (score != FG_SCORE_SOFTMAX && score != FG_SCORE_SIGMOID))
     return FG_EINVAL;
   if (T == 0) return FG_OK;
-  if (!logits || !aligned(logits, dtype == FG_BF16 ? 2 : 4)) return FG_EINVAL;
+  if (!logits || !aligned(logits, 16)) return FG_EINVAL;
   return FG_OK;
 }
 
-template <class R, int V, class... Args>
+template <class R, int L, int V, class... Args>
 void launch_v(bool grad, int T, hipStream_t s, const void* logits, const void* b, void* ids, void* w, Args... a) {
-  const dim3 grid((unsigned)((T + kWaves - 1L) / kWaves)), block(64 * kWaves);
+  const dim3 grid((unsigned)((T + kThreads / L - 1L) / (kThreads / L))), block(kThreads);
   if (grad)
-    hipLaunchKernelGGL((route_topk_grad<R, V>), grid, block, 0, s, logits, (const int32_t*)b, (const float*)ids, w, T, a...);
+    hipLaunchKernelGGL((route_topk_grad<R, L, V>), grid, block, 0, s, logits, (const int32_t*)b, (const float*)ids, w, T, a...);
   else
-    hipLaunchKernelGGL((route_topk<R, V>), grid, block, 0, s, logits, (const float*)b, (int32_t*)ids, (float*)w, T, a...);
+    hipLaunchKernelGGL((route_topk<R, L, V>), grid, block, 0, s, logits, (const float*)b, (int32_t*)ids, (float*)w, T, a...);
 }
 
 template <class R, class... Args>
-void launch_e(int E, Args... a) {
-  if (E <= 64) launch_v<R, 1>(a...);
-  else if (E <= 128) launch_v<R, 2>(a...);
-  else if (E <= 256) launch_v<R, 4>(a...);
-  else if (E <= 512) launch_v<R, 8>(a...);
-  else launch_v<R, 16>(a...);
+void launch_e(int E, bool grad, int T, Args... a) {
+  if (T >= kPackTokens && E <= 256) {
+    if (E <= 16) launch_v<R, 16, 1>(grad, T, a...);
+    else if (E <= 32) launch_v<R, 16, 2>(grad, T, a...);
+    else if (E <= 64) launch_v<R, 16, 4>(grad, T, a...);
+    else if (E <= 128) launch_v<R, 16, 8>(grad, T, a...);
+    else launch_v<R, 16, 16>(grad, T, a...);
+  } else {
+    if (E <= 64) launch_v<R, 64, 1>(grad, T, a...);
+    else if (E <= 128) launch_v<R, 64, 2>(grad, T, a...);
+    else if (E <= 256) launch_v<R, 64, 4>(grad, T, a...);
+    else if (E <= 512) launch_v<R, 64, 8>(grad, T, a...);
+    else launch_v<R, 64, 16>(grad, T, a...);
+  }
 }
 
 int route(bool grad, const void* logits, int dtype, const void* b, void* ids, void* w, int T, int E, int k,
@@ -250,7 +303,7 @@ int fg_route_topk_grad(const void* logits, int dtype, const int32_t* ids, const 
                        int E, int k, int score, int renorm, float scale, hipStream_t stream) {
   const int rc = check(logits, dtype, T, E, k, score);
   if (rc != FG_OK || T == 0) return rc;
-  if (!ids || !dw || !dlogits || !aligned(ids, 4) || !aligned(dw, 4) || !aligned(dlogits, dtype == FG_BF16 ? 2 : 4))
+  if (!ids || !dw || !dlogits || !aligned(ids, 4) || !aligned(dw, 4) || !aligned(dlogits, 16))
     return FG_EINVAL;
   return route(true, logits, dtype, ids, const_cast<float*>(dw), dlogits, T, E, k, score, renorm, scale, stream);
 }

@@ -89,6 +89,8 @@ __device__ __forceinline__ bool unit_of(int per, int T, long* t, int* i) {
   return *t < T;
 }
 
+constexpr int kAtOnce = 4;   // choices whose row indices are loaded together
+
 template <class R, bool POW2, bool W>
 __global__ __launch_bounds__(kThreads) void dispatch_quant(const void* __restrict__ x,
                                                            const int32_t* __restrict__ rows,
@@ -98,25 +100,35 @@ __global__ __launch_bounds__(kThreads) void dispatch_quant(const void* __restric
   if (!unit_of(o.H >> 4, T, &t, &i)) return;   // whole groups of eight lanes leave together
   float f[16];
   load16<R>(x, t, o.H, i, f);
+  float s = 0.0f;
+  u32x4 q = {0u, 0u, 0u, 0u};
   if (!W) {
-    float s = block_scale(group8_max(amax16(f)));
+    s = block_scale(group8_max(amax16(f)));
     if (POW2) s = pow2_up(s);
-    const u32x4 q = encode16(f, s, POW2);
-    for (int j = 0; j < k; ++j) {
-      const int row = rows[t * k + j];
-      if ((unsigned)row < (unsigned)o.GM) store_unit(o, row, i, q, s);
-    }
-  } else {
-    for (int j = 0; j < k; ++j) {
-      const int row = rows[t * k + j];
-      if ((unsigned)row >= (unsigned)o.GM) continue;
-      const float wj = w[t * k + j];
-      float v[16];
+    q = encode16(f, s, POW2);
+  }
+  for (int j0 = 0; j0 < k; j0 += kAtOnce) {
+    int row[kAtOnce];
+    float wj[kAtOnce];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = f[e] * wj;
-      float s = block_scale(group8_max(amax16(v)));
-      if (POW2) s = pow2_up(s);
-      store_unit(o, row, i, encode16(v, s, POW2), s);
+    for (int c = 0; c < kAtOnce; ++c) {
+      const long slot = t * k + (j0 + c < k ? j0 + c : j0);   // loads are not predicated
+      row[c] = rows[slot];
+      wj[c] = W ? w[slot] : 0.0f;
+      if (j0 + c >= k) row[c] = -1;
+    }
+#pragma unroll
+    for (int c = 0; c < kAtOnce; ++c) {
+      if ((unsigned)row[c] >= (unsigned)o.GM) continue;
+      if (W) {
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = f[e] * wj[c];
+        s = block_scale(group8_max(amax16(v)));
+        if (POW2) s = pow2_up(s);
+        q = encode16(v, s, POW2);
+      }
+      store_unit(o, row[c], i, q, s);
     }
   }
 }
@@ -133,19 +145,25 @@ __global__ __launch_bounds__(kThreads) void combine(const void* __restrict__ y, 
   const u32x4* yv = (const u32x4*)y;
 #pragma unroll
   for (int e = 0; e < R::kPer16; ++e) acc[e] = 0.0f;
-  for (int j0 = 0; j0 < k; j0 += 4) {
+  for (int j0 = 0; j0 < k && n_rows > 0; j0 += 4) {
     u32x4 v[4];
     float wj[4];
+    bool ok[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int j = j0 + c;
-      const int row = j < k ? rows[t * k + j] : -1;
-      const bool ok = (unsigned)row < (unsigned)n_rows;
-      wj[c] = !ok ? 0.0f : W ? w[t * k + j] : 1.0f;
-      v[c] = ok ? yv[(long)row * per + i] : u32x4{0u, 0u, 0u, 0u};
+      // loads are not predicated (a branch each, and a wait): without a row the first one is read and dropped
+      const int row = rows[t * k + (j < k ? j : j0)];
+      ok[c] = j < k && (unsigned)row < (unsigned)n_rows;
+      wj[c] = W ? w[t * k + (j < k ? j : j0)] : 1.0f;
+      v[c] = yv[(long)(ok[c] ? row : 0) * per + i];
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      if (!ok[c]) {
+        v[c] = u32x4{0u, 0u, 0u, 0u};
+        wj[c] = 0.0f;
+      }
       float f[R::kPer16];
       R::unpack(v[c], f);
 #pragma unroll

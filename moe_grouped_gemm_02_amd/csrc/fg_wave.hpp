@@ -22,7 +22,7 @@ constexpr int kBcast15 = 0x142, kBcast31 = 0x143;
 // The lane's partner value under a DPP control; rows outside ROWS get 0.
 template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, ROWS == 0xf);
 }
 template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ float dpp_f32(float v) {
@@ -31,27 +31,35 @@ __device__ __forceinline__ float dpp_f32(float v) {
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// Largest value over the wave (0 is the identity), uniform.
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+// Reductions over each group of 16 lanes or over the wave (L = 16 or 64), the
+// result in every lane of the group; sums in a fixed order.
+template <int L>
+__device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
   v = umax(v, dpp_u32<kQuadXor1>(v));
   v = umax(v, dpp_u32<kQuadXor2>(v));
   v = umax(v, dpp_u32<kHalfMirror>(v));
   v = umax(v, dpp_u32<kMirror>(v));
-  v = umax(v, dpp_u32<kBcast15, 0xa>(v));
-  v = umax(v, dpp_u32<kBcast31, 0xc>(v));
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+  if (L == 64) {
+    v = umax(v, dpp_u32<kBcast15, 0xa>(v));
+    v = umax(v, dpp_u32<kBcast31, 0xc>(v));
+    v = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+  }
+  return v;
 }
-
-// Sum over the wave in a fixed order, uniform.
-__device__ __forceinline__ float wave_sum(float v) {
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
   v += dpp_f32<kQuadXor1>(v);
   v += dpp_f32<kQuadXor2>(v);
   v += dpp_f32<kHalfMirror>(v);
   v += dpp_f32<kMirror>(v);
-  v += dpp_f32<kBcast15, 0xa>(v);
-  v += dpp_f32<kBcast31, 0xc>(v);
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+  if (L == 64) {
+    v += dpp_f32<kBcast15, 0xa>(v);
+    v += dpp_f32<kBcast31, 0xc>(v);
+    v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+  }
+  return v;
 }
+__device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
 
 // Largest value over each group of eight lanes, for values >= 0.
 __device__ __forceinline__ float group8_max(float v) {

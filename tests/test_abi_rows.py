@@ -95,7 +95,7 @@ def test_plan_capacity_is_reached_and_enough(T, k, G, align):
 
 def test_adapters_workspace():
     L, size = fg.lib(), ctypes.c_size_t()
-    assert L.fg_adapters_workspace(16, 7168, 1024, 16, ctypes.byref(size)) == OK and size.value % (1024 * 16 * 4) == 0
+    assert L.fg_adapters_workspace(16, 7168, 1024, 16, ctypes.byref(size)) == OK and size.value >= 1024 * 16 * 4
     assert L.fg_adapters_workspace(16, 7168, 1000, 16, ctypes.byref(size)) == EINVAL
     assert L.fg_adapters_workspace(16, 7168, 1024, 16, None) == EINVAL
     assert L.fg_plan_workspace(4, 8, 16, ctypes.byref(size)) == OK and size.value == 0
