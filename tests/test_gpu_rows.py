@@ -533,3 +533,35 @@ def test_refusals():
         fg.adapters(**{**ok, "D": torch.zeros(4, 64, device=d)})
     with pytest.raises(ValueError):
         fg.Plan.masked(p.rows, p.slots, ids.view(-1)[:3], 7)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("H", [128, 1024, 1152])
+def test_dispatch_quant_extreme_blocks(H, pow2):
+    """Signed zeros, blocks of tiny and of huge values, values that are exact ties of the code grid: bit for bit the oracle's."""
+    T, k, G = 64, 2, 3
+    rng = np.random.default_rng(H)
+    x = rng.standard_normal((T, H)).astype(np.float32)
+    for i, e in enumerate(range(-110, 120, 8)):      # scales from 2^-117 (below 2^-141 amax / 448 is no fp32 number)
+        x[i] *= np.float32(2.0 ** e)
+    x[40] = 0.0
+    x[41] = -0.0
+    x[42, ::2] = -0.0
+    t = oracle.decode_table()[:0x7F]
+    ties = ((t[:-1] + t[1:]) / 2).astype(np.float32)
+    for i in range(43, 60):
+        x[i, :126] = ties * rng.choice([-1, 1], 126)
+        x[i, 126] = 448.0
+        x[i] *= np.float32(1 + (i - 43) / 16)
+    p = make_plan("contiguous", T, k, G, drop=False)
+    w = (2.0 ** rng.integers(-3, 3, (T, k))).astype(np.float32)
+    for weight in (None, w):
+        Q, sa = fg.dispatch_quant(to_dev(x), p, w=None if weight is None else to_dev(weight), pow2=pow2)
+        slots = host(p.slots)
+        real = slots >= 0
+        v = x[np.maximum(slots, 0) // k]
+        if weight is not None:
+            v = v * weight.reshape(-1)[np.maximum(slots, 0)][:, None]
+        codes, scales = oracle.quantize_act_1x128(v, pow2)
+        assert np.array_equal(host(sa).T[real], scales[real])
+        assert np.array_equal(host(Q)[real], codes[real])
