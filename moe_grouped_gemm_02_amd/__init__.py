@@ -136,11 +136,12 @@ def _call(fn, dev, *args):
     FGError on a nonzero return code."""
     torch = _torch()
     if torch.cuda.current_device() == dev.index:
-        code = getattr(lib(), fn)(*args)
+        code = getattr(_lib or lib(), fn)(*args)
     else:
         with torch.cuda.device(dev):
             code = getattr(lib(), fn)(*args)
-    _check(code, fn)
+    if code:
+        _check(code, fn)
 
 
 def _fp8(t, name, shape, device=None):
@@ -497,48 +498,53 @@ class Plan:
     rows [T, k] int32: the slot's row, -1 if none; slots int32: each row's slot t * k + j,
     -1 if none. Contiguous: m_indices (per row, as grouped_contiguous takes it), offsets
     [G + 1], align. Masked: masked_m [G], M_max; row g * M_max + r is row r of expert g."""
-    __slots__ = ("layout", "rows", "slots", "m_indices", "offsets", "align", "masked_m", "M_max", "G")
+    __slots__ = ("layout", "rows", "slots", "m_indices", "offsets", "align", "masked_m", "M_max", "G",
+                 "T", "k", "device", "capacity", "lead", "_blocks")
 
     def __init__(self, layout, rows, slots, m_indices, offsets, align, masked_m, M_max, G):
         self.layout, self.rows, self.slots, self.G = layout, rows, slots, G
         self.m_indices, self.offsets, self.align = m_indices, offsets, align
         self.masked_m, self.M_max = masked_m, M_max
+        self.T, self.k = rows.shape
+        self.device = rows.device
+        self.capacity = slots.shape[0]          # rows of the layout (masked: G * M_max)
+        # leading dimensions of the layout's tensors: (capacity,) or (G, M_max)
+        self.lead = (G, M_max) if layout == LAYOUT_MASKED else (self.capacity,)
+        self._blocks = self.lead if layout == LAYOUT_MASKED else (1, self.capacity)   # the library's G, M
 
     @classmethod
     def contiguous(cls, rows, slots, m_indices, offsets, align):
-        torch = _torch()
         _plan_rows(rows, slots)
-        _dev(m_indices, "m_indices", (slots.shape[0],), torch.int32, rows.device)
-        _dev(offsets, "offsets", (offsets.numel(),), torch.int32, rows.device)
-        if align < 1 or slots.shape[0] % align or offsets.numel() < 2:
+        _index(m_indices, "m_indices", rows.device, slots.shape[0])
+        _index(offsets, "offsets", rows.device)
+        if align < 1 or slots.shape[0] % align or offsets.shape[0] < 2:
             raise ValueError("a contiguous plan has G + 1 >= 2 offsets and a multiple of align rows")
-        return cls(LAYOUT_CONTIGUOUS, rows, slots, m_indices, offsets, align, None, 0, offsets.numel() - 1)
+        return cls(LAYOUT_CONTIGUOUS, rows, slots, m_indices, offsets, align, None, 0, offsets.shape[0] - 1)
 
     @classmethod
     def masked(cls, rows, slots, masked_m, M_max):
-        torch = _torch()
         _plan_rows(rows, slots)
-        _dev(masked_m, "masked_m", (masked_m.numel(),), torch.int32, rows.device)
-        if slots.shape[0] != masked_m.numel() * M_max or M_max < 1 or masked_m.numel() < 1:
+        _index(masked_m, "masked_m", rows.device)
+        G = masked_m.shape[0]
+        if slots.shape[0] != G * M_max or M_max < 1 or G < 1:
             raise ValueError("a masked plan has G * M_max slots")
-        return cls(LAYOUT_MASKED, rows, slots, None, None, 1, masked_m, M_max, masked_m.numel())
+        return cls(LAYOUT_MASKED, rows, slots, None, None, 1, masked_m, M_max, G)
 
-    @property
-    def capacity(self):
-        """Rows of the layout (masked: G * M_max)."""
-        return self.slots.shape[0]
 
-    def lead(self):
-        """Leading dimensions of the layout's tensors: (capacity,) or (G, M_max)."""
-        return (self.G, self.M_max) if self.layout == LAYOUT_MASKED else (self.slots.shape[0],)
+def _index(t, name, device, n=None):
+    """Checks an int32 vector (of n entries if given) on `device`."""
+    shape = t.shape
+    if (len(shape) == 1 and t.dtype is _torch().int32 and t.device == device and t.is_contiguous()
+            and (n is None or shape[0] == n)):
+        return
+    _dev(t, name, (t.numel() if n is None else n,), _torch().int32, device)
 
 
 def _plan_rows(rows, slots):
-    torch = _torch()
     if rows.dim() != 2 or slots.dim() != 1:
         raise ValueError("rows must be [T, k] and slots [rows]")
-    _dev(rows, "rows", tuple(rows.shape), torch.int32)
-    _dev(slots, "slots", tuple(slots.shape), torch.int32, rows.device)
+    _dev(rows, "rows", rows.shape, _torch().int32)
+    _index(slots, "slots", rows.device)
 
 
 def _plan_args(ids, G):
@@ -602,52 +608,44 @@ def plan_masked(ids, G, M_max):
     return Plan(LAYOUT_MASKED, rows, slots, None, None, 1, masked_m, M_max, G)
 
 
-def _quant_rows(plan, H, dev, Q, sa):
+def _quant_rows(plan, H, Q, sa):
     """The sorted E4M3 operand: Q [*lead, H], sa [H/128, capacity] or [G, H/128, M_max]."""
     torch = _torch()
-    lead = plan.lead()
-    sa_shape = lead[:-1] + (H // 128, lead[-1])
-    if H % 128:
-        raise ValueError("rows must be a multiple of 128 long")
+    lead = plan.lead
+    if H % 128 or H < 128:
+        raise ValueError("rows must be a positive multiple of 128 long")
     if Q is None:
-        Q = torch.empty(lead + (H,), dtype=torch.uint8, device=dev)
+        Q = torch.empty(lead + (H,), dtype=torch.uint8, device=plan.device)
     else:
-        _fp8(Q, "Q", lead + (H,), dev)
-    sa = _new(sa, "sa", sa_shape, torch.float32, dev)
-    G, M = (lead if len(lead) == 2 else (1,) + lead)
-    return Q, sa, G, M
-
-
-def _token_rows(t, name, plan, dev=None):
-    T = plan.rows.shape[0]
-    if t.dim() != 2 or t.shape[0] != T:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{T}, columns]")
-    _dev(t, name, tuple(t.shape), device=plan.rows.device)
-    return t.shape[1]
+        _fp8(Q, "Q", lead + (H,), plan.device)
+    sa = _new(sa, "sa", lead[:-1] + (H // 128, lead[-1]), torch.float32, plan.device)
+    return Q, sa
 
 
 def dispatch_quant(x, plan, w=None, pow2=False, Q=None, sa=None):
     """Token rows x [T, H] (bf16 or fp32), times w [T, k] if given, into the plan's layout as
     the grouped GEMM's A operand: E4M3 codes Q ([capacity, H] or [G, M_max, H]) and scales sa
     ([H/128, capacity] or [G, H/128, M_max]). Rows without a slot are not written."""
-    torch = _torch()
     dt = _elem(x, "x")
-    H = _token_rows(x, "x", plan)
-    dev = x.device
-    T, k = plan.rows.shape
+    dev, T, k = plan.device, plan.T, plan.k
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [{T}, columns]")
+    H = x.shape[1]
+    _dev(x, "x", (T, H), None, dev)
     if w is not None:
-        _dev(w, "w", (T, k), torch.float32, dev)
-    Q, sa, G, M = _quant_rows(plan, H, dev, Q, sa)
+        _dev(w, "w", (T, k), _torch().float32, dev)
+    Q, sa = _quant_rows(plan, H, Q, sa)
+    G, M = plan._blocks
     _call("fg_dispatch_quant", dev, _ptr(x), dt, _ptr(plan.rows), _opt_ptr(w), _ptr(Q), _ptr(sa), T, k, H, G, M,
           int(bool(pow2)), _stream(x))
     return Q, sa
 
 
-def _sorted_rows(y, plan, dev):
-    if y.dim() != len(plan.lead()) + 1:
-        raise ValueError(f"y has shape {tuple(y.shape)}, expected {plan.lead()} + (N,)")
+def _sorted_rows(y, plan):
+    if y.dim() != len(plan.lead) + 1:
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected {plan.lead} + (N,)")
     N = y.shape[-1]
-    _dev(y, "y", plan.lead() + (N,), device=dev)
+    _dev(y, "y", plan.lead + (N,), None, plan.device)
     if N % 8 or N < 8:
         raise ValueError("N must be a positive multiple of 8")
     return N
@@ -656,13 +654,11 @@ def _sorted_rows(y, plan, dev):
 def combine(y, plan, w=None, base=None, out=None):
     """out[t] = base[t] + sum_j w[t, j] y[row of slot (t, j)]: the experts' rows back in token
     order ([T, N], y's type). w None: all ones, which is dispatch's gradient. out may be base."""
-    torch = _torch()
-    dev = plan.rows.device
     dt = _elem(y, "y")
-    N = _sorted_rows(y, plan, dev)
-    T, k = plan.rows.shape
+    N = _sorted_rows(y, plan)
+    dev, T, k = plan.device, plan.T, plan.k
     if w is not None:
-        _dev(w, "w", (T, k), torch.float32, dev)
+        _dev(w, "w", (T, k), _torch().float32, dev)
     if base is not None:
         _dev(base, "base", (T, N), y.dtype, dev)
     out = _new(out, "out", (T, N), y.dtype, dev)
@@ -677,34 +673,33 @@ def dispatch_grad(dA, plan, out=None):
 
 
 def _combine_grad_args(dout, y, plan, w, dw):
-    torch = _torch()
-    dev = plan.rows.device
     dt = _elem(y, "y")
-    N = _sorted_rows(y, plan, dev)
-    T, k = plan.rows.shape
+    N = _sorted_rows(y, plan)
+    dev, T, k = plan.device, plan.T, plan.k
+    f32 = _torch().float32
     _dev(dout, "dout", (T, N), y.dtype, dev)
-    _dev(w, "w", (T, k), torch.float32, dev)
-    return dev, dt, N, T, k, _new(dw, "dw", (T, k), torch.float32, dev)
+    _dev(w, "w", (T, k), f32, dev)
+    return dt, N, _new(dw, "dw", (T, k), f32, dev)
 
 
 def combine_grad(dout, y, plan, w, dy=None, dw=None, with_dy=True):
     """Gradient of combine: (dy in y's shape and type, rows without a slot not written, or None
     with with_dy=False; dw [T, k] fp32)."""
-    torch = _torch()
-    dev, dt, N, T, k, dw = _combine_grad_args(dout, y, plan, w, dw)
+    dt, N, dw = _combine_grad_args(dout, y, plan, w, dw)
     if dy is not None or with_dy:
-        dy = _new(dy, "dy", tuple(y.shape), y.dtype, dev)
-    _call("fg_combine_grad", dev, _ptr(dout), _ptr(y), dt, _ptr(plan.rows), _ptr(w), _opt_ptr(dy), _ptr(dw), T, k, N,
-          plan.capacity, _stream(dout))
+        dy = _new(dy, "dy", y.shape, y.dtype, plan.device)
+    _call("fg_combine_grad", plan.device, _ptr(dout), _ptr(y), dt, _ptr(plan.rows), _ptr(w), _opt_ptr(dy), _ptr(dw),
+          plan.T, plan.k, N, plan.capacity, _stream(dout))
     return dy, dw
 
 
 def combine_grad_quant(dout, y, plan, w, pow2=False, Q=None, sa=None, dw=None):
     """combine_grad with dy as the backward GEMM's operand: (Q E4M3 codes, sa scales, dw)."""
-    dev, dt, N, T, k, dw = _combine_grad_args(dout, y, plan, w, dw)
-    Q, sa, G, M = _quant_rows(plan, N, dev, Q, sa)
-    _call("fg_combine_grad_quant", dev, _ptr(dout), _ptr(y), dt, _ptr(plan.rows), _ptr(w), _ptr(Q), _ptr(sa),
-          _ptr(dw), T, k, N, G, M, int(bool(pow2)), _stream(dout))
+    dt, N, dw = _combine_grad_args(dout, y, plan, w, dw)
+    Q, sa = _quant_rows(plan, N, Q, sa)
+    G, M = plan._blocks
+    _call("fg_combine_grad_quant", plan.device, _ptr(dout), _ptr(y), dt, _ptr(plan.rows), _ptr(w), _ptr(Q), _ptr(sa),
+          _ptr(dw), plan.T, plan.k, N, G, M, int(bool(pow2)), _stream(dout))
     return Q, sa, dw
 
 
@@ -723,15 +718,15 @@ def adapters(D, x, A, B, scales, plan, out=None):
     torch = _torch()
     if D.dim() != 2 or x.dim() != 2 or A.dim() != 3:
         raise ValueError("D must be [T, N], x [T, K] and A [L, R, K]")
-    if plan.layout != LAYOUT_CONTIGUOUS or plan.rows.shape[1] != 1 or plan.align % 16:
+    if plan.layout != LAYOUT_CONTIGUOUS or plan.k != 1 or plan.align % 16:
         raise ValueError("adapters need a contiguous plan of ids [T, 1] with align a multiple of 16")
     T, N = D.shape
     L, R, K = A.shape
     dev = D.device
     bf = torch.bfloat16
-    if plan.rows.shape[0] != T or plan.G != L or plan.rows.device != dev:
-        raise ValueError(f"the plan is of {plan.rows.shape[0]} tokens and {plan.G} adapters on "
-                         f"{plan.rows.device}, the call of {T} and {L} on {dev}")
+    if plan.T != T or plan.G != L or plan.device != dev:
+        raise ValueError(f"the plan is of {plan.T} tokens and {plan.G} adapters on {plan.device}, "
+                         f"the call of {T} and {L} on {dev}")
     if R % 8 or not 8 <= R <= 128 or K % 128 or N % 8:
         raise ValueError("R must be a multiple of 8 up to 128, K of 128 and N of 8")
     _dev(D, "D", (T, N), bf, dev)

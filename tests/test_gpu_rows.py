@@ -212,7 +212,7 @@ def test_dispatch_quant(layout, T, k, G, H, pow2, dtype, weighted):
     p = make_plan(layout, T, k, G)
     x = to_dev(rows_input(rng, (T, H)), torch.bfloat16 if dtype == "bf16" else torch.float32)
     w = rng.standard_normal((T, k)).astype(np.float32) if weighted else None
-    lead = p.lead()
+    lead = p.lead
     Q = torch.full(lead + (H,), 0x55, dtype=torch.uint8, device=dev())
     sa = torch.full(lead[:-1] + (H // 128, lead[-1]), -7.0, device=dev())
     fg.dispatch_quant(x, p, w=None if w is None else to_dev(w), pow2=pow2, Q=Q, sa=sa)
@@ -237,7 +237,7 @@ def test_combine(layout, T, k, G, N, dtype, weighted, with_base):
     rng = np.random.default_rng(N + T)
     p = make_plan(layout, T, k, G)
     td = torch.bfloat16 if dtype == "bf16" else torch.float32
-    y = torch.full(p.lead() + (N,), float("nan"), dtype=td, device=dev())     # rows without a slot are never read into a sum
+    y = torch.full(p.lead + (N,), float("nan"), dtype=td, device=dev())     # rows without a slot are never read into a sum
     real = to_dev((host(p.slots) >= 0))
     y.view(-1, N)[real] = torch.from_numpy(rng.standard_normal((int(real.sum()), N)).astype(np.float32)).to(dev(), td)
     w = rng.standard_normal((T, k)).astype(np.float32) if weighted else None
@@ -255,7 +255,7 @@ def grad_inputs(layout, T, k, G, N, dtype):
     rng = np.random.default_rng(N + T + 1)
     p = make_plan(layout, T, k, G)
     td = torch.bfloat16 if dtype == "bf16" else torch.float32
-    y = to_dev(rng.standard_normal(p.lead() + (N,)).astype(np.float32), td)
+    y = to_dev(rng.standard_normal(p.lead + (N,)).astype(np.float32), td)
     dout = to_dev(rows_input(rng, (T, N)), td)
     w = rng.standard_normal((T, k)).astype(np.float32)
     return p, y, dout, w, td
@@ -279,7 +279,7 @@ def check_dw(dw, p, y, dout, N):
 def test_combine_grad(layout, T, k, G, N, dtype):
     print(f"grad {layout} {T}x{k} G={G} N={N} {dtype}", flush=True)
     p, y, dout, w, td = grad_inputs(layout, T, k, G, N, dtype)
-    dy = torch.full(p.lead() + (N,), 9.0, dtype=td, device=dev())
+    dy = torch.full(p.lead + (N,), 9.0, dtype=td, device=dev())
     dy, dw = fg.combine_grad(dout, y, p, to_dev(w), dy=dy)
     check_dw(host(dw), p, y, dout, N)
     slots = host(p.slots)
@@ -299,7 +299,7 @@ def test_combine_grad_quant(layout, T, k, G, N, pow2, dtype):
     """The E4M3 gradient is dispatch_quant's of the weighted rows, bit for bit; the weights' gradient as in 64 bits."""
     print(f"grad quant {layout} {T}x{k} G={G} N={N} pow2={pow2} {dtype}", flush=True)
     p, y, dout, w, _ = grad_inputs(layout, T, k, G, N, dtype)
-    lead = p.lead()
+    lead = p.lead
     mk = lambda: (torch.full(lead + (N,), 0x55, dtype=torch.uint8, device=dev()),  # noqa: E731
                   torch.full(lead[:-1] + (N // 128, lead[-1]), -7.0, device=dev()))
     Q, sa = mk()
@@ -315,12 +315,12 @@ def test_combine_gradient_against_differences():
     T, k, G, N = 20, 3, 4, 64
     rng = np.random.default_rng(5)
     p = make_plan("contiguous", T, k, G)
-    y = to_dev(rng.standard_normal(p.lead() + (N,)).astype(np.float32))
+    y = to_dev(rng.standard_normal(p.lead + (N,)).astype(np.float32))
     dout = to_dev(rng.standard_normal((T, N)).astype(np.float32))
     w = to_dev(rng.standard_normal((T, k)).astype(np.float32))
     dy, dw = fg.combine_grad(dout, y, p, w, dy=torch.zeros_like(y))
     dirw = to_dev(rng.standard_normal((T, k)).astype(np.float32))
-    diry = to_dev(rng.standard_normal(p.lead() + (N,)).astype(np.float32))
+    diry = to_dev(rng.standard_normal(p.lead + (N,)).astype(np.float32))
     f = lambda y_, w_: (dout.double() * fg.combine(y_, p, w=w_).double()).sum()  # noqa: E731
     for num, ana in (((f(y, w + dirw) - f(y, w - dirw)) / 2, (dw.double() * dirw.double()).sum()),
                      ((f(y + diry, w) - f(y - diry, w)) / 2, (dy.double() * diry.double()).sum())):
@@ -333,7 +333,7 @@ def test_dispatch_gradient_is_the_copies_transpose():
     T, k, G, N = 50, 4, 6, 256
     rng = np.random.default_rng(6)
     p = make_plan("masked", T, k, G)
-    dA = rng.standard_normal(p.lead() + (N,)).astype(np.float32)
+    dA = rng.standard_normal(p.lead + (N,)).astype(np.float32)
     x = rng.standard_normal((T, N)).astype(np.float32)
     slots = host(p.slots)
     copies = np.where((slots >= 0)[:, None], x[np.maximum(slots, 0) // k], 0)
