@@ -307,8 +307,8 @@ int fg_route_topk_grad(const void* logits, int dtype, const int32_t* ids, const 
  *   rows  [T][k] int32 out: the slot's row, -1 if it has none.
  *   slots [rows] int32 out: the row's slot, -1 if it has none.
  * Contiguous: expert g's slots are rows offsets[g] ..., and every segment
- *   starts at a multiple of `align` rows (128 for the grouped GEMM; 16, 32 or
- *   64 for fg_adapters). slots and m_indices have fg_plan_capacity rows, the
+ *   starts at a multiple of `align` rows (128 for the grouped GEMM; 16 or 64
+ *   for fg_adapters). slots and m_indices have fg_plan_capacity rows, the
  *   most any ids can need; m_indices is the row's expert or -1, as
  *   fg_grouped_contiguous reads it; offsets [G + 1], offsets[G] the rows in use.
  * Masked: row g * M_max + r holds expert g's r-th slot; slots past M_max get no
@@ -362,18 +362,18 @@ int fg_combine_grad_quant(const void* dout, const void* y, int dtype, const int3
  *   out[t] = D[t] + scales[a] * (x[t] . A[a]^T) . B[a]^T, a = the token's adapter,
  * in fp32, rounded once; out[t] = D[t] for a token without one.
  *   D, out [T][N] bf16 (out may be D), x [T][K] bf16, A [L][R][K] bf16,
- *   B [L][N][R] bf16, scales [L] fp32; rows, slots, m_indices: the contiguous
+ *   B [L][N][R] bf16, scales [L] fp32; rows, slots, m_indices, offsets: the contiguous
  *   plan of the tokens' adapter ids (k = 1, G = L), cap its rows and align its
  *   alignment, a multiple of 16. A tile has 64 rows if 64 divides align, else
- *   32 or 16: 64 suits prompts (many tokens per adapter), 16 decode.
+ *   16: 64 suits prompts (many tokens per adapter), 16 decode.
  *   R % 8 == 0, 8 <= R <= 128 (smaller adapters are padded with zeros);
  *   K % 128 == 0, N % 8 == 0; tensors 16-byte aligned.
  *   ws: fg_adapters_workspace bytes, 16-byte aligned.
  */
 int fg_adapters_workspace(int R, int K, int cap, int align, size_t* bytes);
 int fg_adapters(const void* D, const void* x, const void* A, const void* B, const float* scales, const int32_t* rows,
-                const int32_t* slots, const int32_t* m_indices, void* out, void* ws, int T, int L, int R, int K, int N,
-                int cap, int align, hipStream_t stream);
+                const int32_t* slots, const int32_t* m_indices, const int32_t* offsets, void* out, void* ws, int T,
+                int L, int R, int K, int N, int cap, int align, hipStream_t stream);
 
 /* Static, human-readable description of a return code. */
 const char* fg_strerror(int code);

@@ -65,7 +65,7 @@ def _declare(L):
     L.fg_combine_grad.argtypes = [vp, vp, i, ip, fp, vp, fp, i, i, i, i, vp]
     L.fg_combine_grad_quant.argtypes = [vp, vp, i, ip, fp, vp, fp, fp, i, i, i, i, i, i, vp]
     L.fg_adapters_workspace.argtypes = [i, i, i, i, sz]
-    L.fg_adapters.argtypes = [vp, vp, vp, vp, fp, ip, ip, ip, vp, vp, i, i, i, i, i, i, i, vp]
+    L.fg_adapters.argtypes = [vp, vp, vp, vp, fp, ip, ip, ip, ip, vp, vp, i, i, i, i, i, i, i, vp]
     L.fg_strerror.argtypes = [i]
     L.fg_strerror.restype = ctypes.c_char_p
     for name in ENTRY_POINTS:
@@ -737,5 +737,5 @@ def adapters(D, x, A, B, scales, plan, out=None):
     out = _new(out, "out", (T, N), bf, dev)
     ws = torch.empty(_adapters_workspace(R, K, plan.capacity, plan.align), dtype=torch.uint8, device=dev)
     _call("fg_adapters", dev, _ptr(D), _ptr(x), _ptr(A), _ptr(B), _ptr(scales), _ptr(plan.rows), _ptr(plan.slots),
-          _ptr(plan.m_indices), _ptr(out), _ptr(ws), T, L, R, K, N, plan.capacity, plan.align, _stream(D))
+          _ptr(plan.m_indices), _ptr(plan.offsets), _ptr(out), _ptr(ws), T, L, R, K, N, plan.capacity, plan.align, _stream(D))
     return out

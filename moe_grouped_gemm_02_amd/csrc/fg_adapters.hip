@@ -46,15 +46,26 @@ struct AdapterArgs {
   const uint16_t *D, *x, *A, *B;
   const float* scales;
   const int32_t *rows, *slots, *m_indices;
+  const int32_t* used;    // rows of the plan in use (its offsets[L])
   uint16_t* out;
   float* ws;              // [parts][cap][16 * TR]
   uint16_t* spare;        // 64 x 16 bytes that hold nothing
   int T, L, R, K, N, cap;
   int parts;              // parts of K
   int strip;              // columns of one expand workgroup
-  int tiles;              // row tiles
-  int copies;             // workgroups of expand that pass tokens through
+  int tiles, tiles_up8;   // row tiles, and their number rounded up to 8
+  int copies;             // workgroups of expand that pass tokens through (a multiple of 8)
 };
+
+// The row tile of position i of the tiles_up8 in a launch: workgroups go round-robin
+// to the 8 XCDs, and each XCD gets a run of the tiles in use, so that an adapter's A
+// and B pass through one or two of the L2s and not through all. -1: no tile.
+__device__ __forceinline__ int tile_of(const AdapterArgs& p, int i, int rows) {
+  const int in_use = *p.used / rows, U = in_use < p.tiles ? in_use : p.tiles;
+  const int xcd = i & 7, lo = (int)((long)U * xcd >> 3), hi = (int)((long)U * (xcd + 1) >> 3);
+  const int tile = lo + (i >> 3);
+  return tile < hi ? tile : -1;
+}
 
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
@@ -71,7 +82,8 @@ template <int TR>
 __global__ __launch_bounds__(kThreads) void adapter_shrink16(AdapterArgs p) {
   constexpr int RT = 16, RC = 16 * TR, RP = RC + 4;
   __shared__ float red[kWaves][RT][RP];
-  const int r0 = blockIdx.x * RT;
+  const int tile = tile_of(p, blockIdx.x, RT), r0 = tile * RT;
+  if (tile < 0) return;
   const int a = p.m_indices[r0];
   if ((unsigned)a >= (unsigned)p.L) return;   // no token in this tile (uniform)
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -169,7 +181,8 @@ __global__ __launch_bounds__(kThreads) void adapter_shrink64(AdapterArgs p) {
   constexpr int AI = TR > 2 ? TR / 2 : 1;           // A loads per wave and stage
   constexpr int kStageBytes = RT * 128 + RC * 128;
   __shared__ __attribute__((aligned(128))) uint8_t ring[kStages * kStageBytes];
-  const int r0 = blockIdx.x * RT;
+  const int tile = tile_of(p, blockIdx.x, RT), r0 = tile * RT;
+  if (tile < 0) return;
   const int a = p.m_indices[r0];
   if ((unsigned)a >= (unsigned)p.L) return;   // no token in this tile (uniform)
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -314,13 +327,19 @@ __device__ __forceinline__ void copy_tokens(const AdapterArgs& p, int block) {
 // eight consecutive columns 8 q .. 8 q + 7 and D moves in 16-byte pieces.
 __device__ __forceinline__ int pair_row(int i, int e) { return 8 * (i >> 2) + 4 * e + (i & 3); }
 
-// out = D + the pair's products, for one lane's eight columns.
-__device__ __forceinline__ u32x4 add_pair(u32x4 d, const f32x4v* acc) {
-  float v[8];
-  RowBf16::unpack(d, v);
+// A lane's eight columns of D as the products' starting values, and back as bf16.
+__device__ __forceinline__ void start_pair(u32x4 d, f32x4v* acc) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] += acc[e >> 2][e & 3];
-  return RowBf16::pack(v);
+  for (int e = 0; e < 4; ++e) {
+    acc[e >> 1][2 * (e & 1)] = bf16_lo(d[e]);
+    acc[e >> 1][2 * (e & 1) + 1] = bf16_hi(d[e]);
+  }
+}
+__device__ __forceinline__ u32x4 end_pair(const f32x4v* acc) {
+  u32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = bf16_pair(acc[e >> 1][2 * (e & 1)], acc[e >> 1][2 * (e & 1) + 1]);
+  return r;
 }
 
 // Expand for 16-row tiles: each wave has its own columns, 32 at a time, and B's
@@ -329,7 +348,9 @@ template <int TR>
 __global__ __launch_bounds__(kThreads) void adapter_expand16(AdapterArgs p) {
   using H = HFrags<TR>;
   if ((int)blockIdx.x < p.copies) return copy_tokens(p, blockIdx.x);
-  const int job = blockIdx.x - p.copies, strip = job / p.tiles, r0 = (job - strip * p.tiles) * 16;
+  const int job = blockIdx.x - p.copies, strip = job / p.tiles_up8;
+  const int tile = tile_of(p, job - strip * p.tiles_up8, 16), r0 = tile * 16;
+  if (tile < 0) return;
   const int a = p.m_indices[r0];
   if ((unsigned)a >= (unsigned)p.L) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -357,14 +378,15 @@ __global__ __launch_bounds__(kThreads) void adapter_expand16(AdapterArgs p) {
     const int col = n0 + 8 * q;
     const bool ok = real && col < n_hi;
     const u32x4 d = *(const u32x4*)(drow + (col < n_hi ? col : n_lo));
-    f32x4v acc[2] = {};
+    f32x4v acc[2];
+    start_pair(d, acc);
 #pragma unroll
     for (int l = H::HL - 1; l >= 0; --l)   // the small halves first
 #pragma unroll
       for (int f = 0; f < H::KF; ++f)
 #pragma unroll
         for (int e = 0; e < 2; ++e) acc[e] = mfma(bf[e][f], h.f[l][f], acc[e]);
-    if (ok) *(u32x4*)(p.out + (long)tok * p.N + col) = add_pair(d, acc);
+    if (ok) *(u32x4*)(p.out + (long)tok * p.N + col) = end_pair(acc);
   }
 }
 
@@ -381,35 +403,43 @@ __device__ __forceinline__ int swizzle_key(int n, int chunks) {
   return (chunks & (chunks - 1)) ? 0 : ((n & 3) | ((n >> 1) & 4)) & (chunks - 1);
 }
 
-template <int TR>
+// FULL: R is 16 TR, every fragment is of ranks below R.
+template <int TR, bool FULL>
 __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
   using H = HFrags<TR>;
   constexpr int NI = TR;                       // loads per wave and buffer: 128 columns x 2 TR chunks / 256
   __shared__ __attribute__((aligned(128))) uint8_t ring[2][NI * kThreads * 16];
   if ((int)blockIdx.x < p.copies) return copy_tokens(p, blockIdx.x);
-  const int job = blockIdx.x - p.copies, strip = job / p.tiles, r0 = (job - strip * p.tiles) * 64;
+  const int job = blockIdx.x - p.copies, strip = job / p.tiles_up8;
+  const int tile = tile_of(p, job - strip * p.tiles_up8, 64), r0 = tile * 64;
+  if (tile < 0) return;
   const int a = p.m_indices[r0];
   if ((unsigned)a >= (unsigned)p.L) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lrow = lane & 15, q = lane >> 4;
   const int n_lo = strip * p.strip, n_hi = n_lo + p.strip < p.N ? n_lo + p.strip : p.N;
-  const int chunks = p.R >> 3;                 // 16-byte chunks of a row of B
+  const int chunks = FULL ? 2 * TR : p.R >> 3;   // 16-byte chunks of a row of B
   const uint16_t* Ba = p.B + (long)a * p.N * p.R;
   const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)&ring[0][0];
-  // this lane's LDS chunks hold row bn of the buffer's 128, chunk bc of it
-  int bn[NI], bc[NI];
+  // This lane's LDS chunks hold row bn of the buffer's 128, chunk bc of it: at byte boff from the
+  // buffer's first row in B. Rows past the buffer's 128 (R below 16 TR) or past N repeat a
+  // valid one; nothing reads them.
+  const int row_bytes = 16 * chunks;
+  int boff[NI], bmax[NI];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int g = (i * kWaves + wave) * 64 + lane;
-    bn[i] = g / chunks;
-    bc[i] = (g - bn[i] * chunks) ^ swizzle_key(bn[i], chunks);
+    const int g = (i * kWaves + wave) * 64 + lane, bn = g / chunks;
+    const int bc = (g - bn * chunks) ^ swizzle_key(bn, chunks);
+    boff[i] = (bn < kCols ? bn : kCols - 1) * row_bytes + 16 * bc;
+    bmax[i] = 16 * bc;
   }
   const auto issue = [&](int buffer, int n0) {
+    const char* base = (const char*)Ba + (long)n0 * row_bytes;
+    const int left = (p.N - 1 - n0) < kCols ? (p.N - 1 - n0) * row_bytes : kCols * row_bytes;   // last row of B from here
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      // rows past the buffer's 128 (R below 16 TR) or past N repeat a valid one; nothing reads them
-      const int n = n0 + (bn[i] < kCols ? bn[i] : kCols - 1);
-      dma16(Ba + (long)(n < p.N ? n : p.N - 1) * p.R + 8 * bc[i],
+      const int most = left + bmax[i];
+      dma16(base + (boff[i] < most ? boff[i] : most),
             lds0 + buffer * (NI * kThreads * 16) + (i * kWaves + wave) * 1024);
     }
   };
@@ -426,7 +456,7 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
 #pragma unroll
   for (int f = 0; f < H::KF; ++f) {
     const int c = TR == 1 ? q & 1 : 4 * f + q;
-    cc[f] = c < chunks ? c : 0;
+    cc[f] = FULL || c < chunks ? c : 0;
   }
   u32x4 d[2][NG];
   const auto load_d = [&](u32x4* v, int n0) {
@@ -437,23 +467,25 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
     }
   };
   load_d(d[0], n_lo);
-  // Loads and stores count down in order, so a wait for a load also waits for every
-  // store before it. Each round therefore issues the next round's loads before its
-  // own NG stores and leaves just those under way when it waits; for the count to be
-  // exact no store is skipped: lanes without an output write to spare memory.
+  // Each round issues the next one's loads, then its own NG stores. Loads and stores
+  // count down in order, so a wait for a load also waits for every store before it; at
+  // a round's end only its own stores stay under way. For the count to be exact no
+  // store is skipped: lanes without an output write to spare memory. (Loads two rounds
+  // ahead, with a third buffer, were slower: 47 against 38-46 us.)
   wait_vm<0>();
-  const auto round = [&](auto odd, int n0) {
-    constexpr int B = decltype(odd)::value;
+  const auto round = [&](auto which, int r) {
+    constexpr int B = decltype(which)::value;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the other buffer's reads are done
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    const int next = n0 + kCols < n_hi ? n0 + kCols : n_lo;   // the last round loads its first columns again
+    const int n0 = n_lo + kCols * r, next = n0 + kCols < n_hi ? n0 + kCols : n_lo;   // after the last, the first again
     issue(B ^ 1, next);
     load_d(d[B ^ 1], next);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      f32x4v acc[2] = {};
+      f32x4v acc[2];
+      start_pair(d[B][g], acc);
 #pragma unroll
       for (int f = 0; f < H::KF; ++f) {
 #pragma unroll
@@ -461,20 +493,21 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
           const int n = 32 * g + pair_row(lrow, e);
           // ranks past R: any chunk, dropped (a predicated read would be a branch and a wait of its own)
           u32x4 b = *(const u32x4*)(ring[B] + ((n * chunks + (cc[f] ^ swizzle_key(n, chunks))) << 4));
-          if (cc[f] != (TR == 1 ? q & 1 : 4 * f + q)) b = u32x4{0u, 0u, 0u, 0u};
+          if (!FULL && cc[f] != (TR == 1 ? q & 1 : 4 * f + q)) b = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
           for (int l = H::HL - 1; l >= 0; --l) acc[e] = mfma(b, h.f[l][f], acc[e]);
         }
       }
       const int col = n0 + 32 * g + 8 * q;
-      *(u32x4*)(real && col < n_hi ? orow + col : spare) = add_pair(d[B][g], acc);
+      *(u32x4*)(real && col < n_hi ? orow + col : spare) = end_pair(acc);
     }
     __builtin_amdgcn_sched_barrier(0);
     wait_vm<NG>();
   };
-  for (int n0 = n_lo; n0 < n_hi; n0 += 2 * kCols) {
-    round(std::integral_constant<int, 0>{}, n0);
-    if (n0 + kCols < n_hi) round(std::integral_constant<int, 1>{}, n0 + kCols);
+  const int rounds = (n_hi - n_lo + kCols - 1) / kCols;
+  for (int r = 0; r < rounds; r += 2) {
+    round(std::integral_constant<int, 0>{}, r);
+    if (r + 1 < rounds) round(std::integral_constant<int, 1>{}, r + 1);
   }
   wait_vm<0>();   // nothing may land in LDS after the workgroup has ended
 }
@@ -508,10 +541,11 @@ int sizes(int R, int K, int cap, int align) {
 
 template <int TR>
 void launch(const AdapterArgs& p, bool wide, hipStream_t s) {
-  const dim3 g1(p.tiles, p.parts), g2(p.copies + p.tiles * ((p.N + p.strip - 1) / p.strip)), b(kThreads);
+  const dim3 g1(p.tiles_up8, p.parts), g2(p.copies + p.tiles_up8 * ((p.N + p.strip - 1) / p.strip)), b(kThreads);
   if (wide) {
     hipLaunchKernelGGL(adapter_shrink64<TR>, g1, b, 0, s, p);
-    hipLaunchKernelGGL(adapter_expand64<TR>, g2, b, 0, s, p);
+    if (p.R == 16 * TR) hipLaunchKernelGGL((adapter_expand64<TR, true>), g2, b, 0, s, p);
+    else hipLaunchKernelGGL((adapter_expand64<TR, false>), g2, b, 0, s, p);
   } else {
     hipLaunchKernelGGL(adapter_shrink16<TR>, g1, b, 0, s, p);
     hipLaunchKernelGGL(adapter_expand16<TR>, g2, b, 0, s, p);
@@ -529,14 +563,15 @@ int fg_adapters_workspace(int R, int K, int cap, int align, size_t* bytes) {
 }
 
 int fg_adapters(const void* D, const void* x, const void* A, const void* B, const float* scales, const int32_t* rows,
-                const int32_t* slots, const int32_t* m_indices, void* out, void* ws, int T, int L, int R, int K, int N,
+                const int32_t* slots, const int32_t* m_indices, const int32_t* offsets, void* out, void* ws, int T, int L, int R, int K, int N,
                 int cap, int align, hipStream_t stream) {
   if (T < 0 || L < 1 || N < 8 || N % 8 || N > (1 << 24) || sizes(R, K, cap, align) != FG_OK) return FG_EINVAL;
   if (T == 0) return FG_OK;
   if (cap < 1) return FG_EINVAL;   // a plan of T > 0 tokens has rows
-  if (!D || !x || !A || !B || !scales || !rows || !slots || !m_indices || !out || !ws) return FG_EINVAL;
+  if (!D || !x || !A || !B || !scales || !rows || !slots || !m_indices || !offsets || !out || !ws) return FG_EINVAL;
   if (!aligned(D, 16) || !aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(out, 16) ||
-      !aligned(ws, 16) || !aligned(scales, 4) || !aligned(rows, 4) || !aligned(slots, 4) || !aligned(m_indices, 4))
+      !aligned(ws, 16) || !aligned(scales, 4) || !aligned(rows, 4) || !aligned(slots, 4) || !aligned(m_indices, 4) ||
+      !aligned(offsets, 4))
     return FG_EINVAL;
   const int st = current_device(nullptr);
   if (st != FG_OK) return st;
@@ -549,6 +584,7 @@ int fg_adapters(const void* D, const void* x, const void* A, const void* B, cons
   p.rows = rows;
   p.slots = slots;
   p.m_indices = m_indices;
+  p.used = offsets + L;
   p.out = static_cast<uint16_t*>(out);
   p.spare = static_cast<uint16_t*>(ws);
   p.ws = static_cast<float*>(ws) + kSpareBytes / sizeof(float);
@@ -560,14 +596,15 @@ int fg_adapters(const void* D, const void* x, const void* A, const void* B, cons
   p.cap = cap;
   const int rt = tile_rows(align);
   p.tiles = cap / rt;
+  p.tiles_up8 = (p.tiles + 7) / 8 * 8;
   p.parts = k_parts(p.tiles, rt, K);
-  p.copies = out != D ? (int)((T + 15L) / 16) : 0;
+  p.copies = out != D ? (int)((T + 127L) / 128 * 8) : 0;
   // columns of an expand workgroup: long strips load h less often, short ones fill the
   // chip (64-row tiles, T 8192, N 4096: 256 / 512 / 1024 / 2048 / 4096 columns take 47 /
   // 40 / 38-45 / 39 / 56 us)
   p.strip = 1024;
   while (p.strip > 128 && (long)p.tiles * ((N + p.strip - 1) / p.strip) < (rt == 64 ? 512 : 1024)) p.strip /= 2;
-  if ((long)p.copies + (long)p.tiles * ((N + p.strip - 1) / p.strip) > 0x7fffffffL) return FG_EINVAL;
+  if ((long)p.copies + (long)p.tiles_up8 * ((N + p.strip - 1) / p.strip) > 0x7fffffffL) return FG_EINVAL;
   switch (rank_groups(R)) {
     case 1: launch<1>(p, rt == 64, stream); break;
     case 2: launch<2>(p, rt == 64, stream); break;

@@ -26,7 +26,7 @@ DISPATCH = dict(x=P, dtype=0, rows=P, w=None, Q=P, sa=P, T=4, k=2, H=256, G=1, M
 COMBINE = dict(y=P, dtype=0, rows=P, w=None, base=None, out=P, T=4, k=2, N=64, n_rows=128, stream=None)
 GRAD = dict(dout=P, y=P, dtype=0, rows=P, w=P, dy=None, dw=P, T=4, k=2, N=64, n_rows=128, stream=None)
 GRAD_Q = dict(dout=P, y=P, dtype=0, rows=P, w=P, Q=P, sq=P, dw=P, T=4, k=2, N=128, G=2, M=64, scales=0, stream=None)
-ADAPTERS = dict(D=P, x=P, A=P, B=P, scales=P, rows=P, slots=P, m_indices=P, out=P, ws=P, T=4, L=2, R=16, K=128, N=64,
+ADAPTERS = dict(D=P, x=P, A=P, B=P, scales=P, rows=P, slots=P, m_indices=P, offsets=P, out=P, ws=P, T=4, L=2, R=16, K=128, N=64,
                 cap=32, align=16, stream=None)
 
 
@@ -53,7 +53,7 @@ ADAPTERS = dict(D=P, x=P, A=P, B=P, scales=P, rows=P, slots=P, m_indices=P, out=
                                            dict(scales=-1), dict(y=None)]),
         ("fg_adapters", ADAPTERS, [dict(T=-1), dict(L=0), dict(R=4), dict(R=12), dict(R=136), dict(K=64), dict(N=12),
                                    dict(align=8), dict(align=24), dict(cap=20), dict(cap=0), dict(ws=None), dict(D=None),
-                                   dict(x=ODD), dict(out=ODD), dict(slots=None), dict(scales=ODD)]),
+                                   dict(x=ODD), dict(out=ODD), dict(slots=None), dict(scales=ODD), dict(offsets=None)]),
     ] for c in cs], ids=lambda v: v if isinstance(v, str) else ",".join(v) if isinstance(v, dict) and len(v) < 4 else "")
 def test_bad_arguments_are_refused(name, good, changes):
     assert call(name, good, **changes) == EINVAL
