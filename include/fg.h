@@ -313,7 +313,7 @@ int fg_route_topk_grad(const void* logits, int dtype, const int32_t* ids, const 
  *   fg_grouped_contiguous reads it; offsets [G + 1], offsets[G] the rows in use.
  * Masked: row g * M_max + r holds expert g's r-th slot; slots past M_max get no
  *   row. slots has G * M_max entries; masked_m [G] as fg_grouped_masked reads it.
- * ws: fg_plan_workspace bytes of scratch (4-byte aligned), free again when the
+ * ws: fg_plan_workspace bytes of scratch (16-byte aligned), free again when the
  *   call's work on the stream is done; NULL where that is 0. G <= 1024.
  */
 int fg_plan_capacity(int T, int k, int G, int align, int* rows);

@@ -13,12 +13,15 @@
 // lane the mask of lanes with its id; the lanes below it in that mask are its
 // rank inside the batch of 64, and the lowest of them adds the batch's count to
 // the wave's histogram in LDS. Each wave owns consecutive slots, so scanning
-// the waves' histograms in order makes the ranks of a whole chunk; no atomics.
+// the waves' histograms in order makes the ranks of a workgroup's chunk.
 //
-// A batch of at most kOneBlock slots is sorted by one workgroup in one launch.
-// A larger one is cut into chunks: a first launch writes each chunk's
-// histogram to the workspace, a second one lets every chunk sum the histograms
-// before its own (its base) and all of them (the segments), and place its slots.
+// What a workgroup needs of the others is counts alone: of each expert's slots
+// before its chunk and in the whole batch. Up to kRecount slots every workgroup
+// counts the batch itself (whole-number LDS atomics, a few microseconds at most),
+// which saves a launch; beyond, a first launch leaves each chunk's histogram in the
+// workspace. Both are bound by latency. In a graph, G 64, contiguous, the one launch
+// takes 5.4 / 6.1 / 6.7 / 8.3 us at 2048 / 8192 / 16384 / 32768 slots and the two
+// launches 8.8 / 11.3 / 11.9 us at the first three and 10.4 us at 131072.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -32,14 +35,16 @@ using namespace fg;
 
 constexpr int kThreads = 512, kPlanWaves = kThreads / 64;
 constexpr int kMaxGroups = 1024;
-constexpr int kOneBlock = 4096;    // slots one workgroup sorts alone
-constexpr int kChunk = 2048;       // slots per workgroup otherwise
+constexpr int kRecount = 32768;    // slots up to which every workgroup counts them all
+constexpr int kBatches = 4;        // batches of 64 slots per wave beyond that
+constexpr int kChunk = kThreads * kBatches;
+constexpr int kFillRows = 1024;    // rows of the layout per workgroup, where that needs more of them
 
 struct PlanArgs {
   const int32_t* ids;
   int32_t *rows, *slots, *m_indices, *offsets, *masked_m;
-  const int32_t* hist;   // [chunks][G], null: a single workgroup
-  int S, G, align, M_max, cap, bits;
+  const int32_t* hist;   // [G][chunks_up4], null: count here
+  int S, G, align, M_max, cap, bits, chunks, chunks_up4;
 };
 
 // Inclusive sum over the workgroup's threads in thread order.
@@ -58,7 +63,7 @@ __device__ __forceinline__ int block_scan(int v, int* part) {
 }
 
 __global__ __launch_bounds__(kThreads) void plan_count(const int32_t* __restrict__ ids, int32_t* __restrict__ hist,
-                                                       int S, int G) {
+                                                       int S, int G, int chunks_up4) {
   __shared__ int n[kMaxGroups];
   for (int g = threadIdx.x; g < G; g += kThreads) n[g] = 0;
   __syncthreads();
@@ -70,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void plan_count(const int32_t* __restrict
     if (id >= 0 && id < G) atomicAdd(&n[id], 1);   // whole numbers: any order gives the same count
   }
   __syncthreads();
-  for (int g = threadIdx.x; g < G; g += kThreads) hist[(long)blockIdx.x * G + g] = n[g];
+  for (int g = threadIdx.x; g < G; g += kThreads) hist[(long)g * chunks_up4 + blockIdx.x] = n[g];
 }
 
 // NB: batches of 64 slots per wave.
@@ -112,29 +117,41 @@ __global__ __launch_bounds__(kThreads) void plan_place(PlanArgs p) {
     if (below == 0) mine[id[b]] = rank[b] + __popcll(same);
     __builtin_amdgcn_wave_barrier();
   }
+  // total and base, in whole numbers (any order of additions gives the same)
   if (p.hist) {
-    // threads take (expert, every parts-th chunk) pairs; whole-number sums
-    const int chunks = gridDim.x;
-    const int parts = kThreads / G > 1 ? kThreads / G : 1;
-    for (int i = tid; i < parts * G; i += kThreads) {
-      const int g = i % G;
+    // threads take (expert, four chunks) pairs
+    const int quads = p.chunks_up4 / 4;
+    for (int i = tid; i < G * quads; i += kThreads) {
+      const int g = i / quads, c = 4 * (i - g * quads);
+      const int4 n = *(const int4*)(p.hist + (long)g * p.chunks_up4 + c);
+      const int v[4] = {n.x, n.y, n.z, n.w};
       int before = 0, all = 0;
-      for (int c0 = i / G; c0 < chunks; c0 += 8 * parts) {
-        int n[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int c = c0 + u * parts;
-          n[u] = c < chunks ? p.hist[(long)c * G + g] : 0;
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          all += n[u];
-          before += c0 + u * parts < (int)blockIdx.x ? n[u] : 0;
-        }
+      for (int u = 0; u < 4; ++u) {
+        const int k = c + u < p.chunks ? v[u] : 0;
+        all += k;
+        before += c + u < (int)blockIdx.x ? k : 0;
       }
-      atomicAdd(&total[g], all);
-      atomicAdd(&base[g], before);
+      if (all) atomicAdd(&total[g], all);
+      if (before) atomicAdd(&base[g], before);
     }
+  } else if (gridDim.x > 1) {
+    const int first = (int)blockIdx.x * (kThreads * NB);
+    for (int s1 = 0; s1 < p.S; s1 += 8 * kThreads) {
+      int v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int s = s1 + u * kThreads + tid;
+        v[u] = p.ids[s < p.S ? s : p.S - 1];
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int s = s1 + u * kThreads + tid;
+        if (s < p.S && v[u] >= 0 && v[u] < G) atomicAdd(s < first ? &base[v[u]] : &total[v[u]], 1);
+      }
+    }
+    __syncthreads();
+    for (int g = tid; g < G; g += kThreads) total[g] += base[g];
   }
   __syncthreads();
   // each wave's first rank inside the chunk; one workgroup: the chunk is the batch
@@ -146,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void plan_place(PlanArgs p) {
       hist[w * GS + g] = n;
       n += c;
     }
-    if (!p.hist) total[g] = n;
+    if (gridDim.x == 1) total[g] = n;
   }
   __syncthreads();
   // first rows of the experts
@@ -183,19 +200,19 @@ __global__ __launch_bounds__(kThreads) void plan_place(PlanArgs p) {
       p.rows[s] = row;
     }
   }
-  // rows without a slot: behind each expert's last one, and behind the last expert
-  const int nw = gridDim.x * kPlanWaves;
-  for (int g = blockIdx.x * kPlanWaves + wave; g <= G; g += nw) {
-    int from = start[g], to = p.cap;
-    if (g < G) {
-      const int n = total[g];
-      from += masked && n > p.M_max ? p.M_max : n;
-      to = start[g + 1];
-    }
-    for (int r = from + lane; r < to; r += 64) {
+  // rows without a slot: behind each expert's last one, a wave per expert, and behind
+  // the last expert, all waves
+  const int nw = gridDim.x * kPlanWaves, me = blockIdx.x * kPlanWaves + wave;
+  for (int g = me; g < G; g += nw) {
+    const int n = total[g], to = start[g + 1];
+    for (int r = start[g] + (masked && n > p.M_max ? p.M_max : n) + lane; r < to; r += 64) {
       p.slots[r] = -1;
       if (!masked) p.m_indices[r] = -1;
     }
+  }
+  for (long r = (long)start[G] + 64L * me + lane; r < p.cap; r += 64L * nw) {
+    p.slots[r] = -1;
+    if (!masked) p.m_indices[r] = -1;
   }
   if (blockIdx.x == 0) {
     for (int g = tid; g <= G; g += kThreads) {
@@ -215,25 +232,28 @@ long long capacity(int T, int k, int G, int align) {
 }
 
 int chunks_of(int S) { return (int)(((long long)S + kChunk - 1) / kChunk); }
+int up4(int n) { return (n + 3) / 4 * 4; }
 
 int plan(PlanArgs p, void* ws, hipStream_t stream) {
   const int st = current_device(nullptr);
   if (st != FG_OK) return st;
   p.bits = 32 - __builtin_clz((unsigned)p.G);   // ids 0 .. G
-  const int chunks = p.S <= kOneBlock ? 1 : chunks_of(p.S);
   const size_t lds = sizeof(int) * ((size_t)(kPlanWaves + 1) * (p.G + 1) + 2 * p.G + kPlanWaves);
-  if (chunks > 1) {
-    if (!ws || !aligned(ws, 4)) return FG_EINVAL;
+  // enough workgroups for the slots, and for the rows without one
+  const int fill = p.cap / kFillRows < 256 ? p.cap / kFillRows : 256;
+  if (p.S > kRecount) {
+    if (!ws || !aligned(ws, 16)) return FG_EINVAL;
     int32_t* hist = static_cast<int32_t*>(ws);
-    hipLaunchKernelGGL(plan_count, dim3(chunks), dim3(kThreads), 0, stream, p.ids, hist, p.S, p.G);
+    p.chunks = chunks_of(p.S);
+    p.chunks_up4 = up4(p.chunks);
+    hipLaunchKernelGGL(plan_count, dim3(p.chunks), dim3(kThreads), 0, stream, p.ids, hist, p.S, p.G, p.chunks_up4);
     if (hipGetLastError() != hipSuccess) return FG_ELAUNCH;
     p.hist = hist;
-    hipLaunchKernelGGL((plan_place<kChunk / kThreads>), dim3(chunks), dim3(kThreads), lds, stream, p);
+    const int grid = fill > p.chunks ? fill : p.chunks;
+    hipLaunchKernelGGL((plan_place<kBatches>), dim3(grid), dim3(kThreads), lds, stream, p);
   } else {
-    p.hist = nullptr;
-    if (p.S <= kThreads) hipLaunchKernelGGL((plan_place<1>), dim3(1), dim3(kThreads), lds, stream, p);
-    else if (p.S <= 4 * kThreads) hipLaunchKernelGGL((plan_place<4>), dim3(1), dim3(kThreads), lds, stream, p);
-    else hipLaunchKernelGGL((plan_place<kOneBlock / kThreads>), dim3(1), dim3(kThreads), lds, stream, p);
+    const int chunks = (p.S + kThreads - 1) / kThreads, most = fill > chunks ? fill : chunks;
+    hipLaunchKernelGGL((plan_place<1>), dim3(most > 1 ? most : 1), dim3(kThreads), lds, stream, p);
   }
   return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
 }
@@ -253,7 +273,7 @@ int fg_plan_capacity(int T, int k, int G, int align, int* rows) {
 int fg_plan_workspace(int T, int k, int G, size_t* bytes) {
   if (!sizes_ok(T, k, G) || !bytes) return FG_EINVAL;
   const int S = T * k;
-  *bytes = S <= kOneBlock ? 0 : (size_t)chunks_of(S) * G * sizeof(int32_t);
+  *bytes = S <= kRecount ? 0 : (size_t)up4(chunks_of(S)) * G * sizeof(int32_t);
   return FG_OK;
 }
 

@@ -40,7 +40,11 @@ using namespace fg;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kThreads = 256;
-constexpr int kPackTokens = 2048;   // from here on four tokens share a wave
+// Tokens from which on four of at most 64 experts share a wave: with few tokens the
+// wave's longer chain shows, with many its fewer instructions (E 64, k 8, one token /
+// four a wave: T 1024 3.4 / 3.8, 4096 3.9 / 3.9, 16384 7.7 / 6.0 us; with 16 experts a
+// lane, E 256, four a wave lose at every T: 6.2 / 8.1 at 4096, 14.7 / 16.5 at 16384).
+constexpr int kPackTokens = 8192;
 
 // V consecutive elements of a row move in pieces of up to 16 bytes where V
 // divides E (a lane then has V experts or none, and pieces are aligned).
@@ -96,58 +100,86 @@ __device__ __forceinline__ void store_row(void* out, long row, int E, int e0, co
   }
 }
 
+// The largest of the group's logits (-inf if nothing is eligible).
+template <int L, int V>
+__device__ __forceinline__ float top_logit(const float* l) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+  const uint32_t u = group_max_u32<L>(order_key(m));
+  return __uint_as_float((u >> 31) ? (u & 0x7fffffffu) : ~u);
+}
+
+// A score before its division: exp(l - top) or the whole sigmoid; 0 for l = -inf.
+__device__ __forceinline__ float raw_score(float l, float top, int softmax) {
+  if (!(l > -INFINITY)) return 0.0f;
+  return softmax ? expf(l - top) : 1.0f / (1.0f + expf(-l));
+}
+
 // Scores of the lane's V logits.
 template <int L, int V>
 __device__ __forceinline__ void scores(const float* l, int softmax, float* s) {
+  const float top = softmax ? top_logit<L, V>(l) : 0.0f;
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    s[i] = raw_score(l[i], top, softmax);
+    sum += s[i];
+  }
   if (softmax) {
-    float m = l[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
-    const uint32_t u = group_max_u32<L>(order_key(m));
-    const float top = __uint_as_float((u >> 31) ? (u & 0x7fffffffu) : ~u);
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      s[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
-      sum += s[i];
-    }
     sum = group_sum<L>(sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = s[i] == 0.0f ? 0.0f : s[i] / sum;   // a row with nothing eligible has sum 0
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = l[i] > -INFINITY ? 1.0f / (1.0f + expf(-l[i])) : 0.0f;
   }
 }
 
-template <class R, int L, int V>
+// BIAS: the ranks are scores + bias, so every expert's score is worked out first.
+// Without one the logits are ranked, and only the chosen are divided (softmax) or
+// have a score at all (sigmoid).
+template <class R, int L, int V, bool BIAS>
 __global__ __launch_bounds__(kThreads) void route_topk(const void* __restrict__ logits,
                                                        const float* __restrict__ bias, int32_t* __restrict__ ids,
                                                        float* __restrict__ w, int T, int E, int k, int softmax,
                                                        int renorm, float scale) {
   __shared__ int32_t best_id[kThreads / L][kMaxTopK];
-  __shared__ float best_s[kThreads / L][kMaxTopK];
+  __shared__ float best_v[kThreads / L][kMaxTopK];   // the choice's score (BIAS) or logit
   const int group = threadIdx.x / L, lane = threadIdx.x % L;
   const long t = (long)blockIdx.x * (kThreads / L) + group;
   const long row = t < T ? t : T - 1L;   // groups past the last token repeat it and store nothing
-  float l[V], s[V], b[V];
+  float l[V], s[V];
   uint32_t key[V];
   load_logits<R, V>(logits, row, E, lane * V, l);
-  if (bias) {
+  float top = 0.0f, total = 1.0f;
+  if (BIAS) {
+    float b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) b[i] = bias[lane * V + i < E ? lane * V + i : E - 1];
-  }
-  scores<L, V>(l, softmax, s);
+    scores<L, V>(l, softmax, s);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float rank = bias && l[i] > -INFINITY ? s[i] + b[i] : l[i];
-    key[i] = rank > -INFINITY ? order_key(rank) : 0u;
+    for (int i = 0; i < V; ++i) {
+      const float rank = l[i] > -INFINITY ? s[i] + b[i] : l[i];
+      key[i] = rank > -INFINITY ? order_key(rank) : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s[i] = l[i];
+      key[i] = l[i] > -INFINITY ? order_key(l[i]) : 0u;
+    }
+    if (softmax) {
+      top = top_logit<L, V>(l);
+      if (!renorm) {   // renormalised, the sum over all experts cancels
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += raw_score(l[i], top, 1);
+        total = group_sum<L>(sum);
+      }
+    }
   }
   for (int j = lane; j < k; j += L) {
     best_id[group][j] = -1;
-    best_s[group][j] = 0.0f;
+    best_v[group][j] = BIAS ? 0.0f : -INFINITY;
   }
-  float sum = 0.0f;   // of this lane's chosen scores
   for (int j = 0; j < k; ++j) {
     uint32_t m = key[0];
 #pragma unroll
@@ -158,27 +190,42 @@ __global__ __launch_bounds__(kThreads) void route_topk(const void* __restrict__ 
     if (L == 16) same = (same >> (threadIdx.x & 48)) & 0xffffu;
     if (__builtin_ctzll(same | (1ull << 63)) == lane && best != 0u) {
       int at = 0;
-      float sc = 0.0f;
+      float v = 0.0f;
 #pragma unroll
       for (int i = V - 1; i >= 0; --i) {
         at = key[i] == best ? i : at;
-        sc = key[i] == best ? s[i] : sc;
+        v = key[i] == best ? s[i] : v;
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) key[i] = i == at ? 0u : key[i];
       best_id[group][j] = lane * V + at;
-      best_s[group][j] = sc;
-      sum += sc;
+      best_v[group][j] = v;
     }
+  }
+  // the group's own LDS writes, in order within its wave
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  constexpr int kEach = (kMaxTopK + L - 1) / L;   // choices per lane
+  float c[kEach], sum = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int j = lane + u * L;
+    c[u] = 0.0f;
+    if (j < k) {
+      const float v = best_v[group][j];
+      c[u] = BIAS ? v : raw_score(v, top, softmax);
+      if (!BIAS && softmax && !renorm) c[u] = c[u] == 0.0f ? 0.0f : c[u] / total;
+    }
+    sum += c[u];
   }
   if (renorm) sum = group_sum<L>(sum);
   if (t >= T) return;
-  // the group's own LDS writes, in order within its wave
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  for (int j = lane; j < k; j += L) {
-    const float c = best_s[group][j];
-    ids[t * k + j] = best_id[group][j];
-    w[t * k + j] = (renorm ? (sum > 0.0f ? c / sum : 0.0f) : c) * scale;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int j = lane + u * L;
+    if (j < k) {
+      ids[t * k + j] = best_id[group][j];
+      w[t * k + j] = (renorm ? (sum > 0.0f ? c[u] / sum : 0.0f) : c[u]) * scale;
+    }
   }
 }
 
@@ -254,25 +301,20 @@ void launch_v(bool grad, int T, hipStream_t s, const void* logits, const void* b
   const dim3 grid((unsigned)((T + kThreads / L - 1L) / (kThreads / L))), block(kThreads);
   if (grad)
     hipLaunchKernelGGL((route_topk_grad<R, L, V>), grid, block, 0, s, logits, (const int32_t*)b, (const float*)ids, w, T, a...);
+  else if (b)
+    hipLaunchKernelGGL((route_topk<R, L, V, true>), grid, block, 0, s, logits, (const float*)b, (int32_t*)ids, (float*)w, T, a...);
   else
-    hipLaunchKernelGGL((route_topk<R, L, V>), grid, block, 0, s, logits, (const float*)b, (int32_t*)ids, (float*)w, T, a...);
+    hipLaunchKernelGGL((route_topk<R, L, V, false>), grid, block, 0, s, logits, (const float*)b, (int32_t*)ids, (float*)w, T, a...);
 }
 
 template <class R, class... Args>
 void launch_e(int E, bool grad, int T, Args... a) {
-  if (T >= kPackTokens && E <= 256) {
-    if (E <= 16) launch_v<R, 16, 1>(grad, T, a...);
-    else if (E <= 32) launch_v<R, 16, 2>(grad, T, a...);
-    else if (E <= 64) launch_v<R, 16, 4>(grad, T, a...);
-    else if (E <= 128) launch_v<R, 16, 8>(grad, T, a...);
-    else launch_v<R, 16, 16>(grad, T, a...);
-  } else {
-    if (E <= 64) launch_v<R, 64, 1>(grad, T, a...);
-    else if (E <= 128) launch_v<R, 64, 2>(grad, T, a...);
-    else if (E <= 256) launch_v<R, 64, 4>(grad, T, a...);
-    else if (E <= 512) launch_v<R, 64, 8>(grad, T, a...);
-    else launch_v<R, 64, 16>(grad, T, a...);
-  }
+  if (T >= kPackTokens && E <= 64) launch_v<R, 16, 4>(grad, T, a...);
+  else if (E <= 64) launch_v<R, 64, 1>(grad, T, a...);
+  else if (E <= 128) launch_v<R, 64, 2>(grad, T, a...);
+  else if (E <= 256) launch_v<R, 64, 4>(grad, T, a...);
+  else if (E <= 512) launch_v<R, 64, 8>(grad, T, a...);
+  else launch_v<R, 64, 16>(grad, T, a...);
 }
 
 int route(bool grad, const void* logits, int dtype, const void* b, void* ids, void* w, int T, int E, int k,
