@@ -19,9 +19,10 @@
 // before its chunk and in the whole batch. Up to kRecount slots every workgroup
 // counts the batch itself (whole-number LDS atomics, a few microseconds at most),
 // which saves a launch; beyond, a first launch leaves each chunk's histogram in the
-// workspace. Both are bound by latency. In a graph, G 64, contiguous, the one launch
-// takes 5.4 / 6.1 / 6.7 / 8.3 us at 2048 / 8192 / 16384 / 32768 slots and the two
-// launches 8.8 / 11.3 / 11.9 us at the first three and 10.4 us at 131072.
+// workspace. Both are bound by latency: 131072 slots are 2 MB of ids, rows, slots and
+// experts, under a microsecond of traffic. In a graph, G 64, contiguous, the one launch
+// takes 5.2 / 5.8 / 7.0 / 9.5 us at 2048 / 8192 / 16384 / 32768 slots, two launches
+// 8.6 / 9.0 / 9.5 / 9.6 us; at 131072 it is 24.9 against 10.4 us.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
