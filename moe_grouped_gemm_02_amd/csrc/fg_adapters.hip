@@ -473,6 +473,7 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
   // store is skipped: lanes without an output write to spare memory. (Loads two rounds
   // ahead, with a third buffer, were slower: 47 against 38-46 us.)
   wait_vm<0>();
+  __builtin_amdgcn_s_waitcnt(0x0f70);
   const auto round = [&](auto which, int r) {
     constexpr int B = decltype(which)::value;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the other buffer's reads are done
@@ -503,6 +504,9 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
     }
     __builtin_amdgcn_sched_barrier(0);
     wait_vm<NG>();
+    // The same wait in the compiler's own terms. It does not see the loads into LDS, so
+    // its waits for d would take them for older operations and wait for the next round's.
+    __builtin_amdgcn_s_waitcnt(0x0f70 | NG);
   };
   const int rounds = (n_hi - n_lo + kCols - 1) / kCols;
   for (int r = 0; r < rounds; r += 2) {
