@@ -32,7 +32,7 @@ UNITS = [("fg_host", "fg_host.hip", []), ("fg_host_testing", "fg_host.hip", ["-D
          ("fg_quant", "fg_quant.hip", []), ("fg_route", "fg_route.hip", []), ("fg_plan", "fg_plan.hip", []),
          ("fg_rows", "fg_rows.hip", []), ("fg_adapters", "fg_adapters.hip", []), ("fg_ceiling", "fg_ceiling.hip", [])] + [
     (f"fg_launch_{i}", "fg_launch.hip", [f"-DFG_LAUNCH_PART={i}"]) for i in range(LAUNCH_PARTS)]
-HEADERS = ["fg_kernel.hpp", "fg_e4m3.hpp", "fg_tiles.hpp", "fg_device.hpp", "fg_wave.hpp"]
+HEADERS = ["fg_kernel.hpp", "fg_e4m3.hpp", "fg_e4m3_quot.hpp", "fg_tiles.hpp", "fg_device.hpp", "fg_wave.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -22,7 +22,7 @@
 
 #include "fg.h"
 #include "fg_device.hpp"
-#include "fg_e4m3.hpp"
+#include "fg_e4m3_quot.hpp"
 #include "fg_wave.hpp"
 
 namespace {

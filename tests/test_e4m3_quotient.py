@@ -1,4 +1,4 @@
-"""The quotient step of the row operators' E4M3 encoder (fg_e4m3.hpp, e4m3x4_quot):
+"""The quotient step of the row operators' E4M3 encoder (fg_e4m3_quot.hpp):
 q = x * inv, then one correction by the exact residual. It can leave the correctly
 rounded quotient only where x / s lies within 2^-23 ulp of the middle of two floats,
 and the code can then change only if one of the two is a boundary between E4M3 codes
