@@ -9,21 +9,27 @@
 // matrix cores.
 //
 // Two launches, because every output column needs the whole sum over K:
-//   shrink  h = x A^T. A workgroup takes one tile of rows and one part of K, its
-//           four waves a quarter of that part each; v_mfma_f32_16x16x32_bf16 on
-//           fragments loaded straight from global memory (nothing is used twice
-//           within a wave, so LDS would add only a copy). The waves' sums meet in
-//           LDS, the parts' in the workspace, both added in a fixed order.
+//   shrink  h = x A^T. A workgroup takes one tile of rows and one part of K; the
+//           parts' sums meet in the workspace and are added in a fixed order.
 //   expand  out = D + h B^T. A workgroup takes one tile of rows and a strip of
 //           columns; h is summed over the parts, scaled, and split into two bf16
 //           (h = hi + lo to 2^-17) so that rounding it costs nothing visible:
-//           the work is bound by the rows of D, not by the matrix cores. For
-//           R <= 16 both halves fit one 32-deep MFMA, hi against k 0..15 and lo
-//           against k 16..31 with B's fragment repeated.
+//           the work is bound by moving D, not by the matrix cores. For R <= 16 both
+//           halves fit one 32-deep MFMA, hi against k 0..15 and lo against k 16..31
+//           with B's fragment repeated.
+// Each has a kernel for 16-row tiles (decode), where A and B are read once and go
+// straight into fragments, and one for 64-row tiles (prompts), where four waves share
+// them through LDS.
 //
-// K order in a fragment: both operands of an MFMA may take their 32 k values in
-// any common order; lane quarter q takes the 16 consecutive values at 16 q of a
-// 64-wide step over two MFMAs, so a row's 64 values are one 128-byte line.
+// Floors and times. T 8192, L 8, R 64, K 7168, N 4096 moves 257 MB: 49 us at the 5.25
+// TB/s of a large copy; shrink takes 27 us (37 where 124 or more tiles are in use: some
+// compute units then hold three of its workgroups, and at about 25 bytes a clock their
+// loads into LDS are the limit), expand 37. 64 tokens of 64 adapters, R 16: 15 MB and
+// two launches, 6.0 and 6.2 us, mostly latency: plan, rows, operands one after another.
+//
+// K order in a fragment: both operands of an MFMA may take their 32 k values in any
+// common order. With 16-row tiles lane quarter q takes the 16 consecutive values at
+// 16 q of a 64-wide step over two MFMAs, so a row's 64 values are one 128-byte line.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -397,7 +403,12 @@ __global__ __launch_bounds__(kThreads) void adapter_expand16(AdapterArgs p) {
 // rows per instruction) its loads took 22 us of 55 at T = 8192, N = 4096, R = 64.
 // A row's 16-byte chunk c sits at c ^ key(n) where the chunks per row are a power of
 // two, key(n) spreading the rows that eight neighbouring lanes read over the banks.
-constexpr int kCols = 128;
+//
+// The products leave the matrix cores with 16 rows to an instruction; they turn round
+// in LDS, 64 columns at a time, so that each load of D and store of out covers whole
+// 128-byte lines of eight rows. Straight from the registers, 64-byte halves of 16 rows,
+// the kernel took 38 or 46 us by the relative placing of D and out; so 37 us for either.
+constexpr int kCols = 128, kHalf = 64;
 
 __device__ __forceinline__ int swizzle_key(int n, int chunks) {
   return (chunks & (chunks - 1)) ? 0 : ((n & 3) | ((n >> 1) & 4)) & (chunks - 1);
@@ -409,6 +420,7 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
   using H = HFrags<TR>;
   constexpr int NI = TR;                       // loads per wave and buffer: 128 columns x 2 TR chunks / 256
   __shared__ __attribute__((aligned(128))) uint8_t ring[2][NI * kThreads * 16];
+  __shared__ float turn[kWaves][16][kHalf + 4];
   if ((int)blockIdx.x < p.copies) return copy_tokens(p, blockIdx.x);
   const int job = blockIdx.x - p.copies, strip = job / p.tiles_up8;
   const int tile = tile_of(p, job - strip * p.tiles_up8, 64), r0 = tile * 64;
@@ -444,10 +456,20 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
     }
   };
   issue(0, n_lo);
-  const int tok = p.slots[r0 + 16 * wave + lrow];
-  const bool real = (unsigned)tok < (unsigned)p.T;
-  const uint16_t* drow = p.D + (long)(real ? tok : 0) * p.N;
-  uint16_t* orow = p.out + (long)(real ? tok : 0) * p.N;
+  const bool real = (unsigned)p.slots[r0 + 16 * wave + lrow] < (unsigned)p.T;
+  // the two rows of D and out that this lane moves (8 i + lane / 8 of the wave's 16), at its
+  // eight columns of a half round
+  const uint16_t* drow[2];
+  uint16_t* orow[2];
+  bool has[2];
+  const int dcol = 8 * (lane & 7);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int tok = p.slots[r0 + 16 * wave + 8 * i + (lane >> 3)];
+    has[i] = (unsigned)tok < (unsigned)p.T;
+    drow[i] = p.D + (long)(has[i] ? tok : 0) * p.N + dcol;
+    orow[i] = p.out + (long)(has[i] ? tok : 0) * p.N + dcol;
+  }
   uint16_t* spare = p.spare + 8 * lane;
   H h;
   load_h<TR>(p, r0 + 16 * wave + lrow, real, p.scales[a], q, h);
@@ -462,8 +484,8 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
   const auto load_d = [&](u32x4* v, int n0) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const int col = n0 + 32 * g + 8 * q;
-      v[g] = *(const u32x4*)(drow + (col < n_hi ? col : n_lo));
+      const int at = n0 + kHalf * (g >> 1);
+      v[g] = *(const u32x4*)(drow[g & 1] + (at + dcol < n_hi ? at : n_lo - dcol));   // outside: the strip's first
     }
   };
   load_d(d[0], n_lo);
@@ -471,7 +493,7 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
   // count down in order, so a wait for a load also waits for every store before it; at
   // a round's end only its own stores stay under way. For the count to be exact no
   // store is skipped: lanes without an output write to spare memory. (Loads two rounds
-  // ahead, with a third buffer, were slower: 47 against 38-46 us.)
+  // ahead, with a third buffer, were slower: 47 against 42 us.)
   wait_vm<0>();
   __builtin_amdgcn_s_waitcnt(0x0f70);
   const auto round = [&](auto which, int r) {
@@ -486,7 +508,7 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       f32x4v acc[2];
-      start_pair(d[B][g], acc);
+      acc[0] = acc[1] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int f = 0; f < H::KF; ++f) {
 #pragma unroll
@@ -499,8 +521,23 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
           for (int l = H::HL - 1; l >= 0; --l) acc[e] = mfma(b, h.f[l][f], acc[e]);
         }
       }
-      const int col = n0 + 32 * g + 8 * q;
-      *(u32x4*)(real && col < n_hi ? orow + col : spare) = end_pair(acc);
+      float* to = &turn[wave][lrow][32 * (g & 1) + 8 * q];
+      *(f32x4v*)to = acc[0];
+      *(f32x4v*)(to + 4) = acc[1];
+      if (g & 1) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the wave's own LDS accesses, in order
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float* from = &turn[wave][8 * i + (lane >> 3)][dcol];
+          f32x4v sum[2];
+          start_pair(d[B][g - 1 + i], sum);
+          sum[0] += *(const f32x4v*)from;
+          sum[1] += *(const f32x4v*)(from + 4);
+          const int at = n0 + kHalf * (g >> 1);
+          *(u32x4*)(has[i] && at + dcol < n_hi ? orow[i] + at : spare) = end_pair(sum);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     wait_vm<NG>();
@@ -604,8 +641,8 @@ int fg_adapters(const void* D, const void* x, const void* A, const void* B, cons
   p.parts = k_parts(p.tiles, rt, K);
   p.copies = out != D ? (int)((T + 127L) / 128 * 8) : 0;
   // columns of an expand workgroup: long strips load h less often, short ones fill the
-  // chip (64-row tiles, T 8192, N 4096: 256 / 512 / 1024 / 2048 / 4096 columns take 47 /
-  // 40 / 38-45 / 39 / 56 us)
+  // chip (64-row tiles, T 8192, N 4096: 512 / 1024 / 2048 columns take 40 / 37 / 37 us;
+  // 16-row tiles, 64 tokens of 64 adapters: 512 / 1024 / 2048 workgroups 6.7 / 6.2 / 7.8 us)
   p.strip = 1024;
   while (p.strip > 128 && (long)p.tiles * ((N + p.strip - 1) / p.strip) < (rt == 64 ? 512 : 1024)) p.strip /= 2;
   if ((long)p.copies + (long)p.tiles_up8 * ((N + p.strip - 1) / p.strip) > 0x7fffffffL) return FG_EINVAL;
