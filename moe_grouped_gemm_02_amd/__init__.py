@@ -119,15 +119,26 @@ def _torch():
 _raw_stream = None
 
 
+_current_device = None
+
+
 def _stream(t):
     """The current HIP stream of t's device as an address. torch's raw getter takes 0.1 us;
     a Stream object, where a torch has no such getter, 1.9 us, a third of a small call."""
-    global _raw_stream
     if _raw_stream is None:
-        torch = _torch()
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _getters()
     return _raw_stream(t.device.index)
+
+
+def _getters():
+    """torch's raw getters of the current stream and device (its public ones where it has
+    no such), set once CUDA is initialised by the first tensor on a device."""
+    global _raw_stream, _current_device
+    torch = _torch()
+    lib()
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, dev, *args):
@@ -135,8 +146,8 @@ def _call(fn, dev, *args):
     launches on the current device, on the stream passed last) and raises
     FGError on a nonzero return code."""
     torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        code = getattr(_lib or lib(), fn)(*args)
+    if _current_device is not None and _current_device() == dev.index:
+        code = getattr(_lib, fn)(*args)
     else:
         with torch.cuda.device(dev):
             code = getattr(lib(), fn)(*args)
@@ -514,37 +525,35 @@ class Plan:
 
     @classmethod
     def contiguous(cls, rows, slots, m_indices, offsets, align):
-        _plan_rows(rows, slots)
-        _index(m_indices, "m_indices", rows.device, slots.shape[0])
-        _index(offsets, "offsets", rows.device)
-        if align < 1 or slots.shape[0] % align or offsets.shape[0] < 2:
+        cap, G = _plan_rows(rows, slots), offsets.shape[0] - 1
+        _index(m_indices, "m_indices", rows.device, cap)
+        _index(offsets, "offsets", rows.device, G + 1)
+        if align < 1 or cap % align or G < 1:
             raise ValueError("a contiguous plan has G + 1 >= 2 offsets and a multiple of align rows")
-        return cls(LAYOUT_CONTIGUOUS, rows, slots, m_indices, offsets, align, None, 0, offsets.shape[0] - 1)
+        return cls(LAYOUT_CONTIGUOUS, rows, slots, m_indices, offsets, align, None, 0, G)
 
     @classmethod
     def masked(cls, rows, slots, masked_m, M_max):
-        _plan_rows(rows, slots)
-        _index(masked_m, "masked_m", rows.device)
-        G = masked_m.shape[0]
-        if slots.shape[0] != G * M_max or M_max < 1 or G < 1:
+        cap, G = _plan_rows(rows, slots), masked_m.shape[0]
+        _index(masked_m, "masked_m", rows.device, G)
+        if cap != G * M_max or M_max < 1 or G < 1:
             raise ValueError("a masked plan has G * M_max slots")
         return cls(LAYOUT_MASKED, rows, slots, None, None, 1, masked_m, M_max, G)
 
 
-def _index(t, name, device, n=None):
-    """Checks an int32 vector (of n entries if given) on `device`."""
-    shape = t.shape
-    if (len(shape) == 1 and t.dtype is _torch().int32 and t.device == device and t.is_contiguous()
-            and (n is None or shape[0] == n)):
-        return
-    _dev(t, name, (t.numel() if n is None else n,), _torch().int32, device)
+def _index(t, name, device, n):
+    """Checks an int32 vector of n entries on `device`."""
+    if t.dtype is not _torch().int32 or t.device != device or t.shape != (n,) or not t.is_contiguous():
+        _dev(t, name, (n,), _torch().int32, device)
 
 
 def _plan_rows(rows, slots):
     if rows.dim() != 2 or slots.dim() != 1:
         raise ValueError("rows must be [T, k] and slots [rows]")
     _dev(rows, "rows", rows.shape, _torch().int32)
-    _index(slots, "slots", rows.device)
+    cap = slots.shape[0]
+    _index(slots, "slots", rows.device, cap)
+    return cap
 
 
 def _plan_args(ids, G):
