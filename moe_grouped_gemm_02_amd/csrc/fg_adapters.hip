@@ -59,6 +59,7 @@ struct AdapterArgs {
   int T, L, R, K, N, cap;
   int parts;              // parts of K
   int strip;              // columns of one expand workgroup
+  bool stream;            // out is larger than the caches
   int tiles, tiles_up8;   // row tiles, and their number rounded up to 8
   int copies;             // workgroups of expand that pass tokens through (a multiple of 8)
 };
@@ -307,6 +308,7 @@ __device__ __forceinline__ void load_h(const AdapterArgs& p, int row, bool real,
 // Tokens without an adapter pass through: workgroup `block` of the launch's first
 // p.copies takes 16 tokens, each wave four, all its loads under way before the
 // first store.
+template <bool STREAM>
 __device__ __forceinline__ void copy_tokens(const AdapterArgs& p, int block) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const long t0 = ((long)block * kWaves + wave) * 4;
@@ -324,7 +326,7 @@ __device__ __forceinline__ void copy_tokens(const AdapterArgs& p, int block) {
     for (int i = 0; i < 4; ++i) v[i] = *(const u32x4*)(p.D + tok[i] * p.N + n);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (pass[i]) *(u32x4*)(p.out + tok[i] * p.N + n) = v[i];
+      if (pass[i]) store16<STREAM>((u32x4*)(p.out + tok[i] * p.N + n), v[i]);
   }
 }
 
@@ -353,7 +355,7 @@ __device__ __forceinline__ u32x4 end_pair(const f32x4v* acc) {
 template <int TR>
 __global__ __launch_bounds__(kThreads) void adapter_expand16(AdapterArgs p) {
   using H = HFrags<TR>;
-  if ((int)blockIdx.x < p.copies) return copy_tokens(p, blockIdx.x);
+  if ((int)blockIdx.x < p.copies) return copy_tokens<false>(p, blockIdx.x);
   const int job = blockIdx.x - p.copies, strip = job / p.tiles_up8;
   const int tile = tile_of(p, job - strip * p.tiles_up8, 16), r0 = tile * 16;
   if (tile < 0) return;
@@ -414,14 +416,15 @@ __device__ __forceinline__ int swizzle_key(int n, int chunks) {
   return (chunks & (chunks - 1)) ? 0 : ((n & 3) | ((n >> 1) & 4)) & (chunks - 1);
 }
 
-// FULL: R is 16 TR, every fragment is of ranks below R.
-template <int TR, bool FULL>
+// FULL: R is 16 TR, every fragment is of ranks below R. STREAM: out is larger than
+// the caches.
+template <int TR, bool FULL, bool STREAM>
 __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
   using H = HFrags<TR>;
   constexpr int NI = TR;                       // loads per wave and buffer: 128 columns x 2 TR chunks / 256
   __shared__ __attribute__((aligned(128))) uint8_t ring[2][NI * kThreads * 16];
   __shared__ float turn[kWaves][16][kHalf + 4];
-  if ((int)blockIdx.x < p.copies) return copy_tokens(p, blockIdx.x);
+  if ((int)blockIdx.x < p.copies) return copy_tokens<STREAM>(p, blockIdx.x);
   const int job = blockIdx.x - p.copies, strip = job / p.tiles_up8;
   const int tile = tile_of(p, job - strip * p.tiles_up8, 64), r0 = tile * 64;
   if (tile < 0) return;
@@ -534,7 +537,7 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
           sum[0] += *(const f32x4v*)from;
           sum[1] += *(const f32x4v*)(from + 4);
           const int at = n0 + kHalf * (g >> 1);
-          *(u32x4*)(has[i] && at + dcol < n_hi ? orow[i] + at : spare) = end_pair(sum);
+          store16<STREAM>((u32x4*)(has[i] && at + dcol < n_hi ? orow[i] + at : spare), end_pair(sum));
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
@@ -585,8 +588,11 @@ void launch(const AdapterArgs& p, bool wide, hipStream_t s) {
   const dim3 g1(p.tiles_up8, p.parts), g2(p.copies + p.tiles_up8 * ((p.N + p.strip - 1) / p.strip)), b(kThreads);
   if (wide) {
     hipLaunchKernelGGL(adapter_shrink64<TR>, g1, b, 0, s, p);
-    if (p.R == 16 * TR) hipLaunchKernelGGL((adapter_expand64<TR, true>), g2, b, 0, s, p);
-    else hipLaunchKernelGGL((adapter_expand64<TR, false>), g2, b, 0, s, p);
+    const bool full = p.R == 16 * TR;
+    if (full && p.stream) hipLaunchKernelGGL((adapter_expand64<TR, true, true>), g2, b, 0, s, p);
+    else if (full) hipLaunchKernelGGL((adapter_expand64<TR, true, false>), g2, b, 0, s, p);
+    else if (p.stream) hipLaunchKernelGGL((adapter_expand64<TR, false, true>), g2, b, 0, s, p);
+    else hipLaunchKernelGGL((adapter_expand64<TR, false, false>), g2, b, 0, s, p);
   } else {
     hipLaunchKernelGGL(adapter_shrink16<TR>, g1, b, 0, s, p);
     hipLaunchKernelGGL(adapter_expand16<TR>, g2, b, 0, s, p);
@@ -639,6 +645,7 @@ int fg_adapters(const void* D, const void* x, const void* A, const void* B, cons
   p.tiles = cap / rt;
   p.tiles_up8 = (p.tiles + 7) / 8 * 8;
   p.parts = k_parts(p.tiles, rt, K);
+  p.stream = (long long)T * N * 2 > kStreamBytes;
   p.copies = out != D ? (int)((T + 127L) / 128 * 8) : 0;
   // columns of an expand workgroup: long strips load h less often, short ones fill the
   // chip (64-row tiles, T 8192, N 4096: 512 / 1024 / 2048 columns take 40 / 37 / 37 us;

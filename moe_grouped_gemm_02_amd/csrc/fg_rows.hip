@@ -83,12 +83,15 @@ __device__ __forceinline__ void store_unit(const QuantOut& o, int row, int i, u3
 
 // Token and unit of this lane when a token has `per` units, lanes taken in order.
 __device__ __forceinline__ bool unit_of(int per, int T, long* t, int* i) {
-  const long b0 = (long)blockIdx.x * kThreads;
-  const long t0 = b0 / per;                       // uniform
-  const unsigned v = (unsigned)(b0 - t0 * per) + threadIdx.x;
-  const unsigned q = v / (unsigned)per;
-  *t = t0 + q;
-  *i = (int)(v - q * (unsigned)per);
+  if (gridDim.x < (1u << 23)) {   // below 2^31 units 32 bits do: a 64-bit division is half of combine's instructions
+    const unsigned v = blockIdx.x * kThreads + threadIdx.x, q = v / (unsigned)per;
+    *t = q;
+    *i = (int)(v - q * (unsigned)per);
+  } else {
+    const long v = (long)blockIdx.x * kThreads + threadIdx.x;
+    *t = v / per;
+    *i = (int)(v - *t * per);
+  }
   return *t < T;
 }
 
@@ -159,10 +162,11 @@ __global__ __launch_bounds__(kDispatchThreads) void dispatch_quant(const void* _
   }
 }
 
-template <class R, bool W>
+// STREAM: out is larger than the caches.
+template <class R, bool W, bool STREAM>
 __global__ __launch_bounds__(kThreads) void combine(const void* __restrict__ y, const int32_t* __restrict__ rows,
-                                                    const float* __restrict__ w, const void* __restrict__ base,
-                                                    void* __restrict__ out, int T, int k, int N, int n_rows) {
+                                                    const float* __restrict__ w, const void* base,
+                                                    void* out, int T, int k, int N, int n_rows) {
   long t;
   int i;
   const int per = N / R::kPer16;
@@ -204,7 +208,7 @@ __global__ __launch_bounds__(kThreads) void combine(const void* __restrict__ y, 
 #pragma unroll
     for (int e = 0; e < R::kPer16; ++e) acc[e] += f[e];
   }
-  ((u32x4*)out)[t * per + i] = R::pack(acc);
+  store16<STREAM>(&((u32x4*)out)[t * per + i], R::pack(acc));
 }
 
 // One workgroup per token: its row of dout stays in registers for a unit at a
@@ -344,6 +348,15 @@ void launch_dispatch(bool pow2, hipStream_t s, const void* x, const int32_t* row
   else hipLaunchKernelGGL((dispatch_quant<R, false, false>), g, b, 0, s, x, rows, w, o, T, k, strips);
 }
 
+template <class R, class... Args>
+void launch_combine(bool weighted, bool big, dim3 g, hipStream_t s, Args... a) {
+  const dim3 b(kThreads);
+  if (weighted && big) hipLaunchKernelGGL((combine<R, true, true>), g, b, 0, s, a...);
+  else if (weighted) hipLaunchKernelGGL((combine<R, true, false>), g, b, 0, s, a...);
+  else if (big) hipLaunchKernelGGL((combine<R, false, true>), g, b, 0, s, a...);
+  else hipLaunchKernelGGL((combine<R, false, false>), g, b, 0, s, a...);
+}
+
 int launched() { return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH; }
 
 }  // namespace
@@ -378,11 +391,10 @@ int fg_combine(const void* y, int dtype, const int32_t* rows, const float* w, co
   if (grid == 0) return FG_EINVAL;
   const int st = current_device(nullptr);
   if (st != FG_OK) return st;
-  const dim3 g(grid), b(kThreads);
-  if (dtype == FG_BF16 && w) hipLaunchKernelGGL((combine<RowBf16, true>), g, b, 0, stream, y, rows, w, base, out, T, k, N, n_rows);
-  else if (dtype == FG_BF16) hipLaunchKernelGGL((combine<RowBf16, false>), g, b, 0, stream, y, rows, w, base, out, T, k, N, n_rows);
-  else if (w) hipLaunchKernelGGL((combine<RowF32, true>), g, b, 0, stream, y, rows, w, base, out, T, k, N, n_rows);
-  else hipLaunchKernelGGL((combine<RowF32, false>), g, b, 0, stream, y, rows, w, base, out, T, k, N, n_rows);
+  const dim3 g(grid);
+  const bool big = (long long)T * N * (dtype == FG_BF16 ? 2 : 4) > kStreamBytes;
+  if (dtype == FG_BF16) launch_combine<RowBf16>(w != nullptr, big, g, stream, y, rows, w, base, out, T, k, N, n_rows);
+  else launch_combine<RowF32>(w != nullptr, big, g, stream, y, rows, w, base, out, T, k, N, n_rows);
   return launched();
 }
 
