@@ -321,7 +321,7 @@ bool type_ok(int dtype) { return dtype == FG_BF16 || dtype == FG_FP32; }
 
 // Sizes of the E4M3 rows: G x M of them, H columns.
 int check_quant(int dtype, int T, int k, int H, int G, int M, int scales) {
-  if (T < 0 || k < 1 || H < 128 || H % 128 || H > (1 << 24) || G < 1 || M < 1 || !type_ok(dtype)) return FG_EINVAL;
+  if (T < 0 || k < 1 || H < 128 || H % 128 || H > (1 << 24) || G < 1 || M < (T > 0 ? 1 : 0) || !type_ok(dtype)) return FG_EINVAL;
   if ((scales != FG_SCALES_FP32 && scales != FG_SCALES_POW2) || (long long)G * M > 0x7fffffffLL) return FG_EINVAL;
   return FG_OK;
 }

@@ -565,3 +565,22 @@ def test_dispatch_quant_extreme_blocks(H, pow2):
         codes, scales = oracle.quantize_act_1x128(v, pow2)
         assert np.array_equal(host(sa).T[real], scales[real])
         assert np.array_equal(host(Q)[real], codes[real])
+
+
+@pytest.mark.parametrize("layout", ["contiguous", "masked"])
+def test_no_tokens_anywhere(layout):
+    """An empty batch goes through every call and comes out empty."""
+    ids, w = fg.route_topk(torch.empty(0, 8, device=dev()), 2)
+    p = fg.plan_contiguous(ids, 8) if layout == "contiguous" else fg.plan_masked(ids, 8, 4)
+    x = torch.empty(0, 256, dtype=torch.bfloat16, device=dev())
+    Q, sa = fg.dispatch_quant(x, p)
+    assert Q.shape == p.lead + (256,) and sa.shape[-1] == p.lead[-1]
+    y = torch.zeros(p.lead + (256,), dtype=torch.bfloat16, device=dev())
+    assert fg.combine(y, p, w=w).shape == (0, 256) and fg.dispatch_grad(y, p).shape == (0, 256)
+    _, dw = fg.combine_grad(x, y, p, w)
+    assert dw.shape == (0, 2)
+    assert fg.combine_grad_quant(x, y, p, w)[2].shape == (0, 2)
+    low = fg.plan_contiguous(torch.empty(0, 1, dtype=torch.int32, device=dev()), 3, align=64)
+    A, B = (torch.zeros(s, dtype=torch.bfloat16, device=dev()) for s in ((3, 16, 256), (3, 64, 16)))
+    D = torch.empty(0, 64, dtype=torch.bfloat16, device=dev())
+    assert fg.adapters(D, x, A, B, torch.ones(3, device=dev()), low).shape == (0, 64)
