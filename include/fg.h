@@ -365,7 +365,7 @@ int fg_combine_grad_quant(const void* dout, const void* y, int dtype, const int3
  *   B [L][N][R] bf16, scales [L] fp32; rows, slots, m_indices, offsets: the contiguous
  *   plan of the tokens' adapter ids (k = 1, G = L), cap its rows and align its
  *   alignment, a multiple of 16. A tile has 64 rows if 64 divides align, else
- *   16: 64 suits prompts (many tokens per adapter), 16 decode.
+ *   16: 64 pays from about 32 tokens per adapter on.
  *   R % 8 == 0, 8 <= R <= 128 (smaller adapters are padded with zeros);
  *   K % 128 == 0, N % 8 == 0; tensors 16-byte aligned.
  *   ws: fg_adapters_workspace bytes, 16-byte aligned.

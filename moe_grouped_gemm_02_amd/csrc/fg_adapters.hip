@@ -24,8 +24,11 @@
 // Floors and times. T 8192, L 8, R 64, K 7168, N 4096 moves 257 MB: 49 us at the 5.25
 // TB/s of a large copy; shrink takes 27 us (37 where 124 or more tiles are in use: some
 // compute units then hold three of its workgroups, and at about 25 bytes a clock their
-// loads into LDS are the limit), expand 37. 64 tokens of 64 adapters, R 16: 15 MB and
-// two launches, 6.0 and 6.2 us, mostly latency: plan, rows, operands one after another.
+// loads into LDS are the limit), expand 37-39. 64 tokens of 64 adapters, R 16: 15 MB and
+// two launches, 6 us each, mostly latency: plan, rows, operands one after another.
+// 16- against 64-row tiles, both launches: R 16, L 8, T 128 / 256 / 1024: 9.7 / 11.0 /
+// 17.1 against 10.6 / 10.7 / 14.4 us; L 64, T 1024 / 2048 19.5 / 25.8 against 21.3 / 21.6:
+// 64 pays from about 32 tokens an adapter on.
 //
 // K order in a fragment: both operands of an MFMA may take their 32 k values in any
 // common order. With 16-row tiles lane quarter q takes the 16 consecutive values at
@@ -274,25 +277,46 @@ struct HFrags {
   static constexpr int HL = TR == 1 ? 1 : 2;        // hi (and lo)
   u32x4 f[HL][KF];
 };
+// `first`: the tile's first row, read in the place of rows without a token.
 template <int TR>
-__device__ __forceinline__ void load_h(const AdapterArgs& p, int row, bool real, float scale, int q, HFrags<TR>& h) {
-  constexpr int RC = 16 * TR;
+__device__ __forceinline__ void load_h(const AdapterArgs& p, int row, int first, bool real, float scale, int q,
+                                       HFrags<TR>& h) {
+  constexpr int RC = 16 * TR, KF = HFrags<TR>::KF;
+  constexpr int kTogether = KF > 2 ? 2 : 4;   // parts whose loads are under way together
+  f32x4v v[KF][2];
 #pragma unroll
-  for (int k = 0; k < HFrags<TR>::KF; ++k) {
-    const int r = TR == 1 ? 8 * (q & 1) : 32 * k + 8 * q;
-    f32x4v v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    const float* src = p.ws + (long)row * RC + r;   // inside the workspace whether or not it was written
-#pragma unroll 4
-    for (int c = 0; c < p.parts; ++c) {
-      v[0] += *(const f32x4v*)src;
-      v[1] += *(const f32x4v*)(src + 4);
-      src += (long)p.cap * RC;
+  for (int k = 0; k < KF; ++k) v[k][0] = v[k][1] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  const float* src = p.ws + (long)(real ? row : first) * RC + (TR == 1 ? 8 * (q & 1) : 8 * q);
+  const long stride = (long)p.cap * RC;
+  for (int c = 0; c < p.parts; c += kTogether) {
+    f32x4v u[kTogether][KF][2];
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i) {
+      const float* part = src + stride * (c + i < p.parts ? c + i : c);
+#pragma unroll
+      for (int k = 0; k < KF; ++k) {
+        u[i][k][0] = *(const f32x4v*)(part + 32 * k);
+        u[i][k][1] = *(const f32x4v*)(part + 32 * k + 4);
+      }
     }
-    if (!real || r >= p.R) v[0] = v[1] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i) {
+      if (c + i < p.parts) {   // uniform
+#pragma unroll
+        for (int k = 0; k < KF; ++k) {
+          v[k][0] += u[i][k][0];
+          v[k][1] += u[i][k][1];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < KF; ++k) {
+    if (!real || (TR == 1 ? 8 * (q & 1) : 32 * k + 8 * q) >= p.R) v[k][0] = v[k][1] = f32x4v{0.f, 0.f, 0.f, 0.f};
     u32x4 hi, lo;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float x = v[e >> 1][2 * (e & 1)] * scale, y = v[e >> 1][2 * (e & 1) + 1] * scale;
+      const float x = v[k][e >> 1][2 * (e & 1)] * scale, y = v[k][e >> 1][2 * (e & 1) + 1] * scale;
       hi[e] = bf16_pair(x, y);
       lo[e] = bf16_pair(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
     }
@@ -369,7 +393,7 @@ __global__ __launch_bounds__(kThreads) void adapter_expand16(AdapterArgs p) {
   const int first = p.slots[r0];
   const uint16_t* drow = p.D + (long)(real ? tok : (unsigned)first < (unsigned)p.T ? first : 0) * p.N;
   H h;
-  load_h<TR>(p, r0 + lrow, real, p.scales[a], q, h);
+  load_h<TR>(p, r0 + lrow, r0, real, p.scales[a], q, h);
   const uint16_t* Ba = p.B + (long)a * p.N * p.R;
   for (int n0 = n_lo + 32 * wave; n0 < n_hi; n0 += 32 * kWaves) {
     u32x4 bf[2][H::KF];
@@ -475,7 +499,7 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
   }
   uint16_t* spare = p.spare + 8 * lane;
   H h;
-  load_h<TR>(p, r0 + 16 * wave + lrow, real, p.scales[a], q, h);
+  load_h<TR>(p, r0 + 16 * wave + lrow, r0, real, p.scales[a], q, h);
   constexpr int NG = kCols / 32;
   int cc[H::KF];   // this lane's chunk of a row of B in each fragment
 #pragma unroll
@@ -563,16 +587,18 @@ int rank_groups(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 int tile_rows(int align) { return align % 64 == 0 ? 64 : 16; }
 
 // Parts of K: enough workgroups to fill the chip, at least one step of K a wave.
-// Every part is one more partial h for each expand workgroup to read: with 16-row
-// tiles, 64 tokens of 64 adapters (K 7168, N 4096, R 16), 2 / 4 / 8 parts take 8.6 /
-// 5.8 / 5.6 us in shrink and 5.6 / 6.2 / 8.3 us in expand, so those stop at 256
-// workgroups. With 64-row tiles (T 8192, L 8, R 64) 2, 4 and 8 parts take 27.9, 27.4
-// and 34 us in shrink.
-int k_parts(int tiles, int rt, int K) {
+// Every part is one more partial h, rows x rank, for each expand workgroup to read.
+// 16-row tiles, 64 tokens of 64 adapters (K 7168, N 4096, R 16): 2 / 4 / 8 parts take
+// 8.6 / 5.8 / 5.6 us in shrink and 5.6 / 6.2 / 8.3 us in expand, so those stop at 256
+// workgroups. Both launches in a graph, at most 4 / 8 / 16 parts: one token, R 16, 7.3 /
+// 6.9 / 7.5 us; one token, R 64, 12.4 / 10.0 / 9.9; 64-row tiles, T 1024 of 8 adapters, R
+// 16, 15.1 / 13.5 / 15.0; R 64, 21.8 / 24.2 / 35.3 us.
+int k_parts(int tiles, int rt, int K, int R) {
   const int most = K / (kStepK * kWaves) > 1 ? K / (kStepK * kWaves) : 1;
+  const int limit = rt == 64 && R > 32 ? 4 : 8;
   const long fill = rt == 64 ? 512 : 256;
   int parts = 1;
-  while (parts < 16 && 2 * parts <= most && (long)tiles * parts < fill) parts *= 2;
+  while (parts < limit && 2 * parts <= most && (long)tiles * parts < fill) parts *= 2;
   return parts;
 }
 
@@ -605,7 +631,7 @@ extern "C" {
 
 int fg_adapters_workspace(int R, int K, int cap, int align, size_t* bytes) {
   if (!bytes || sizes(R, K, cap, align) != FG_OK) return FG_EINVAL;
-  *bytes = kSpareBytes + (size_t)k_parts(cap / tile_rows(align), tile_rows(align), K) * cap * (16 * rank_groups(R)) * sizeof(float);
+  *bytes = kSpareBytes + (size_t)k_parts(cap / tile_rows(align), tile_rows(align), K, R) * cap * (16 * rank_groups(R)) * sizeof(float);
   return FG_OK;
 }
 
@@ -644,14 +670,16 @@ int fg_adapters(const void* D, const void* x, const void* A, const void* B, cons
   const int rt = tile_rows(align);
   p.tiles = cap / rt;
   p.tiles_up8 = (p.tiles + 7) / 8 * 8;
-  p.parts = k_parts(p.tiles, rt, K);
+  p.parts = k_parts(p.tiles, rt, K, R);
   p.stream = (long long)T * N * 2 > kStreamBytes;
   p.copies = out != D ? (int)((T + 127L) / 128 * 8) : 0;
-  // columns of an expand workgroup: long strips load h less often, short ones fill the
-  // chip (64-row tiles, T 8192, N 4096: 512 / 1024 / 2048 columns take 40 / 37 / 37 us;
-  // 16-row tiles, 64 tokens of 64 adapters: 512 / 1024 / 2048 workgroups 6.7 / 6.2 / 7.8 us)
+  // Columns of an expand workgroup: long strips load h less often, short ones fill the
+  // chip. 64-row tiles, T 8192, N 4096, R 64: 512 / 1024 / 2048 columns take 40 / 37 / 37
+  // us; both launches of 512 / 4096 tokens of 8 adapters, R 128, with strips for 256 or
+  // for 512 workgroups: 25.5 / 55 against 31 / 62 us. 16-row tiles, 1024 tokens of 64
+  // adapters, R 16 / 64: 18.5 / 38.4 us for 512 workgroups, 19.8 / 39.6 for 1024.
   p.strip = 1024;
-  while (p.strip > 128 && (long)p.tiles * ((N + p.strip - 1) / p.strip) < (rt == 64 ? 512 : 1024)) p.strip /= 2;
+  while (p.strip > 128 && (long)p.tiles * ((N + p.strip - 1) / p.strip) < (rt == 64 ? 256 : 512)) p.strip /= 2;
   if ((long)p.copies + (long)p.tiles_up8 * ((N + p.strip - 1) / p.strip) > 0x7fffffffL) return FG_EINVAL;
   switch (rank_groups(R)) {
     case 1: launch<1>(p, rt == 64, stream); break;
