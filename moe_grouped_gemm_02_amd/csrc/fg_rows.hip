@@ -211,11 +211,13 @@ __global__ __launch_bounds__(kThreads) void combine(const void* __restrict__ y, 
   store16<STREAM>(&((u32x4*)out)[t * per + i], R::pack(acc));
 }
 
-// One workgroup per token: its row of dout stays in registers for a unit at a
-// time while the choices' rows of y pass by; JC choices per sweep of the row.
+// One workgroup of NTH threads per token: its row of dout stays in registers for a unit
+// at a time while the choices' rows of y pass by, kGradChoices per sweep of the row.
 constexpr int kGradChoices = 8;
+constexpr int kFewTokens = 512;
 
-// Sums acc[JC] over the workgroup in a fixed order and writes dw.
+// Sums acc over the workgroup in a fixed order and writes dw.
+template <int NTH>
 __device__ __forceinline__ void reduce_dw(float* acc, float (*part)[kGradChoices], float* dw, int n) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -227,18 +229,18 @@ __device__ __forceinline__ void reduce_dw(float* acc, float (*part)[kGradChoices
   if ((int)threadIdx.x < n) {
     float s = 0.0f;
 #pragma unroll
-    for (int v = 0; v < kThreads / 64; ++v) s += part[v][threadIdx.x];
+    for (int v = 0; v < NTH / 64; ++v) s += part[v][threadIdx.x];
     dw[threadIdx.x] = s;
   }
   __syncthreads();
 }
 
-template <class R>
-__global__ __launch_bounds__(kThreads) void combine_grad(const void* __restrict__ dout, const void* __restrict__ y,
+template <class R, int NTH>
+__global__ __launch_bounds__(NTH) void combine_grad(const void* __restrict__ dout, const void* __restrict__ y,
                                                          const int32_t* __restrict__ rows,
                                                          const float* __restrict__ w, void* __restrict__ dy,
                                                          float* __restrict__ dw, int k, int N, int n_rows) {
-  __shared__ float part[kThreads / 64][kGradChoices];
+  __shared__ float part[NTH / 64][kGradChoices];
   const long t = blockIdx.x;
   const int per = N / R::kPer16;
   const u32x4* dv = (const u32x4*)dout + t * per;
@@ -253,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad(const void* __restrict_
       wj[c] = c < n ? w[t * k + j0 + c] : 0.0f;
       acc[c] = 0.0f;
     }
-    for (int i = threadIdx.x; i < per; i += kThreads) {
+    for (int i = threadIdx.x; i < per; i += NTH) {
       float d[R::kPer16];
       R::unpack(dv[i], d);
 #pragma unroll
@@ -270,17 +272,17 @@ __global__ __launch_bounds__(kThreads) void combine_grad(const void* __restrict_
         if (dy) ((u32x4*)dy)[at] = R::pack(f);
       }
     }
-    reduce_dw(acc, part, dw + t * k + j0, n);
+    reduce_dw<NTH>(acc, part, dw + t * k + j0, n);
   }
 }
 
-template <class R, bool POW2>
-__global__ __launch_bounds__(kThreads) void combine_grad_quant(const void* __restrict__ dout,
+template <class R, bool POW2, int NTH>
+__global__ __launch_bounds__(NTH) void combine_grad_quant(const void* __restrict__ dout,
                                                                const void* __restrict__ y,
                                                                const int32_t* __restrict__ rows,
                                                                const float* __restrict__ w, QuantOut o,
                                                                float* __restrict__ dw, int k) {
-  __shared__ float part[kThreads / 64][kGradChoices];
+  __shared__ float part[NTH / 64][kGradChoices];
   const long t = blockIdx.x;
   const int per = o.H >> 4;
   for (int j0 = 0; j0 < k; j0 += kGradChoices) {
@@ -294,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_quant(const void* __res
       wj[c] = c < n ? w[t * k + j0 + c] : 0.0f;
       acc[c] = 0.0f;
     }
-    for (int i = threadIdx.x; i < per; i += kThreads) {   // whole groups of eight lanes
+    for (int i = threadIdx.x; i < per; i += NTH) {   // whole groups of eight lanes
       float d[16];
       load16<R>(dout, t, o.H, i, d);
       const float top = group8_max(amax16(d));
@@ -313,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_quant(const void* __res
         store_unit(o, row[c], i, encode16(f, s, POW2), s);
       }
     }
-    reduce_dw(acc, part, dw + t * k + j0, n);
+    reduce_dw<NTH>(acc, part, dw + t * k + j0, n);
   }
 }
 
@@ -346,6 +348,32 @@ void launch_dispatch(bool pow2, hipStream_t s, const void* x, const int32_t* row
   else if (pow2) hipLaunchKernelGGL((dispatch_quant<R, true, false>), g, b, 0, s, x, rows, w, o, T, k, strips);
   else if (w) hipLaunchKernelGGL((dispatch_quant<R, false, true>), g, b, 0, s, x, rows, w, o, T, k, strips);
   else hipLaunchKernelGGL((dispatch_quant<R, false, false>), g, b, 0, s, x, rows, w, o, T, k, strips);
+}
+
+// Threads of a gradient workgroup for rows of `per` units: no more than have one (256
+// with a quarter at work: N 1024, k 2, T 4096 to E4M3, 16.6 us); with few tokens enough
+// for the whole row at once, else 256, which leaves room for other workgroups. 256 / 1024
+// threads, bf16: N 7168, k 8, T 1 / 64 / 256 10.4 / 15.2 / 17.9 against 6.1 / 8.0 / 12.1 us;
+// N 4096, k 4, T 256 / 512 / 2048 7.8 / 9.5 / 30.5 against 6.4 / 10.8 / 44.8 us.
+int grad_threads(int T, int per) { return per <= 64 ? 64 : per > 256 && T < kFewTokens ? 1024 : 256; }
+
+template <class R, class... Args>
+void launch_grad(int T, int per, hipStream_t s, Args... a) {
+  const dim3 g((unsigned)T);
+  switch (grad_threads(T, per)) {
+    case 64: hipLaunchKernelGGL((combine_grad<R, 64>), g, dim3(64), 0, s, a...); break;
+    case 256: hipLaunchKernelGGL((combine_grad<R, 256>), g, dim3(256), 0, s, a...); break;
+    default: hipLaunchKernelGGL((combine_grad<R, 1024>), g, dim3(1024), 0, s, a...); break;
+  }
+}
+template <class R, bool POW2, class... Args>
+void launch_grad_quant(int T, int per, hipStream_t s, Args... a) {
+  const dim3 g((unsigned)T);
+  switch (grad_threads(T, per)) {
+    case 64: hipLaunchKernelGGL((combine_grad_quant<R, POW2, 64>), g, dim3(64), 0, s, a...); break;
+    case 256: hipLaunchKernelGGL((combine_grad_quant<R, POW2, 256>), g, dim3(256), 0, s, a...); break;
+    default: hipLaunchKernelGGL((combine_grad_quant<R, POW2, 1024>), g, dim3(1024), 0, s, a...); break;
+  }
 }
 
 template <class R, class... Args>
@@ -407,9 +435,8 @@ int fg_combine_grad(const void* dout, const void* y, int dtype, const int32_t* r
     return FG_EINVAL;
   const int st = current_device(nullptr);
   if (st != FG_OK) return st;
-  const dim3 g((unsigned)T), b(kThreads);
-  if (dtype == FG_BF16) hipLaunchKernelGGL((combine_grad<RowBf16>), g, b, 0, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
-  else hipLaunchKernelGGL((combine_grad<RowF32>), g, b, 0, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
+  if (dtype == FG_BF16) launch_grad<RowBf16>(T, N / 8, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
+  else launch_grad<RowF32>(T, N / 4, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
   return launched();
 }
 
@@ -423,12 +450,11 @@ int fg_combine_grad_quant(const void* dout, const void* y, int dtype, const int3
   const int st = current_device(nullptr);
   if (st != FG_OK) return st;
   const QuantOut o = {static_cast<uint8_t*>(Q), sq, N, M, G * M};
-  const dim3 g((unsigned)T), b(kThreads);
   const bool pow2 = scales == FG_SCALES_POW2;
-  if (dtype == FG_BF16 && pow2) hipLaunchKernelGGL((combine_grad_quant<RowBf16, true>), g, b, 0, stream, dout, y, rows, w, o, dw, k);
-  else if (dtype == FG_BF16) hipLaunchKernelGGL((combine_grad_quant<RowBf16, false>), g, b, 0, stream, dout, y, rows, w, o, dw, k);
-  else if (pow2) hipLaunchKernelGGL((combine_grad_quant<RowF32, true>), g, b, 0, stream, dout, y, rows, w, o, dw, k);
-  else hipLaunchKernelGGL((combine_grad_quant<RowF32, false>), g, b, 0, stream, dout, y, rows, w, o, dw, k);
+  if (dtype == FG_BF16 && pow2) launch_grad_quant<RowBf16, true>(T, N / 16, stream, dout, y, rows, w, o, dw, k);
+  else if (dtype == FG_BF16) launch_grad_quant<RowBf16, false>(T, N / 16, stream, dout, y, rows, w, o, dw, k);
+  else if (pow2) launch_grad_quant<RowF32, true>(T, N / 16, stream, dout, y, rows, w, o, dw, k);
+  else launch_grad_quant<RowF32, false>(T, N / 16, stream, dout, y, rows, w, o, dw, k);
   return launched();
 }
 
