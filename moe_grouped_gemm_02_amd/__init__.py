@@ -15,6 +15,11 @@ Tensor conventions (all on the same CUDA/HIP device, contiguous):
     B   uint8 or float8_e4m3fn  [N, K]        (grouped: [G, N, K])
     sb  float32                 [ceil(N/128), K/128] (grouped: [G, ceil(N/128), K/128])
     D   bfloat16                [M, N]        (masked: [G, M_max, N])
+
+Row operators around the grouped calls (route_topk, plan_contiguous, plan_masked,
+dispatch_quant, combine and their gradients) and beside the dense one (adapters):
+see their own docstrings; token rows are [T, columns] in bfloat16 or float32,
+choices [T, k] int32, weights [T, k] float32.
 """
 import ctypes
 import functools

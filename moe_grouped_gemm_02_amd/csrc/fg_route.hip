@@ -63,12 +63,18 @@ __device__ __forceinline__ void load_logits(const void* logits, long row, int E,
   using P = Pieces<R, V>;
   if (E % V == 0) {
     const int at = e0 < E ? e0 : E - V;
-    const auto* src = (const typename P::Piece*)((const char*)logits + (row * E + at) * R::kBytes);
-    typename P::Piece raw[P::kCount];
+    const char* src = (const char*)logits + (row * E + at) * R::kBytes;
+    if constexpr (P::kBytes == 16) {
+      u32x4 raw[P::kCount];
 #pragma unroll
-    for (int c = 0; c < P::kCount; ++c) raw[c] = src[c];
+      for (int c = 0; c < P::kCount; ++c) raw[c] = ((const u32x4*)src)[c];
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = R::load1(raw, i);
+      for (int c = 0; c < P::kCount; ++c) R::unpack(raw[c], l + c * R::kPer16);
+    } else {
+      const typename P::Piece raw = *(const typename P::Piece*)src;
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = R::load1(&raw, i);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -85,13 +91,16 @@ template <class R, int V>
 __device__ __forceinline__ void store_row(void* out, long row, int E, int e0, const float* v) {
   using P = Pieces<R, V>;
   if (E % V == 0) {
-    typename P::Piece raw[P::kCount];
+    char* dst = (char*)out + (row * E + e0) * R::kBytes;
+    if (e0 >= E) return;
+    if constexpr (P::kBytes == 16) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) R::store1(raw, i, v[i]);
-    auto* dst = (typename P::Piece*)((char*)out + (row * E + e0) * R::kBytes);
-    if (e0 < E) {
+      for (int c = 0; c < P::kCount; ++c) ((u32x4*)dst)[c] = R::pack(v + c * R::kPer16);
+    } else {
+      typename P::Piece raw;
 #pragma unroll
-      for (int c = 0; c < P::kCount; ++c) dst[c] = raw[c];
+      for (int i = 0; i < V; ++i) R::store1(&raw, i, v[i]);
+      *(typename P::Piece*)dst = raw;
     }
   } else {
 #pragma unroll
