@@ -40,11 +40,15 @@ using namespace fg;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kThreads = 256;
-// Tokens from which on four of at most 64 experts share a wave: with few tokens the
-// wave's longer chain shows, with many its fewer instructions (E 64, k 8, one token /
-// four a wave: T 1024 3.4 / 3.8, 4096 3.9 / 3.9, 16384 7.7 / 6.0 us; with 16 experts a
-// lane, E 256, four a wave lose at every T: 6.2 / 8.1 at 4096, 14.7 / 16.5 at 16384).
-constexpr int kPackTokens = 8192;
+// Tokens from which on four share a wave: with few tokens the wave's longer chain
+// shows, with many its fewer instructions. One token / four a wave, k 8, fp32 softmax
+// in a graph: E 64, T 1024 3.3 / 3.8, 4096 3.9 / 3.9, 16384 7.8 / 5.6 us, its gradient
+// 5.7 / 5.0. E 128, T 4096 4.5 / 4.5, 16384 9.5 / 7.2; sigmoid with a bias 9.4 / 9.2 there
+// but 6.0 / 6.8 at 8192, so twice the tokens. Above 128 experts one token a wave always:
+// with E 256 and T 16384 softmax would gain (12.9 / 11.0) but sigmoid with a bias (13.6 /
+// 15.0) and the gradient (12.3 / 15.0) lose.
+constexpr int kPackTokens = 8192;        // E <= 64
+constexpr int kPackTokensWide = 16384;   // E <= 128
 
 // V consecutive elements of a row move in pieces of up to 16 bytes where V
 // divides E (a lane then has V experts or none, and pieces are aligned).
@@ -319,6 +323,7 @@ void launch_v(bool grad, int T, hipStream_t s, const void* logits, const void* b
 template <class R, class... Args>
 void launch_e(int E, bool grad, int T, Args... a) {
   if (T >= kPackTokens && E <= 64) launch_v<R, 16, 4>(grad, T, a...);
+  else if (T >= kPackTokensWide && E > 64 && E <= 128) launch_v<R, 16, 8>(grad, T, a...);
   else if (E <= 64) launch_v<R, 64, 1>(grad, T, a...);
   else if (E <= 128) launch_v<R, 64, 2>(grad, T, a...);
   else if (E <= 256) launch_v<R, 64, 4>(grad, T, a...);

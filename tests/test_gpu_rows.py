@@ -99,6 +99,15 @@ def test_route_and_gradient(T, E, k, score, with_bias, renorm, dtype):
     assert np.all(near(host(got), ref, tol + 1e-30, dtype))
 
 
+@pytest.mark.parametrize("score,with_bias,renorm", [("softmax", False, False), ("sigmoid", True, True)])
+@pytest.mark.parametrize("T,E,k", [(8191, 64, 8), (8192, 64, 8), (8195, 21, 5), (16383, 128, 8), (16387, 128, 8),
+                                   (16385, 77, 11)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_route_and_gradient_many_tokens(T, E, k, score, with_bias, renorm, dtype):
+    """Batches long enough that several tokens share a wave, and the last shorter ones."""
+    test_route_and_gradient(T, E, k, score, with_bias, renorm, dtype)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_gradient_against_differences(score, renorm):
