@@ -260,6 +260,13 @@ def test_combine(layout, T, k, G, N, dtype, weighted, with_base):
         assert torch.equal(fg.dispatch_grad(y, p), out)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("weighted,with_base", [(True, True), (False, False)])
+def test_combine_large_output(dtype, weighted, with_base):
+    """An output past the size from which it is stored past the caches."""
+    test_combine("contiguous", 2400, 2, 4, 7176, dtype, weighted, with_base)
+
+
 def grad_inputs(layout, T, k, G, N, dtype):
     rng = np.random.default_rng(N + T + 1)
     p = make_plan(layout, T, k, G)
@@ -317,6 +324,15 @@ def test_combine_grad_quant(layout, T, k, G, N, pow2, dtype):
     fg.dispatch_quant(dout, p, w=to_dev(w), pow2=pow2, Q=Q2, sa=sa2)
     assert torch.equal(Q, Q2) and torch.equal(sa, sa2)
     check_dw(host(dw), p, y, dout, N)
+
+
+@pytest.mark.parametrize("layout", ["contiguous", "masked"])
+@pytest.mark.parametrize("T", [511, 512])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_combine_grad_long_rows(layout, T, dtype):
+    """Long rows on both sides of the number of tokens from which a token has fewer threads."""
+    test_combine_grad(layout, T, 2, 4, 4104, dtype)
+    test_combine_grad_quant(layout, T, 2, 4, 4224, False, dtype)
 
 
 def test_combine_gradient_against_differences():
@@ -399,6 +415,12 @@ def test_adapters(T, L, align, R, K, N):
     assert np.all(near(got, ref, tol, "bf16"))
     assert np.array_equal(got[ids < 0], host(D)[ids < 0])
     assert fg.adapters(D, x, A, B, to_dev(scales), p, out=D) is D and torch.equal(D, out)
+
+
+@pytest.mark.parametrize("R", [24, 64, 128])
+def test_adapters_large_output(R):
+    """An output past the size from which it is stored past the caches."""
+    test_adapters(4112, 3, 64, R, 256, 4096)
 
 
 def test_adapters_without_any():
