@@ -25,7 +25,7 @@
 // TB/s of a large copy; shrink takes 27 us (37 where 124 or more tiles are in use: some
 // compute units then hold three of its workgroups, and at about 25 bytes a clock their
 // loads into LDS are the limit), expand 37-39. 64 tokens of 64 adapters, R 16: 15 MB and
-// two launches, 6 us each, mostly latency: plan, rows, operands one after another.
+// two launches, 6.2 and 5.6 us, mostly latency: plan, rows, operands one after another.
 // 16- against 64-row tiles, both launches: R 16, L 8, T 128 / 256 / 1024: 9.7 / 11.0 /
 // 17.1 against 10.6 / 10.7 / 14.4 us; L 64, T 1024 / 2048 19.5 / 25.8 against 21.3 / 21.6:
 // 64 pays from about 32 tokens an adapter on.
@@ -433,7 +433,7 @@ __global__ __launch_bounds__(kThreads) void adapter_expand16(AdapterArgs p) {
 // The products leave the matrix cores with 16 rows to an instruction; they turn round
 // in LDS, 64 columns at a time, so that each load of D and store of out covers whole
 // 128-byte lines of eight rows. Straight from the registers, 64-byte halves of 16 rows,
-// the kernel took 38 or 46 us by the relative placing of D and out; so 37 us for either.
+// the kernel took 38 or 46 us by the relative placing of D and out; so 37-39 us for either.
 constexpr int kCols = 128, kHalf = 64;
 
 __device__ __forceinline__ int swizzle_key(int n, int chunks) {
