@@ -235,7 +235,15 @@ __device__ __forceinline__ void reduce_dw(float* acc, float (*part)[kGradChoices
   __syncthreads();
 }
 
-template <class R, int NTH>
+// The bytes of y (all choices, T k N of them) from which combine_grad reads it past the
+// caches. With dy / dw alone, N 7168, k 8, bf16: T 2048 116.6 / 60.2 -> 94.9 / 55.0 us, T
+// 8192 400 / 179 -> 402 / 165; N 2048, k 8, T 8192 113 / 54 -> 98 / 49. Below, shorter
+// batches lose: N 2048, k 8, T 1024 (34 MB) 13.3 / 9.0 -> 15.2 / 9.8 us. Stores of dy past
+// them, and y in the E4M3 form, where a lane reads 32 bytes in two pieces, gain at some
+// sizes what they lose at others and stay ordinary.
+constexpr long long kGradStreamBytes = 128ll << 20;
+
+template <class R, bool STREAM, int NTH>
 __global__ __launch_bounds__(NTH) void combine_grad(const void* __restrict__ dout, const void* __restrict__ y,
                                                          const int32_t* __restrict__ rows,
                                                          const float* __restrict__ w, void* __restrict__ dy,
@@ -263,7 +271,7 @@ __global__ __launch_bounds__(NTH) void combine_grad(const void* __restrict__ dou
         if (row[c] < 0) continue;   // uniform
         float f[R::kPer16];
         const long at = (long)row[c] * per + i;
-        R::unpack(((const u32x4*)y)[at], f);
+        R::unpack(load16b<STREAM>((const u32x4*)y + at), f);
 #pragma unroll
         for (int e = 0; e < R::kPer16; ++e) {
           acc[c] = fmaf(d[e], f[e], acc[c]);
@@ -357,13 +365,13 @@ void launch_dispatch(bool pow2, hipStream_t s, const void* x, const int32_t* row
 // N 4096, k 4, T 256 / 512 / 2048 7.8 / 9.5 / 30.5 against 6.4 / 10.8 / 44.8 us.
 int grad_threads(int T, int per) { return per <= 64 ? 64 : per > 256 && T < kFewTokens ? 1024 : 256; }
 
-template <class R, class... Args>
+template <class R, bool STREAM, class... Args>
 void launch_grad(int T, int per, hipStream_t s, Args... a) {
   const dim3 g((unsigned)T);
   switch (grad_threads(T, per)) {
-    case 64: hipLaunchKernelGGL((combine_grad<R, 64>), g, dim3(64), 0, s, a...); break;
-    case 256: hipLaunchKernelGGL((combine_grad<R, 256>), g, dim3(256), 0, s, a...); break;
-    default: hipLaunchKernelGGL((combine_grad<R, 1024>), g, dim3(1024), 0, s, a...); break;
+    case 64: hipLaunchKernelGGL((combine_grad<R, STREAM, 64>), g, dim3(64), 0, s, a...); break;
+    case 256: hipLaunchKernelGGL((combine_grad<R, STREAM, 256>), g, dim3(256), 0, s, a...); break;
+    default: hipLaunchKernelGGL((combine_grad<R, STREAM, 1024>), g, dim3(1024), 0, s, a...); break;
   }
 }
 template <class R, bool POW2, class... Args>
@@ -435,8 +443,11 @@ int fg_combine_grad(const void* dout, const void* y, int dtype, const int32_t* r
     return FG_EINVAL;
   const int st = current_device(nullptr);
   if (st != FG_OK) return st;
-  if (dtype == FG_BF16) launch_grad<RowBf16>(T, N / 8, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
-  else launch_grad<RowF32>(T, N / 4, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
+  const bool big = (long long)T * k * N * (dtype == FG_BF16 ? 2 : 4) > kGradStreamBytes;
+  if (dtype == FG_BF16 && big) launch_grad<RowBf16, true>(T, N / 8, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
+  else if (dtype == FG_BF16) launch_grad<RowBf16, false>(T, N / 8, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
+  else if (big) launch_grad<RowF32, true>(T, N / 4, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
+  else launch_grad<RowF32, false>(T, N / 4, stream, dout, y, rows, w, dy, dw, k, N, n_rows);
   return launched();
 }
 

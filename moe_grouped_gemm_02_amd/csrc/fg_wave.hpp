@@ -100,6 +100,13 @@ __device__ __forceinline__ void store16(u32x4* p, u32x4 v) {
 }
 constexpr long long kStreamBytes = 32ll << 20;
 
+// A 16-byte load, past the caches where STREAM.
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load16b(const u32x4* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+
 // Element types of activations: 16 bytes of a row at a time.
 struct RowBf16 {
   static constexpr int kPer16 = 8;   // elements in 16 bytes

@@ -335,6 +335,12 @@ def test_combine_grad_long_rows(layout, T, dtype):
     test_combine_grad_quant(layout, T, 2, 4, 4224, False, dtype)
 
 
+@pytest.mark.parametrize("dtype,T", [("bf16", 2400), ("fp32", 1201)])
+def test_combine_grad_large_input(dtype, T):
+    """More of y than the size from which it is read past the caches."""
+    test_combine_grad("contiguous", T, 4, 6, 7176, dtype)
+
+
 def test_combine_gradient_against_differences():
     """<dout, combine(y, w)> along random directions of y and w, in fp32 inputs (combine is bilinear: no truncation error)."""
     T, k, G, N = 20, 3, 4, 64
