@@ -15,8 +15,9 @@
 //           columns; h is summed over the parts, scaled, and cut into three bf16 of
 //           eight bits each, which hold all 24 bits of it: the work is bound by moving
 //           D, not by the matrix cores (T 8192, N 4096, R 64: 39.6 us, 39.1 with two
-//           pieces, which hold 17 bits). For R <= 16 two pieces fit one 32-deep MFMA,
-//           one against k 0..15 and one against k 16..31 with B's fragment repeated.
+//           pieces, which hold 17 bits). For R <= 16 the two lower pieces fit one
+//           32-deep MFMA, one against k 0..15 and one against k 16..31 with B's
+//           fragment repeated.
 // Each has a kernel for 16-row tiles (decode), where A and B are read once and go
 // straight into fragments, and one for 64-row tiles (prompts), where four waves share
 // them through LDS.
@@ -276,8 +277,9 @@ __device__ __forceinline__ uint32_t bf16_pair_cut(float a, float b) {
 // A lane's fragments of h: row `row` of the tile, its parts summed, scaled and cut
 // into three pieces: the upper eight bits of the significand, the upper eight of what
 // is left of it, and the rest, which has eight at most. Both differences are exact.
-// (Bits of h below 2^-133, bf16's smallest, are lost.) TR == 1: the first piece in
-// the lanes of k 0 .. 15 and the second in the others, then the third and zeros.
+// (Bits of h below 2^-133, bf16's smallest, are lost.) TR == 1: half of the first piece
+// in the lanes of k 0 .. 15 and in the others (not zeros: 0 times an infinite weight
+// is NaN), then the second piece and the third.
 template <int TR>
 struct HFrags {
   static constexpr int KF = TR == 1 ? 1 : TR / 2;   // 32-deep fragments of the rank
@@ -332,8 +334,9 @@ __device__ __forceinline__ void load_h(const AdapterArgs& p, int row, int first,
       }
     }
     if constexpr (TR == 1) {
-      h.f[0][0] = q < 2 ? piece[0] : piece[1];
-      h.f[1][0] = q < 2 ? piece[2] : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h.f[0][0][e] = bf16_pair_cut(bf16_lo(piece[0][e]) * 0.5f, bf16_hi(piece[0][e]) * 0.5f);
+      h.f[1][0] = q < 2 ? piece[1] : piece[2];
     } else {
 #pragma unroll
       for (int i = 0; i < 3; ++i) h.f[i][k] = piece[i];
@@ -379,6 +382,16 @@ __device__ __forceinline__ void start_pair(u32x4 d, f32x4v* acc) {
     acc[e >> 1][2 * (e & 1) + 1] = bf16_hi(d[e]);
   }
 }
+// The first pieces' products and the lower pieces' as one sum. Where the lower sum is
+// no number, an h or a weight is infinite or NaN (inf - inf in a lower piece, 0 x inf in
+// a product), and the first pieces alone give what whole values would: they have the
+// signs of h and are zero only where it is.
+__device__ __forceinline__ f32x4v join(f32x4v top, f32x4v rest) {
+  f32x4v r;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) r[v] = top[v] + (__builtin_isfinite(rest[v]) ? rest[v] : 0.0f);
+  return r;
+}
 __device__ __forceinline__ u32x4 end_pair(const f32x4v* acc) {
   u32x4 r;
 #pragma unroll
@@ -422,14 +435,17 @@ __global__ __launch_bounds__(kThreads) void adapter_expand16(AdapterArgs p) {
     const int col = n0 + 8 * q;
     const bool ok = real && col < n_hi;
     const u32x4 d = *(const u32x4*)(drow + (col < n_hi ? col : n_lo));
-    f32x4v acc[2];
+    f32x4v acc[2], rest[2];
     start_pair(d, acc);
+    rest[0] = rest[1] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int l = H::HL - 1; l >= 0; --l)   // the small pieces first
 #pragma unroll
       for (int f = 0; f < H::KF; ++f)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) acc[e] = mfma(bf[e][f], h.f[l][f], acc[e]);
+        for (int e = 0; e < 2; ++e) (l ? rest : acc)[e] = mfma(bf[e][f], h.f[l][f], (l ? rest : acc)[e]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) acc[e] = join(acc[e], rest[e]);
     if (ok) *(u32x4*)(p.out + (long)tok * p.N + col) = end_pair(acc);
   }
 }
@@ -546,8 +562,8 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      f32x4v acc[2];
-      acc[0] = acc[1] = f32x4v{0.f, 0.f, 0.f, 0.f};
+      f32x4v acc[2], rest[2];
+      acc[0] = acc[1] = rest[0] = rest[1] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int f = 0; f < H::KF; ++f) {
 #pragma unroll
@@ -557,12 +573,13 @@ __global__ __launch_bounds__(kThreads) void adapter_expand64(AdapterArgs p) {
           u32x4 b = *(const u32x4*)(ring[B] + ((n * chunks + (cc[f] ^ swizzle_key(n, chunks))) << 4));
           if (!FULL && cc[f] != (TR == 1 ? q & 1 : 4 * f + q)) b = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int l = H::HL - 1; l >= 0; --l) acc[e] = mfma(b, h.f[l][f], acc[e]);
+          for (int l = H::HL - 1; l > 0; --l) rest[e] = mfma(b, h.f[l][f], rest[e]);
+          acc[e] = mfma(b, h.f[0][f], acc[e]);
         }
       }
       float* to = &turn[wave][lrow][32 * (g & 1) + 8 * q];
-      *(f32x4v*)to = acc[0];
-      *(f32x4v*)(to + 4) = acc[1];
+      *(f32x4v*)to = join(acc[0], rest[0]);
+      *(f32x4v*)(to + 4) = join(acc[1], rest[1]);
       if (g & 1) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the wave's own LDS accesses, in order
 #pragma unroll

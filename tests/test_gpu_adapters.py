@@ -1,4 +1,4 @@
-"""The adapters' numerics on the GPU. The inputs are whole numbers (and powers of two) of so few bits that every sum is exact in fp32
+"""The adapters' numerics on the GPU: the inner result held in 32 bits, and infinities. The inputs are whole numbers (and powers of two) of so few bits that every sum is exact in fp32
 whatever its order, so an output has to be the bf16 rounding of the exact result, bit for bit."""
 import numpy as np
 import pytest
@@ -68,3 +68,50 @@ def test_inner_result_keeps_32_bits(R, align):
     want = (scales[:, None] * sign * byte[2])[ids][:, np.arange(N) % (R // 2)] * x[:, 100:101]
     assert np.array_equal(rounded(want), want) and np.all(want != 0)
     assert np.array_equal(out, want)
+
+
+# ------------------------------------------------------------------ infinities
+@pytest.mark.parametrize("align", [16, 64])
+@pytest.mark.parametrize("R", [8, 16, 32, 64, 72, 128])
+def test_infinities_as_in_fp32(R, align):
+    """A product that overflows, an infinite operand and the largest finite h give what fp32 gives: an infinity with
+    its sign, NaN only for inf - inf, inf x 0 and NaN itself."""
+    T, L, K, N = 24, 2, 128, 136
+    rng = np.random.default_rng(R)
+    ids = np.arange(T) % L
+    x, A = np.zeros((T, K)), np.zeros((L, R, K))
+    B = rng.integers(1, 5, (L, N, R)) * rng.choice([-1.0, 1.0], (L, N, R))
+    D = rng.integers(-8, 9, (T, N)).astype(np.float64)
+    D[6:8, 3], D[6:8, 4] = np.inf, -np.inf
+    x[:, 2], A[:, :, 2] = 1.0, rng.integers(1, 100, (L, R))        # ordinary h everywhere
+    # adapter 0: h overflows in rank 1 (both signs, by token); a column without that rank has inf x 0
+    A[0, 1, 7] = 2.0 ** 100
+    x[0, 7], x[2, 7] = 2.0 ** 100, -2.0 ** 100
+    B[0, 9, 1] = 0.0
+    # ranks 2 and 3 overflow together: inf - inf where their columns' signs differ
+    A[0, 2, 11] = A[0, 3, 11] = 2.0 ** 90
+    x[4, 11] = 2.0 ** 90
+    # an infinite input
+    x[8, 7] = np.inf
+    # adapter 1: infinite weights; h of few bits, of 24 bits (both signs), and zero
+    B[1, 5, 0], B[1, 6, 0], B[1, 7, R - 1] = np.inf, -np.inf, np.inf
+    A[1, 0, 40:43] = 251.0, 253.0, 255.0
+    x[3, 40:43] = 65536.0, 256.0, 1.0
+    x[5, 40:43] = -65536.0, -256.0, -1.0
+    x[7] = 0.0
+    # adapter 1, rank 4: h above the largest bf16, below the largest fp32 (255.75 x 2^120)
+    A[1, 4, 60:62] = 255 * 2.0 ** 20, 0.75 * 2.0 ** 20
+    x[9, 60:62] = 2.0 ** 100
+    A[1, 4, 2] = 0.0
+    B[1, :, 4] = 2.0 ** -10 * rng.choice([-1.0, 1.0], N)
+    out, _ = run(D, x, A, B, np.ones(L), ids, align)
+    with np.errstate(over="ignore", invalid="ignore"):
+        ref = rounded(reference(D, x, A, B, np.ones(L), ids))
+    print("inf", int(np.isinf(ref).sum()), "nan", int(np.isnan(ref).sum()), flush=True)
+    assert np.isinf(ref).sum() > 300 and 100 < np.isnan(ref).sum() < 0.25 * ref.size
+    assert np.isfinite(ref[9, 8:]).all() and np.abs(ref[9, 8:]).min() >= 2.0 ** 117
+    bad = ~((out == ref) | (np.isnan(out) & np.isnan(ref)))
+    for t in (3, 5, 9):   # sums of a large h's products and ordinary ones are not exact: one bf16 step there
+        with np.errstate(invalid="ignore"):
+            bad[t] &= ~(np.abs(out[t] - ref[t]) <= 2.0 ** -7 * np.abs(ref[t]))
+    assert not bad.any(), [(int(t), int(n), out[t, n], ref[t, n]) for t, n in np.argwhere(bad)[:8]]
