@@ -1,5 +1,8 @@
-"""The adapters' numerics on the GPU: the inner result held in 32 bits, and infinities. The inputs are whole numbers (and powers of two) of so few bits that every sum is exact in fp32
+"""The adapters' numerics on the GPU: the inner result held in 32 bits, infinities, and both products' loops at the
+depths of real sizes. The inputs are whole numbers (and powers of two) of so few bits that every sum is exact in fp32
 whatever its order, so an output has to be the bf16 rounding of the exact result, bit for bit."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -115,3 +118,59 @@ def test_infinities_as_in_fp32(R, align):
         with np.errstate(invalid="ignore"):
             bad[t] &= ~(np.abs(out[t] - ref[t]) <= 2.0 ** -7 * np.abs(ref[t]))
     assert not bad.any(), [(int(t), int(n), out[t, n], ref[t, n]) for t, n in np.argwhere(bad)[:8]]
+
+
+# ------------------------------------------------------------------ depth of the loops
+def shape_of_work(T, L, align, R, K, N):
+    """What the size rules make of a call: parts of K (from the workspace they need), steps of 64 k for a wave's or
+    workgroup's run, rounds of 128 columns in an expand workgroup, and whether the output is stored past the caches."""
+    cap, size = fg.plan_capacity(T, 1, L, align), ctypes.c_size_t()
+    assert fg.lib().fg_adapters_workspace(R, K, cap, align, ctypes.byref(size)) == 0
+    groups = 1 if R <= 16 else 2 if R <= 32 else 4 if R <= 64 else 8
+    parts, rest = divmod(size.value - 1024, cap * 16 * groups * 4)
+    assert rest == 0
+    rt = 64 if align % 64 == 0 else 16
+    strip, tiles = 1024, cap // rt
+    while strip > 128 and tiles * -(-N // strip) < (256 if rt == 64 else 512):
+        strip //= 2
+    return dict(parts=parts, steps=K // 64 // (parts * (1 if rt == 64 else 4)), rounds=-(-min(strip, N) // 128),
+                stream=T * N * 2 > 32 << 20)
+
+
+DEPTH = [
+    # (T, L, align, R, K, N, what the case is here for)
+    (1, 1, 16, 16, 7168, 4096, dict(parts=8)),
+    (1, 1, 16, 64, 7168, 4096, dict(parts=8)),
+    (1, 1, 16, 128, 7168, 4104, dict(parts=8)),
+    (64, 64, 16, 16, 7168, 4096, dict(parts=4, steps=7, rounds=4)),
+    (300, 200, 16, 64, 7168, 2056, dict(parts=2, steps=14)),
+    (600, 500, 48, 32, 7168, 1000, dict(parts=1, steps=28)),
+    (1024, 8, 64, 16, 7168, 4096, dict(parts=8, steps=14, rounds=2, stream=False)),
+    (512, 8, 64, 128, 7168, 4096, dict(parts=4, steps=28)),
+    (33, 1, 64, 40, 7168, 520, dict(parts=4, steps=28)),
+    (8192, 8, 64, 8, 512, 1000, dict(rounds=4, stream=False)),
+    (8192, 3, 64, 24, 512, 1000, dict(rounds=4, stream=False)),
+    (8192, 3, 128, 64, 256, 1544, dict(rounds=8, stream=False)),
+    (8192, 2, 64, 128, 256, 1000, dict(rounds=4, stream=False)),
+    (4112, 8, 64, 8, 512, 4104, dict(rounds=8, stream=True)),
+    (4112, 8, 64, 16, 512, 4104, dict(rounds=8, stream=True)),
+    (4112, 8, 64, 40, 512, 4104, dict(rounds=8, stream=True)),
+    (4112, 8, 64, 128, 1024, 4104, dict(rounds=8, stream=True)),
+]
+
+
+@pytest.mark.parametrize("T,L,align,R,K,N,what", DEPTH, ids=lambda v: str(v) if not isinstance(v, dict) else "")
+def test_depth(T, L, align, R, K, N, what):
+    got = shape_of_work(T, L, align, R, K, N)
+    print(f"adapters T={T} L={L} align={align} R={R} K={K} N={N} {got}", flush=True)
+    assert {k: got[k] for k in what} == what
+    rng = np.random.default_rng(T + R + N)
+    ids = rng.integers(-1 if T > 1 else 0, L, T)
+    whole = lambda most, *shape: rng.integers(-most, most + 1, shape, dtype=np.int16).astype(np.float32)  # noqa: E731
+    x, D, A, B = whole(4, T, K), whole(200, T, N), whole(2, L, R, K), whole(2, L, N, R)
+    scales = 2.0 ** rng.integers(-2, 3, L)
+    ref = reference(D, x, A, B, scales, ids)
+    assert np.abs(ref).max() < 2 ** 21      # whole quarters below 2^24 of them
+    for in_place in (False, True):
+        out, _ = run(D, x, A, B, scales, ids, align, in_place)
+        assert np.array_equal(out, rounded(ref))
