@@ -20,6 +20,9 @@
 //     sigmoid                  dl = g s (1 - s)
 //     sigmoid, renormalised    dl = (g - <g, p>) / (sum of the chosen s) * s (1 - s), chosen only
 //
+// 1 - s of a sigmoid is worked out from the logit, 1 / (1 + exp(l)): as a difference it
+// keeps u / (1 - s) of relative error (u = 2^-24), 1% at a logit of 12, and is 0 from 17 on.
+//
 // A group of L = 64 or 16 lanes holds a token: lane i of it has experts
 // [i * V, (i + 1) * V). Each of the k rounds is a maximum over the group's 32-bit
 // order keys on the DPP path, a ballot that finds the lowest lane holding it, and
@@ -128,6 +131,9 @@ __device__ __forceinline__ float raw_score(float l, float top, int softmax) {
   if (!(l > -INFINITY)) return 0.0f;
   return softmax ? expf(l - top) : 1.0f / (1.0f + expf(-l));
 }
+
+// 1 - 1 / (1 + exp(-l)), to a few u of itself for either sign of l.
+__device__ __forceinline__ float sigmoid_complement(float l) { return 1.0f / (1.0f + expf(l)); }
 
 // Scores of the lane's V logits.
 template <int L, int V>
@@ -295,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void route_topk_grad(const void* __restri
   for (int i = 0; i < V; ++i) {
     float out = 0.0f;
     if (total > 0.0f) out = g[i] * (renorm ? s[i] / total : s[i]);
-    g[i] = softmax ? out : out * (1.0f - s[i]);
+    g[i] = softmax ? out : out * sigmoid_complement(l[i]);
   }
   store_row<R, V>(dlogits, t, E, lane * V, g);
 }
