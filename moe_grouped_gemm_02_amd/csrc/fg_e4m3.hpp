@@ -18,11 +18,12 @@ namespace fg {
 constexpr float kE4M3Max = 448.0f;
 
 // Nearest E4M3 codes, ties to the even code, sign kept (so -tiny -> 0x80),
-// for finite inputs with |y| <= 448: gfx950's v_cvt_pk_fp8_f32 (OCP E4M3).
-// On every finite fp32 value in that range it gives the same byte as a
+// for finite inputs with |y| <= 448 or the next float above: gfx950's
+// v_cvt_pk_fp8_f32 (OCP E4M3). On every fp32 value up to 448 it gives the same byte as a
 // software round-to-nearest-even encoder (the E4M3 significand rounded at
 // fp32 bit 20, and the subnormal codes as multiples of 2^-9) -- checked
-// exhaustively on the device, all 2^32 bit patterns. Codes of y0, y1 land in
+// exhaustively on the device, all 2^32 bit patterns; the float above 448 gives
+// 448's code (tests/test_gpu_e4m3_quotient.py). Codes of y0, y1 land in
 // bytes 0, 1 (HI = false) or 2, 3 (HI = true) of the result; the other half
 // is kept from `old`.
 template <bool HI>

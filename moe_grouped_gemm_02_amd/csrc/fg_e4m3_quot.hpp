@@ -15,10 +15,14 @@ namespace fg {
 // differ from the rounded quotient only where x / s lies that close to the middle of
 // two floats, and the codes only where one of these floats is a boundary between
 // codes, which has at most 5 significant bits. That needs s within 8 units of a value
-// of 4 significant bits; all such cases were gone through in exact arithmetic and give
-// the rounded quotient (tests/test_e4m3_quotient.py). The residual is exact while
-// s >= 2^-90 (kQuotMin) for every x whose code is not zero; below that the caller
-// divides. The residual is taken as q s - x, which keeps the sign of a zero.
+// of 4 significant bits, from either side; all such cases were gone through in exact
+// arithmetic and give the rounded quotient (tests/test_e4m3_quotient.py). The residual
+// is exact while s >= 2^-90 (kQuotMin) for every x whose code is not zero; below that
+// the caller divides. The residual is taken as q s - x, which keeps the sign of a zero.
+//
+// The quotients are not clamped to +-448 as in e4m3x4_div: where amax / 448 was rounded
+// down, amax / s is the float above 448 (6 to 8 blocks of 100), never more (every
+// significand of amax was gone through), and its code is 448's all the same.
 constexpr float kQuotMin = 8.0779357e-28f;   // 2^-90
 __device__ __forceinline__ float e4m3_quot(float x, float s, float inv) {
   const float q = x * inv;

@@ -7,6 +7,8 @@ arithmetic, and random ones besides."""
 import random
 from fractions import Fraction as F
 
+import numpy as np
+
 
 def rounded(v):
     """v to 24 significant bits, ties to even, no limits on the exponent."""
@@ -64,3 +66,28 @@ def test_random_pairs():
         S, X = rng.randrange(2 ** 23, 2 ** 24), rng.randrange(2 ** 23, 2 ** 24)
         q = corrected(F(X), F(S), rounded(F(1, S)))
         assert q == rounded(F(X, S))
+
+
+def test_every_pair_just_below_a_power_of_two():
+    """The band that near_pairs leaves out: S within 8 below 2^24, the neighbours of 16 x 2^20."""
+    n = 0
+    for S in range(2 ** 24 - 8, 2 ** 24):
+        for m5 in range(16, 32):
+            m = m5 * 2 ** 19
+            for mid in [F(2 * m + 1, 2), F(2 * m - 1, 2)] + ([F(4 * m - 1, 4)] if m == 2 ** 23 else []):
+                for e in (23, 24, 25):
+                    x0 = int(mid * S / F(2) ** e)
+                    for X in range(x0 - 2, x0 + 4):
+                        if 2 ** 23 <= X < 2 ** 24 and abs(F(X) * F(2) ** e / S - mid) <= F(1, 2 ** 20):
+                            n += 1
+                            assert corrected(F(X), F(S), rounded(F(1, S))) == rounded(F(X, S)), (S, X)
+    assert n > 20
+
+
+def test_quotients_pass_448_by_one_float_at_most():
+    """Every significand of amax: amax / (amax / 448), both rounded, is 448 or a neighbour, which is why the encoder's
+    quotients need no clamp; no value of a block is above its amax."""
+    a = np.arange(2 ** 23, 2 ** 24, dtype=np.int64).astype(np.float32)
+    q = a / (a / np.float32(448))
+    below, above = (np.nextafter(np.float32(448), np.float32(to)) for to in (0, 1000))
+    assert set(np.unique(q).tolist()) == {float(below), 448.0, float(above)}
