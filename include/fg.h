@@ -338,9 +338,11 @@ int fg_dispatch_quant(const void* x, int dtype, const int32_t* rows, const float
 /*
  * Combine: out[t] = base[t] + sum_j w[t][j] * y[rows[t][j]], in fp32, rounded
  * once. y [n_rows][N], base [T][N] or NULL, out [T][N] (may be base), all bf16
- * or all fp32 and 16-byte aligned; w [T][k] fp32 or NULL (all ones: the
- * gradient of dispatch's copies). A row outside [0, n_rows) adds nothing.
- * N % 8 == 0. A masked plan's y is its [G * M_max][N].
+ * or all fp32 and 16-byte aligned; w [T][k] fp32 or NULL (all ones). A row
+ * outside [0, n_rows) adds nothing. N % 8 == 0. A masked plan's y is its
+ * [G * M_max][N]. With y the gradient of dispatch's sorted rows and dispatch's own
+ * w (or none) this is the gradient of its x; that of its w is the dw of
+ * fg_combine_grad with dout = x and the same y.
  */
 int fg_combine(const void* y, int dtype, const int32_t* rows, const float* w, const void* base, void* out, int T,
                int k, int N, int n_rows, hipStream_t stream);

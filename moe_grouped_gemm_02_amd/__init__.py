@@ -667,7 +667,7 @@ def _sorted_rows(y, plan):
 
 def combine(y, plan, w=None, base=None, out=None):
     """out[t] = base[t] + sum_j w[t, j] y[row of slot (t, j)]: the experts' rows back in token
-    order ([T, N], y's type). w None: all ones, which is dispatch's gradient. out may be base."""
+    order ([T, N], y's type). w None: all ones, which is unweighted dispatch's gradient. out may be base."""
     dt = _elem(y, "y")
     N = _sorted_rows(y, plan)
     dev, T, k = plan.device, plan.T, plan.k
@@ -681,9 +681,11 @@ def combine(y, plan, w=None, base=None, out=None):
     return out
 
 
-def dispatch_grad(dA, plan, out=None):
-    """Gradient of dispatch's copies with respect to x: the sum of each token's sorted rows."""
-    return combine(dA, plan, out=out)
+def dispatch_grad(dA, plan, out=None, w=None):
+    """Gradient of dispatch's copies with respect to x: the sum of each token's sorted rows, times
+    w [T, k] where dispatch_quant was given it. The weights' own gradient <x[t], dA[row]> is the dw of
+    combine_grad(x, dA, plan, w, with_dy=False). The rounding to E4M3 is passed over."""
+    return combine(dA, plan, w=w, out=out)
 
 
 def _combine_grad_args(dout, y, plan, w, dw):
