@@ -19,10 +19,11 @@
 // before its chunk and in the whole batch. Up to kRecount slots every workgroup
 // counts the batch itself (whole-number LDS atomics, a few microseconds at most),
 // which saves a launch; beyond, a first launch leaves each chunk's histogram in the
-// workspace. Both are bound by latency: 131072 slots are 2 MB of ids, rows, slots and
-// experts, under a microsecond of traffic. In a graph, G 64, contiguous, the one launch
-// takes 5.2 / 5.8 / 7.0 / 9.5 us at 2048 / 8192 / 16384 / 32768 slots, two launches
-// 8.6 / 9.0 / 9.5 / 9.6 us; at 131072 it is 24.9 against 10.4 us.
+// workspace, and where those are many (kSumEntries) a second one makes their prefixes.
+// One or two launches are bound by latency: 131072 slots are 2 MB of ids, rows, slots
+// and experts, under a microsecond of traffic. In a graph, G 64, contiguous, the one
+// launch takes 5.2 / 5.8 / 7.0 / 9.5 us at 2048 / 8192 / 16384 / 32768 slots, two
+// launches 8.6 / 9.0 / 9.5 / 9.6 us; at 131072 it is 24.9 against 10.4 us.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -39,12 +40,20 @@ constexpr int kMaxGroups = 1024;
 constexpr int kRecount = 32768;    // slots up to which every workgroup counts them all
 constexpr int kBatches = 4;        // batches of 64 slots per wave beyond that
 constexpr int kChunk = kThreads * kBatches;
+// Histogram entries (experts x chunks) up to which every placing workgroup sums all of
+// them, work that grows with the square of the slots; beyond, a launch of its own leaves
+// each chunk's prefix and the totals. Summed / with that launch, in a graph, us: 256
+// experts, 65536 slots (8192 entries) 12.8 / 13.5, 131072 14.7 / 14.1, 1048576 111 / 25,
+// 4194304 1400 / 81; 1024 experts, 40960 (20480) 17.3 / 16.3, 4194304 5535 / 139; 64
+// experts, 131072 (4096) 10.4 / 12.1, 262144 (8192) 13.4 / 13.0, 4194304 370 / 56.
+constexpr long kSumEntries = 8192;
 constexpr int kFillRows = 1024;    // rows of the layout per workgroup, where that needs more of them
 
 struct PlanArgs {
   const int32_t* ids;
   int32_t *rows, *slots, *m_indices, *offsets, *masked_m;
   const int32_t* hist;   // [G][chunks_up4], null: count here
+  const int32_t* total;  // [G], hist holds prefixes; null: counts
   int S, G, align, M_max, cap, bits, chunks, chunks_up4;
 };
 
@@ -77,6 +86,32 @@ __global__ __launch_bounds__(kThreads) void plan_count(const int32_t* __restrict
   }
   __syncthreads();
   for (int g = threadIdx.x; g < G; g += kThreads) hist[(long)g * chunks_up4 + blockIdx.x] = n[g];
+}
+
+// Each expert's counts become the sums of the chunks before, and their total: a wave
+// per expert, 256 chunks at a time.
+__global__ __launch_bounds__(256) void plan_prefix(int32_t* __restrict__ hist, int32_t* __restrict__ total, int G,
+                                                   int chunks, int chunks_up4) {
+  const int lane = threadIdx.x & 63, g = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (g >= G) return;
+  int carry = 0;
+  for (int c0 = 0; c0 < chunks; c0 += 256) {
+    const int c = c0 + 4 * lane;
+    int4* at = (int4*)(hist + (long)g * chunks_up4 + (c < chunks_up4 ? c : 0));
+    const int4 n = *at;
+    const int n0 = c < chunks ? n.x : 0, n1 = c + 1 < chunks ? n.y : 0, n2 = c + 2 < chunks ? n.z : 0,
+              n3 = c + 3 < chunks ? n.w : 0, sum = n0 + n1 + n2 + n3;
+    int end = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(end, d, 64);
+      if (lane >= d) end += u;
+    }
+    const int before = carry + end - sum;
+    if (c < chunks_up4) *at = make_int4(before, before + n0, before + n0 + n1, before + n0 + n1 + n2);
+    carry += __shfl(end, 63, 64);
+  }
+  if (lane == 0) total[g] = carry;
 }
 
 // NB: batches of 64 slots per wave.
@@ -119,7 +154,13 @@ __global__ __launch_bounds__(kThreads) void plan_place(PlanArgs p) {
     __builtin_amdgcn_wave_barrier();
   }
   // total and base, in whole numbers (any order of additions gives the same)
-  if (p.hist) {
+  if (p.total) {
+    for (int g = tid; g < G; g += kThreads) {
+      total[g] = p.total[g];
+      // workgroups past the last chunk have no slots
+      base[g] = (int)blockIdx.x < p.chunks ? p.hist[(long)g * p.chunks_up4 + blockIdx.x] : 0;
+    }
+  } else if (p.hist) {
     // threads take (expert, four chunks) pairs
     const int quads = p.chunks_up4 / 4;
     for (int i = tid; i < G * quads; i += kThreads) {
@@ -250,6 +291,12 @@ int plan(PlanArgs p, void* ws, hipStream_t stream) {
     hipLaunchKernelGGL(plan_count, dim3(p.chunks), dim3(kThreads), 0, stream, p.ids, hist, p.S, p.G, p.chunks_up4);
     if (hipGetLastError() != hipSuccess) return FG_ELAUNCH;
     p.hist = hist;
+    if ((long)p.G * p.chunks > kSumEntries) {
+      int32_t* total = hist + (long)p.G * p.chunks_up4;
+      hipLaunchKernelGGL(plan_prefix, dim3((p.G + 3) / 4), dim3(256), 0, stream, hist, total, p.G, p.chunks, p.chunks_up4);
+      if (hipGetLastError() != hipSuccess) return FG_ELAUNCH;
+      p.total = total;
+    }
     const int grid = fill > p.chunks ? fill : p.chunks;
     hipLaunchKernelGGL((plan_place<kBatches>), dim3(grid), dim3(kThreads), lds, stream, p);
   } else {
@@ -274,7 +321,7 @@ int fg_plan_capacity(int T, int k, int G, int align, int* rows) {
 int fg_plan_workspace(int T, int k, int G, size_t* bytes) {
   if (!sizes_ok(T, k, G) || !bytes) return FG_EINVAL;
   const int S = T * k;
-  *bytes = S <= kRecount ? 0 : (size_t)up4(chunks_of(S)) * G * sizeof(int32_t);
+  *bytes = S <= kRecount ? 0 : ((size_t)up4(chunks_of(S)) + 1) * G * sizeof(int32_t);
   return FG_OK;
 }
 
