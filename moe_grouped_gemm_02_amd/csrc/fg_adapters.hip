@@ -15,18 +15,19 @@
 //           columns; h is summed over the parts, scaled, and cut into three bf16 of
 //           eight bits each, which hold all 24 bits of it: the work is bound by moving
 //           D, not by the matrix cores (T 8192, N 4096, R 64: 39.6 us, 39.1 with two
-//           pieces, which hold 17 bits). For R <= 16 the two lower pieces fit one
+//           pieces, whose 17 bits let 0.16% of the outputs miss the correctly rounded
+//           bf16; with three it is 0.02%). For R <= 16 the two lower pieces fit one
 //           32-deep MFMA, one against k 0..15 and one against k 16..31 with B's
 //           fragment repeated.
 // Each has a kernel for 16-row tiles (decode), where A and B are read once and go
 // straight into fragments, and one for 64-row tiles (prompts), where four waves share
 // them through LDS.
 //
-// Floors and times. T 8192, L 8, R 64, K 7168, N 4096 moves 257 MB: 49 us at the 5.25
-// TB/s of a large copy; shrink takes 27 us (37 where 124 or more tiles are in use: some
-// compute units then hold three of its workgroups, and at about 25 bytes a clock their
-// loads into LDS are the limit), expand 37-39. 64 tokens of 64 adapters, R 16: 15 MB and
-// two launches, 6.2 and 5.6 us, mostly latency: plan, rows, operands one after another.
+// Times. T 8192, L 8, R 64, K 7168, N 4096 moves 263 MB: 50 us at the 5.25 TB/s of a
+// large copy; shrink takes 27 us (37 where 124 or more tiles are in use: some compute
+// units then hold three of its workgroups, and at about 25 bytes a clock their loads
+// into LDS are the limit), expand 39-40. 64 tokens of 64 adapters, R 16: 15 MB and two
+// launches, 6.2 and 6.0 us, mostly latency: plan, rows, operands one after another.
 // 16- against 64-row tiles, both launches: R 16, L 8, T 128 / 256 / 1024: 9.7 / 11.0 /
 // 17.1 against 10.6 / 10.7 / 14.4 us; L 64, T 1024 / 2048 19.5 / 25.8 against 21.3 / 21.6:
 // 64 pays from about 32 tokens an adapter on.

@@ -235,8 +235,8 @@ __device__ __forceinline__ void reduce_dw(float* acc, float (*part)[kGradChoices
   __syncthreads();
 }
 
-// The bytes of y (all choices, T k N of them) from which combine_grad reads it past the
-// caches. With dy / dw alone, N 7168, k 8, bf16: T 2048 116.6 / 60.2 -> 94.9 / 55.0 us, T
+// The bytes of y (all choices, T k N of them; how many have a row here the host does not
+// know) from which combine_grad reads it past the caches. With dy / dw alone, N 7168, k 8, bf16: T 2048 116.6 / 60.2 -> 94.9 / 55.0 us, T
 // 8192 400 / 179 -> 402 / 165; N 2048, k 8, T 8192 113 / 54 -> 98 / 49. Below, shorter
 // batches lose: N 2048, k 8, T 1024 (34 MB) 13.3 / 9.0 -> 15.2 / 9.8 us. Stores of dy past
 // them, and y in the E4M3 form, where a lane reads 32 bytes in two pieces, gain at some

@@ -89,10 +89,13 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 }
 
 // A 16-byte store, past the caches where STREAM. (A template: the two sides of a branch
-// become one ordinary store.) Outputs larger than the
-// L2s together (32 MB) go that way: no reader finds them there, and a kernel that leaves
-// the L2s full of them makes the next one wait for the write-back (combine of T 8192, k 4,
-// N 7168 every 117.6 -> 113.8 us, adapters of T 8192, N 4096 75.2 -> 71.3 us a call).
+// become one ordinary store.) Outputs larger than the L2s together (32 MB) go that way:
+// no reader finds them there, and a kernel that leaves the L2s full of them makes the
+// next one wait for the write-back. Ordinary / past the caches, calls one after another:
+// on new inputs and outputs each time, combine of T 8192, k 4, N 7168 118.8 / 114.6 us,
+// adapters of T 8192, N 4096 73-79 / 72-75 us. Into the same output again and again,
+// which the 256 MB last-level cache then keeps, it is the other way: 110.2 / 115 and
+// 67 / 68.6 us; a call alone 130 / 135 and 93 / 98 us.
 template <bool STREAM>
 __device__ __forceinline__ void store16(u32x4* p, u32x4 v) {
   if constexpr (STREAM) __builtin_nontemporal_store(v, p);
