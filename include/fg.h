@@ -377,6 +377,81 @@ int fg_adapters(const void* D, const void* x, const void* A, const void* B, cons
                 const int32_t* slots, const int32_t* m_indices, const int32_t* offsets, void* out, void* ws, int T,
                 int L, int R, int K, int N, int cap, int align, hipStream_t stream);
 
+/*
+ * 8-bit integer products, an alternative to the E4M3 ones with one fp32 scale per
+ * row of A (token) and per row of B (output channel):
+ *   D[m, n] = sa[m] * sb[n] * sum_k A[m, k] * B[n, k],
+ * the sum in 32-bit integers (exact), then fp32, rounded once to bf16. Layouts,
+ * ownership and row rules as fg_gemm_fp8_nt, fg_grouped_contiguous and
+ * fg_grouped_masked, except:
+ *   A, B: signed 8-bit integers (any value, -128 too); sa [M] fp32 (masked [G][M_max]), sb [N]
+ *   (grouped [G][N]).
+ *   K is a multiple of 16 up to 131056, N a multiple of 8 up to 4194296. M * K and
+ *   N * K have no limit of their own.
+ * Results are bitwise reproducible and do not depend on the tile or the layout.
+ */
+int fg_gemm_int8_nt(const void* A, const float* sa, const void* B, const float* sb, void* D, int M, int N, int K,
+                    hipStream_t stream);
+int fg_grouped_contiguous_int8(const void* A, const float* sa, const void* B, const float* sb, void* D,
+                               const int32_t* m_indices, int M, int N, int K, int G, hipStream_t stream);
+int fg_grouped_masked_int8(const void* A, const float* sa, const void* B, const float* sb, void* D,
+                           const int32_t* masked_m, int G, int M_max, int N, int K, hipStream_t stream);
+
+/*
+ * Their operands: rows as 8-bit integers with one scale each,
+ *   s = max(amax / 127, 2^-126) (1 for a row of zeros), q = v / s to the nearest
+ *   integer, ties to even (the quotient rounded to fp32 first), so |q| <= 127.
+ * A row that holds an infinity or NaN gets it as its scale (its codes say nothing).
+ *   fg_quant_int8: v = x [M][K] bf16 or fp32: activations (a row per token) or weights
+ *     (a row per output channel). q [M][K], s [M].
+ *   fg_dispatch_quant_int8: v = w[t][j] * x[t] (w NULL: x[t]) into row rows[t][j] of
+ *     Q [n_rows][H] and s [n_rows]; a row outside [0, n_rows) is skipped, rows must be
+ *     distinct. A masked plan's Q is [G][M_max][H], n_rows = G * M_max.
+ *   fg_swiglu_quant_int8: v = silu(gate) * up of h [rows][2 I], whose columns
+ *     interleave gate and up every 128 (as the fused calls above): Q [rows][I], s
+ *     [rows]. slots (a plan's, or NULL): rows whose slot is below 0 are neither read
+ *     nor written. I % 128 == 0.
+ * K, H, I: multiples of 16 up to 65536. x, h, q, Q 16-byte aligned. dtype: of x or h.
+ */
+int fg_quant_int8(const void* x, int dtype, void* q, float* s, int M, int K, hipStream_t stream);
+int fg_dispatch_quant_int8(const void* x, int dtype, const int32_t* rows, const float* w, void* Q, float* s, int T,
+                           int k, int H, int n_rows, hipStream_t stream);
+int fg_swiglu_quant_int8(const void* h, int dtype, const int32_t* slots, void* Q, float* s, int rows, int I,
+                         hipStream_t stream);
+
+/*
+ * Norms around a block, with the block's gate and the residual scales, in one pass:
+ *   u = y / sqrt(mean(y^2) + eps) * post       (y itself where post is NULL)
+ *   r = alpha * x + beta * gate * u            (x itself where y is NULL: r is not written)
+ *   h = r / sqrt(mean(r^2) + eps) * pre        (pre NULL: no h), of r before its rounding
+ * x (the residual stream), y (a block's output), r [T][N], bf16 or fp32 (dtype), 16-byte aligned; pre,
+ * post [N] fp32; gate fp32, [N] (FG_GATE_CHANNEL) or [T] (FG_GATE_TOKEN), NULL for FG_GATE_NONE.
+ * r may be x or y, and h may be either where it has their type.
+ *   out: FG_OUT_SAME: h [T][N] in x's type, s unused. FG_OUT_E4M3 / FG_OUT_E4M3_POW2: codes
+ *   h [T][N] and scales s [N/128][T] as fg_quant_act_1x128(_pow2) makes them (N % 128 == 0; r finite).
+ *   FG_OUT_INT8: codes h [T][N] and s [T] as fg_quant_int8 (N % 16 == 0).
+ * N % 8 == 0, 8 <= N <= 16384, eps > 0. All arithmetic in fp32, one rounding an output.
+ */
+enum { FG_GATE_NONE = 0, FG_GATE_CHANNEL = 1, FG_GATE_TOKEN = 2 };
+enum { FG_OUT_SAME = 0, FG_OUT_E4M3 = 1, FG_OUT_E4M3_POW2 = 2, FG_OUT_INT8 = 3 };
+int fg_block_norm(const void* x, const void* y, int dtype, const float* pre, const float* post, const float* gate,
+                  int gate_kind, void* r, void* h, float* s, int out, int T, int N, float alpha, float beta, float eps,
+                  hipStream_t stream);
+
+/*
+ * Its gradient, at r as it was stored (an 8-bit h's rounding is passed over). dh: gradient
+ * of h (with pre; NULL without), dr: of r from what else reads it (NULL: none); one of them
+ * at least. dx [T][N], and with y: dy [T][N], in r's type; fp32: dpre [N] (with pre), dpost [N]
+ * (with post), dgate [N] or [T] (with gate). Outputs of parts that are not there may be NULL.
+ * dx may be dr or dh; dy may be y. T == 0 writes zeros to dpre, dpost and a channel's dgate.
+ * ws: fg_block_norm_grad_workspace bytes, 16-byte aligned. The sums over tokens are
+ * fp32 in an order that depends on T and N alone.
+ */
+int fg_block_norm_grad_workspace(int T, int N, size_t* bytes);
+int fg_block_norm_grad(const void* r, const void* dh, const void* dr, const void* y, int dtype, const float* pre,
+                       const float* post, const float* gate, int gate_kind, void* dx, void* dy, float* dgate, float* dpre,
+                       float* dpost, void* ws, int T, int N, float alpha, float beta, float eps, hipStream_t stream);
+
 /* Static, human-readable description of a return code. */
 const char* fg_strerror(int code);
 

@@ -20,6 +20,13 @@ Row operators around the grouped calls (route_topk, plan_contiguous, plan_masked
 dispatch_quant, combine and their gradients) and beside the dense one (adapters):
 see their own docstrings; token rows are [T, columns] in bfloat16 or float32,
 choices [T, k] int32, weights [T, k] float32.
+
+The same products in 8-bit integers (gemm_int8_nt, grouped_contiguous_int8,
+grouped_masked_int8): A and B int8, sa [M] and sb [N] float32, one scale per token and
+per output channel (masked: sa [G, M_max]; grouped: sb [G, N]); quant_int8,
+dispatch_quant_int8 and swiglu_quant_int8 make their operands. block_norm and
+block_norm_grad: the norms before and after a block with its gate and residual scales,
+their output in the row's type or as either product's operand.
 """
 import ctypes
 import functools
@@ -71,6 +78,15 @@ def _declare(L):
     L.fg_combine_grad_quant.argtypes = [vp, vp, i, ip, fp, vp, fp, fp, i, i, i, i, i, i, vp]
     L.fg_adapters_workspace.argtypes = [i, i, i, i, sz]
     L.fg_adapters.argtypes = [vp, vp, vp, vp, fp, ip, ip, ip, ip, vp, vp, i, i, i, i, i, i, i, vp]
+    L.fg_gemm_int8_nt.argtypes = [vp, fp, vp, fp, vp, i, i, i, vp]
+    L.fg_grouped_contiguous_int8.argtypes = L.fg_grouped_contiguous.argtypes
+    L.fg_grouped_masked_int8.argtypes = L.fg_grouped_masked.argtypes
+    L.fg_quant_int8.argtypes = [vp, i, vp, fp, i, i, vp]
+    L.fg_dispatch_quant_int8.argtypes = [vp, i, ip, fp, vp, fp, i, i, i, i, vp]
+    L.fg_swiglu_quant_int8.argtypes = [vp, i, ip, vp, fp, i, i, vp]
+    L.fg_block_norm.argtypes = [vp, vp, i, fp, fp, fp, i, vp, vp, fp, i, i, i, f, f, f, vp]
+    L.fg_block_norm_grad_workspace.argtypes = [i, i, sz]
+    L.fg_block_norm_grad.argtypes = [vp, vp, vp, vp, i, fp, fp, fp, i, vp, vp, fp, fp, fp, vp, i, i, f, f, f, vp]
     L.fg_strerror.argtypes = [i]
     L.fg_strerror.restype = ctypes.c_char_p
     for name in ENTRY_POINTS:
@@ -88,6 +104,9 @@ ENTRY_POINTS = ("fg_gemm_fp8_nt", "fg_grouped_contiguous", "fg_grouped_masked",
                 "fg_route_topk", "fg_route_topk_grad", "fg_plan_capacity", "fg_plan_workspace",
                "fg_plan_contiguous", "fg_plan_masked", "fg_dispatch_quant", "fg_combine",
                "fg_combine_grad", "fg_combine_grad_quant", "fg_adapters_workspace", "fg_adapters",
+               "fg_gemm_int8_nt", "fg_grouped_contiguous_int8", "fg_grouped_masked_int8", "fg_quant_int8",
+               "fg_dispatch_quant_int8", "fg_swiglu_quant_int8", "fg_block_norm", "fg_block_norm_grad_workspace",
+               "fg_block_norm_grad",
                "fg_strerror")
 
 
@@ -755,3 +774,234 @@ def adapters(D, x, A, B, scales, plan, out=None):
     _call("fg_adapters", dev, _ptr(D), _ptr(x), _ptr(A), _ptr(B), _ptr(scales), _ptr(plan.rows), _ptr(plan.slots),
           _ptr(plan.m_indices), _ptr(plan.offsets), _ptr(out), _ptr(ws), T, L, R, K, N, plan.capacity, plan.align, _stream(D))
     return out
+
+
+# ---------------------------------------------------------------- 8-bit integers
+def _int8(t, name, shape, dev=None):
+    _dev(t, name, shape, _torch().int8, dev)
+
+
+def _int8_product(A, sa, B, sb, D, lead, N, K):
+    """Checks of the operands of an integer product; lead: the leading dimensions of A and D."""
+    torch = _torch()
+    dev = A.device
+    _int8(A, "A", lead + (K,))
+    _int8(B, "B", B.shape, dev)
+    if K % 16 or not 16 <= K <= 131056 or N % 8:
+        raise ValueError("K must be a multiple of 16 from 16 to 131056 and N of 8")
+    _dev(sa, "sa", lead, torch.float32, dev)
+    _dev(sb, "sb", B.shape[:-1], torch.float32, dev)
+    _dev(D, "D", lead + (N,), torch.bfloat16, dev)
+    return dev
+
+
+def gemm_int8_nt(A, sa, B, sb, D):
+    """Dense D[m, n] = sa[m] sb[n] sum_k A[m, k] B[n, k]: A [M, K] and B [N, K] int8, sa [M] and
+    sb [N] float32, the sum exact in 32-bit integers; writes D [M, N] bfloat16 in place."""
+    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+        raise ValueError(f"A must be [M, K] and B [N, K], got {tuple(A.shape)} and {tuple(B.shape)}")
+    (M, K), N = A.shape, B.shape[0]
+    dev = _int8_product(A, sa, B, sb, D, (M,), N, K)
+    _call("fg_gemm_int8_nt", dev, _ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(D), M, N, K, _stream(A))
+    return D
+
+
+def grouped_contiguous_int8(A, sa, B, sb, D, m_indices):
+    """gemm_int8_nt in the contiguous layout: rows of A belong to expert m_indices[row] (-1 =
+    padding, not written); B [G, N, K], sb [G, N]."""
+    if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
+        raise ValueError(f"A must be [M, K] and B [G, N, K], got {tuple(A.shape)} and {tuple(B.shape)}")
+    (M, K), (G, N) = A.shape, B.shape[:2]
+    dev = _int8_product(A, sa, B, sb, D, (M,), N, K)
+    _dev(m_indices, "m_indices", (M,), _torch().int32, dev)
+    _call("fg_grouped_contiguous_int8", dev, _ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(D), _ptr(m_indices), M, N, K, G,
+          _stream(A))
+    return D
+
+
+def grouped_masked_int8(A, sa, B, sb, D, masked_m):
+    """gemm_int8_nt in the masked layout: expert g has masked_m[g] valid rows of A[g], and only
+    those of D[g] are written; A [G, M_max, K], sa [G, M_max], B [G, N, K], sb [G, N]."""
+    if A.dim() != 3 or B.dim() != 3 or A.shape[2] != B.shape[2] or A.shape[0] != B.shape[0]:
+        raise ValueError(f"A must be [G, M_max, K] and B [G, N, K], got {tuple(A.shape)} and {tuple(B.shape)}")
+    (G, M_max, K), N = A.shape, B.shape[1]
+    dev = _int8_product(A, sa, B, sb, D, (G, M_max), N, K)
+    _dev(masked_m, "masked_m", (G,), _torch().int32, dev)
+    _call("fg_grouped_masked_int8", dev, _ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(D), _ptr(masked_m), G, M_max, N, K,
+          _stream(A))
+    return D
+
+
+def _int8_rows(lead, K, q, s, dev):
+    """Outputs of an integer quantiser: codes [*lead, K] and scales lead."""
+    torch = _torch()
+    if K % 16 or not 16 <= K <= 65536:
+        raise ValueError("rows must be a multiple of 16 long, from 16 to 65536")
+    return _new(q, "q", lead + (K,), torch.int8, dev), _new(s, "s", lead, torch.float32, dev)
+
+
+def quant_int8(x, q=None, s=None):
+    """Rows of x [..., K] (bf16 or fp32; activations, or weights whose rows are output channels) as
+    8-bit integers with one scale each: (q int8 in x's shape, s [...] fp32), x about q * s."""
+    dt = _elem(x, "x")
+    if x.dim() < 2:
+        raise ValueError("x must be [..., rows, K]")
+    lead, K = x.shape[:-1], x.shape[-1]
+    _dev(x, "x", x.shape)
+    q, s = _int8_rows(lead, K, q, s, x.device)
+    _call("fg_quant_int8", x.device, _ptr(x), dt, _ptr(q), _ptr(s), lead.numel(), K, _stream(x))
+    return q, s
+
+
+def dispatch_quant_int8(x, plan, w=None, Q=None, s=None):
+    """Token rows x [T, H] (bf16 or fp32), times w [T, k] if given, into the plan's layout as the
+    grouped integer product's A operand: Q int8 ([capacity, H] or [G, M_max, H]) and s ([capacity]
+    or [G, M_max]). Rows without a slot are not written."""
+    dt = _elem(x, "x")
+    dev, T, k = plan.device, plan.T, plan.k
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [{T}, columns]")
+    H = x.shape[1]
+    _dev(x, "x", (T, H), None, dev)
+    if w is not None:
+        _dev(w, "w", (T, k), _torch().float32, dev)
+    Q, s = _int8_rows(plan.lead, H, Q, s, dev)
+    _call("fg_dispatch_quant_int8", dev, _ptr(x), dt, _ptr(plan.rows), _opt_ptr(w), _ptr(Q), _ptr(s), T, k, H,
+          plan.capacity, _stream(x))
+    return Q, s
+
+
+def swiglu_quant_int8(h, plan=None, Q=None, s=None):
+    """silu(gate) * up of a first projection's output h [..., 2 I] (bf16 or fp32; gate and up
+    interleaved every 128 columns) as the next integer product's operand: Q int8 [..., I], s [...].
+    With a plan h is in its layout, and rows without a slot are neither read nor written."""
+    dt = _elem(h, "h")
+    if h.dim() < 2 or h.shape[-1] % 256:
+        raise ValueError("h must be [..., rows, 2 I] with 2 I a multiple of 256")
+    lead, I = h.shape[:-1], h.shape[-1] // 2
+    dev = h.device
+    _dev(h, "h", h.shape)
+    if plan is not None and (lead != plan.lead or dev != plan.device):
+        raise ValueError(f"h has shape {tuple(h.shape)} on {dev}, the plan's rows are {plan.lead} on {plan.device}")
+    Q, s = _int8_rows(lead, I, Q, s, dev)
+    _call("fg_swiglu_quant_int8", dev, _ptr(h), dt, None if plan is None else _ptr(plan.slots), _ptr(Q), _ptr(s),
+          lead.numel(), I, _stream(h))
+    return Q, s
+
+
+# ---------------------------------------------------------------- norms around a block
+NORM_OUTPUTS = {None: 0, "e4m3": 1, "e4m3_pow2": 2, "int8": 3}
+
+
+def _norm_args(x, name, y, pre, post, gate, eps):
+    """Checks what block_norm and its gradient share: (element type, T, N, gate kind)."""
+    dt = _elem(x, name)
+    f32 = _torch().float32
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [T, N], got {tuple(x.shape)}")
+    T, N = x.shape
+    dev = x.device
+    _dev(x, name, (T, N))
+    if N % 8 or not 8 <= N <= 16384:
+        raise ValueError("N must be a multiple of 8 from 8 to 16384")
+    if not eps > 0:
+        raise ValueError("eps must be positive")
+    if y is not None:
+        _dev(y, "y", (T, N), x.dtype, dev)
+    elif post is not None or gate is not None:
+        raise ValueError("post and gate belong to a block's output y")
+    if pre is not None:
+        _dev(pre, "pre", (N,), f32, dev)
+    if post is not None:
+        _dev(post, "post", (N,), f32, dev)
+    if gate is None:
+        return dt, T, N, 0
+    if gate.dim() == 1:
+        _dev(gate, "gate", (N,), f32, dev)
+        return dt, T, N, 1
+    _dev(gate, "gate", (T, 1), f32, dev)
+    return dt, T, N, 2
+
+
+def block_norm(x, y=None, pre=None, post=None, gate=None, alpha=1.0, beta=1.0, eps=1e-6, quant=None, r=None, h=None, s=None):
+    """The norms around a block in one pass, x [T, N] the residual stream and y [T, N] the block's
+    output (both bf16 or both fp32):
+
+        u = y / sqrt(mean y^2 + eps) * post       (y itself without post [N] fp32)
+        r = alpha x + beta gate u                 (x itself without y; gate fp32 [N] or [T, 1], or none)
+        h = r / sqrt(mean r^2 + eps) * pre        (None without pre [N] fp32), of r before its rounding
+
+    Returns (r, h, s). quant None: h in x's type, s None; "e4m3" or "e4m3_pow2": h the E4M3 product's
+    operand (uint8 codes) with its scales s [N/128, T]; "int8": the integer product's (int8 codes, s [T]).
+    r may be x or y (in place)."""
+    torch = _torch()
+    if quant not in NORM_OUTPUTS:
+        raise ValueError(f"quant must be one of {list(NORM_OUTPUTS)}, got {quant!r}")
+    if y is None and pre is None:
+        raise ValueError("block_norm needs a block's output y, the next norm's weight pre, or both")
+    dt, T, N, kind = _norm_args(x, "x", y, pre, post, gate, eps)
+    dev, out = x.device, NORM_OUTPUTS[quant]
+    if pre is None and quant is not None:
+        raise ValueError("quant is for h, which needs pre")
+    if y is not None:
+        r = _new(r, "r", (T, N), x.dtype, dev)
+    elif r is not None and r is not x:
+        raise ValueError("without y the stream is x itself")
+    if pre is None:
+        h = s = None
+    elif out == 0:
+        h, s = _new(h, "h", (T, N), x.dtype, dev), None
+    elif out == 3:
+        h, s = _int8_rows((T,), N, h, s, dev)
+        h = h.view(T, N)
+    else:
+        if N % 128:
+            raise ValueError("E4M3 rows must be a multiple of 128 long")
+        if h is None:
+            h = torch.empty((T, N), dtype=torch.uint8, device=dev)
+        else:
+            _fp8(h, "h", (T, N), dev)
+        s = _new(s, "s", (N // 128, T), torch.float32, dev)
+    _call("fg_block_norm", dev, _ptr(x), _opt_ptr(y), dt, _opt_ptr(pre), _opt_ptr(post), _opt_ptr(gate), kind,
+          None if y is None else _ptr(r), _opt_ptr(h), _opt_ptr(s), out, T, N, alpha, beta, eps, _stream(x))
+    return (x if y is None else r), h, s
+
+
+@functools.lru_cache(maxsize=1024)
+def _block_norm_grad_workspace(T, N):
+    size = ctypes.c_size_t()
+    _check(lib().fg_block_norm_grad_workspace(T, N, ctypes.byref(size)), "fg_block_norm_grad_workspace")
+    return size.value
+
+
+def block_norm_grad(r, dh=None, dr=None, y=None, pre=None, post=None, gate=None, alpha=1.0, beta=1.0, eps=1e-6,
+                    dx=None, dy=None):
+    """Gradient of block_norm at the stream r it returned: dh the gradient of h (with pre), dr that of r from
+    what else reads it (None: none), the other arguments as in the forward call (pre None if h was not used).
+    Returns (dx, dy, dgate, dpre, dpost): dx and dy in r's type, the vectors fp32; None where the forward call
+    had no such input. dx may be dr or dh, dy may be y (in place)."""
+    torch = _torch()
+    f32 = torch.float32
+    if (dh is None) != (pre is None):
+        raise ValueError("dh and pre belong together")
+    if dh is None and dr is None:
+        raise ValueError("block_norm_grad needs dh, dr, or both")
+    dt, T, N, kind = _norm_args(r, "r", y, pre, post, gate, eps)
+    dev = r.device
+    if dh is not None:
+        _dev(dh, "dh", (T, N), r.dtype, dev)
+    if dr is not None:
+        _dev(dr, "dr", (T, N), r.dtype, dev)
+    dx = _new(dx, "dx", (T, N), r.dtype, dev)
+    if y is not None:
+        dy = _new(dy, "dy", (T, N), r.dtype, dev)
+    elif dy is not None:
+        raise ValueError("dy is y's gradient, and there is no y")
+    dgate = None if gate is None else torch.empty(gate.shape, dtype=f32, device=dev)
+    dpre = None if pre is None else torch.empty(N, dtype=f32, device=dev)
+    dpost = None if post is None else torch.empty(N, dtype=f32, device=dev)
+    ws = torch.empty(_block_norm_grad_workspace(T, N), dtype=torch.uint8, device=dev)
+    _call("fg_block_norm_grad", dev, _ptr(r), _opt_ptr(dh), _opt_ptr(dr), _opt_ptr(y), dt, _opt_ptr(pre), _opt_ptr(post),
+          _opt_ptr(gate), kind, _ptr(dx), _opt_ptr(dy), _opt_ptr(dgate), _opt_ptr(dpre), _opt_ptr(dpost), _ptr(ws), T, N,
+          alpha, beta, eps, _stream(r))
+    return dx, dy, dgate, dpre, dpost

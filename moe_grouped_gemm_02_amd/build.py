@@ -4,15 +4,16 @@ Run ``python -m moe_grouped_gemm_02_amd.build`` (or call ``build()``). The
 shared object is written next to this file so that it travels with the source
 tree; nothing is installed elsewhere. The GEMM kernels of each layout and scale
 kind are compiled as separate objects (fg_launch.hip with FG_LAUNCH_PART =
-2 * layout + pow2), in parallel, then linked with the host and quantiser code
-and the row operators (routing, sorting, row movement, adapters).
+2 * layout + pow2), in parallel, then linked with the host and quantiser code,
+the row operators (routing, sorting, row movement, adapters), the 8-bit integer
+products (one object per layout) with their quantisers, and the block norms.
 
 libfg_ceiling.so (fg_ceiling.hip) is a benchmark helper that bench.py loads to
 measure the matrix cores' ceiling on this device; the library does not use it.
 
 A second library, libfg_testing.so, links the same kernel objects with the
 host code built with FG_TESTING: it adds a per-thread tile override
-(fgt_force_tile) that the test suite uses to run every compiled tile. The
+(fgt_force_tile, fgt_force_int8) that the test suite uses to run every compiled tile. The
 product library carries no such state.
 """
 import os
@@ -30,9 +31,13 @@ LAUNCH_PARTS = 6   # {dense, contiguous, masked} x {fp32 scales, power-of-two sc
 # (object name, source, extra flags)
 UNITS = [("fg_host", "fg_host.hip", []), ("fg_host_testing", "fg_host.hip", ["-DFG_TESTING"]),
          ("fg_quant", "fg_quant.hip", []), ("fg_route", "fg_route.hip", []), ("fg_plan", "fg_plan.hip", []),
-         ("fg_rows", "fg_rows.hip", []), ("fg_adapters", "fg_adapters.hip", []), ("fg_ceiling", "fg_ceiling.hip", [])] + [
-    (f"fg_launch_{i}", "fg_launch.hip", [f"-DFG_LAUNCH_PART={i}"]) for i in range(LAUNCH_PARTS)]
-HEADERS = ["fg_kernel.hpp", "fg_e4m3.hpp", "fg_e4m3_quot.hpp", "fg_tiles.hpp", "fg_device.hpp", "fg_wave.hpp"]
+         ("fg_rows", "fg_rows.hip", []), ("fg_adapters", "fg_adapters.hip", []), ("fg_ceiling", "fg_ceiling.hip", []),
+         ("fg_int8", "fg_int8.hip", []), ("fg_int8_testing", "fg_int8.hip", ["-DFG_TESTING"]),
+         ("fg_int8_rows", "fg_int8_rows.hip", []), ("fg_norm", "fg_norm.hip", [])] + [
+    (f"fg_launch_{i}", "fg_launch.hip", [f"-DFG_LAUNCH_PART={i}"]) for i in range(LAUNCH_PARTS)] + [
+    (f"fg_int8_launch_{i}", "fg_int8_launch.hip", [f"-DFG_INT8_LAYOUT={i}"]) for i in range(3)]
+HEADERS = ["fg_kernel.hpp", "fg_e4m3.hpp", "fg_e4m3_quot.hpp", "fg_tiles.hpp", "fg_device.hpp", "fg_wave.hpp",
+           "fg_int8_kernel.hpp", "fg_int8_tiles.hpp", "fg_int8_quot.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -74,11 +79,10 @@ def build(verbose=False, jobs=None):
             failed.append(name)
     if failed:
         raise RuntimeError("hipcc failed building " + ", ".join(failed))
-    host = os.path.join(OBJ, "fg_host.o")
-    host_t = os.path.join(OBJ, "fg_host_testing.o")
-    ceiling = os.path.join(OBJ, "fg_ceiling.o")
-    common = [o for o in objs if o not in (host, host_t, ceiling)]
-    for out, link in ((LIB, [host, *common]), (TESTING_LIB, [host_t, *common]), (CEILING_LIB, [ceiling])):
+    at = lambda *names: [os.path.join(OBJ, n + ".o") for n in names]  # noqa: E731
+    host, host_t, ceiling = at("fg_host", "fg_int8"), at("fg_host_testing", "fg_int8_testing"), at("fg_ceiling")
+    common = [o for o in objs if o not in host + host_t + ceiling]
+    for out, link in ((LIB, [*host, *common]), (TESTING_LIB, [*host_t, *common]), (CEILING_LIB, ceiling)):
         cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *link, "-o", out + ".tmp"]
         if verbose:
             print(" ".join(cmd), flush=True)

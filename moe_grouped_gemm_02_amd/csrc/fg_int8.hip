@@ -1,0 +1,187 @@
+// fg_int8.hip -- host side of the 8-bit integer product: argument validation, tile
+// choice and launch behind the C ABI declared in include/fg.h.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "fg.h"
+#include "fg_device.hpp"
+#include "fg_int8_tiles.hpp"
+
+namespace {
+
+using namespace fg;
+using namespace fg::int8_cfg;
+
+struct Tile {
+  int bm, bn, waves;
+  double eff;   // fraction of the matrix-core rate the tile's K loop sustains
+};
+constexpr Tile kTiles[] = {{256, 256, Cfg0::W, 0.80}, {256, 128, Cfg1::W, 0.75}, {128, 256, Cfg2::W, 0.75},
+                           {128, 128, Cfg3::W, 0.70}, {64, 128, Cfg4::W, 0.60}};
+constexpr int kNumTiles = sizeof(kTiles) / sizeof(kTiles[0]);
+constexpr int kWide = 0, kNarrow = 1, kHalf = 2;
+constexpr int kMaxK = 131056;     // 128^2 K < 2^31: the 32-bit sum is exact
+constexpr int kMaxN = 4194296;    // 256 rows of N bf16 stay below 2^31 bytes
+
+long ceil_div(long a, long b) { return (a + b - 1) / b; }
+
+// Estimated cycles of one tile over kblocks K-blocks: its matrix-core time at 8192
+// operations per clock, or its loads into LDS at what the path sustains, and a start and end.
+double tile_cycles(const Tile& t, double kblocks) {
+  const double mfma = t.bm * t.bn * 256.0 / (8192.0 * t.eff), mem = (t.bm + t.bn) * 128.0 / (t.waves >= 8 ? 30.0 : 24.0);
+  return kblocks * (mfma > mem ? mfma : mem) + 4000.0;
+}
+
+#ifdef FG_TESTING
+// Test build only (libfg_testing.so): this thread's later calls run on one of the compiled
+// choices, with at most so many workgroups where these walk their tiles.
+thread_local int t_tile = -1, t_grid = 0;
+#endif
+
+struct Choice {
+  int tile = -1;
+  long grid = 0, tiles_a = 0;
+  int n_split = 0;
+};
+
+// The shape whose tiles, in rounds over the compute units, take the fewest estimated
+// cycles; dense problems also try whole rounds of 256x256 tiles with the remaining
+// columns on 256x128, contiguous ones the run-following kernel.
+Choice choose(int layout, int M, int N, int K, int G, int cus) {
+  Choice best;
+  double cost = 0.0;
+  const double kb = (double)ceil_div(K, 128);
+  for (int i = 0; i < kNumTiles; ++i) {
+    const Tile& t = kTiles[i];
+    if (layout == FG_LAYOUT_CONTIGUOUS && t.bm > 128) continue;   // a tile's rows are one expert's
+    const long tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn) * (layout == FG_LAYOUT_MASKED ? G : 1);
+    const double c = (double)ceil_div(tiles, cus) * tile_cycles(t, kb);
+    if (best.tile < 0 || c < cost) {
+      best.tile = i;
+      best.grid = tiles;
+      cost = c;
+    }
+  }
+  if (layout == FG_LAYOUT_CONTIGUOUS && ceil_div(M, 128) <= kRunMaxBlocks && G <= kRunMaxExperts) {
+    // G runs, half of them odd: full two-block tiles and single blocks per column
+    const long nblk = ceil_div(M, 128), runs = G < nblk ? G : nblk, S = runs / 2, F = (nblk - S) / 2;
+    const long tn = ceil_div(N, 256), items = nblk * tn, grid = items < cus ? items : cus;
+    const double tf = tile_cycles(kTiles[kWide], kb), th = tile_cycles(kTiles[kHalf], kb);
+    const long full = F * tn, rest = full % grid;
+    const double c = rest && 2 * rest + S * tn <= grid ? (double)(full / grid) * tf + th
+                                                       : (double)ceil_div(full, grid) * tf + (double)ceil_div(S * tn, grid) * th;
+    if (c < cost) {
+      best.tile = kRuns;
+      best.grid = grid;
+      cost = c;
+    }
+  }
+  if (layout == FG_LAYOUT_DENSE) {
+    const long tm = ceil_div(M, 256);
+    for (long nc = N / 256 * 256; nc >= 256; nc -= 256) {
+      const long a = tm * (nc / 256);
+      if (a % cus) continue;
+      if (nc == N) break;   // whole rounds on the wide tile alone
+      const long b = tm * ceil_div(N - nc, 128);
+      const double c = (double)(a / cus) * tile_cycles(kTiles[kWide], kb) + (double)ceil_div(b, cus) * tile_cycles(kTiles[kNarrow], kb);
+      if (c < cost) {
+        best.tile = kSplit;
+        best.n_split = (int)nc;
+        best.tiles_a = a;
+        best.grid = (a > b ? a : b) < cus ? (a > b ? a : b) : cus;
+      }
+      break;
+    }
+  }
+  return best;
+}
+
+#ifdef FG_TESTING
+bool forced(int layout, int M, int N, int G, int cus, Choice& c) {
+  c = Choice();
+  c.tile = t_tile;
+  if (t_tile < kNumTiles) {
+    const Tile& t = kTiles[t_tile];
+    c.grid = ceil_div(M, t.bm) * ceil_div(N, t.bn) * (layout == FG_LAYOUT_MASKED ? G : 1);
+    return layout != FG_LAYOUT_CONTIGUOUS || t.bm <= 128;
+  }
+  c.grid = t_grid > 0 ? t_grid : cus;
+  if (t_tile == kRuns) return layout == FG_LAYOUT_CONTIGUOUS;
+  c.n_split = N / 512 * 256;
+  c.tiles_a = ceil_div(M, 256) * (c.n_split / 256);
+  return t_tile == kSplit && layout == FG_LAYOUT_DENSE && c.n_split > 0;
+}
+#endif
+
+int run(int layout, const void* A, const float* sa, const void* B, const float* sb, void* D, const int32_t* index,
+        int M, int N, int K, int G, hipStream_t stream) {
+  if (M < 0 || N < 0 || N % 8 || N > kMaxN || K < 16 || K % 16 || K > kMaxK || G < 1) return FG_EINVAL;
+  if (M == 0 || N == 0) return FG_OK;
+  if (!A || !sa || !B || !sb || !D || (layout != FG_LAYOUT_DENSE && !index)) return FG_EINVAL;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(index, 4))
+    return FG_EINVAL;
+  // the smallest tiles' number, a bound of every choice's
+  if ((layout == FG_LAYOUT_MASKED ? G : 1) * ceil_div(M, 64) * ceil_div(N, 128) > 0x7fffffffL) return FG_EINVAL;
+  int cus = 0;
+  const int st = current_device(&cus);
+  if (st != FG_OK) return st;
+  Choice c = choose(layout, M, N, K, G, cus);
+#ifdef FG_TESTING
+  if (t_tile >= 0 && !forced(layout, M, N, G, cus, c)) return FG_EINVAL;
+#endif
+  const Tile& t = kTiles[c.tile < kNumTiles ? c.tile : kWide];
+  Params p = {};
+  p.A = static_cast<const uint8_t*>(A);
+  p.sa = sa;
+  p.B = static_cast<const uint8_t*>(B);
+  p.sb = sb;
+  p.D = static_cast<uint16_t*>(D);
+  p.m_indices = p.masked_m = index;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.G = G;
+  p.KB = (int)ceil_div(K, 128);
+  p.tiles_m = (int)ceil_div(M, t.bm);
+  p.tiles_n = (int)ceil_div(N, t.bn);
+  p.n_split = c.n_split;
+  p.tiles_a = (int)c.tiles_a;
+  hipError_t e;
+  switch (layout) {
+    case FG_LAYOUT_DENSE: e = launch_int8<kDense>(c.tile, p, (int)c.grid, stream); break;
+    case FG_LAYOUT_CONTIGUOUS: e = launch_int8<kContiguous>(c.tile, p, (int)c.grid, stream); break;
+    default: e = launch_int8<kMasked>(c.tile, p, (int)c.grid, stream);
+  }
+  return e == hipSuccess ? FG_OK : FG_ELAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fg_gemm_int8_nt(const void* A, const float* sa, const void* B, const float* sb, void* D, int M, int N, int K,
+                    hipStream_t stream) {
+  return run(FG_LAYOUT_DENSE, A, sa, B, sb, D, nullptr, M, N, K, 1, stream);
+}
+
+int fg_grouped_contiguous_int8(const void* A, const float* sa, const void* B, const float* sb, void* D,
+                               const int32_t* m_indices, int M, int N, int K, int G, hipStream_t stream) {
+  return run(FG_LAYOUT_CONTIGUOUS, A, sa, B, sb, D, m_indices, M, N, K, G, stream);
+}
+
+int fg_grouped_masked_int8(const void* A, const float* sa, const void* B, const float* sb, void* D,
+                           const int32_t* masked_m, int G, int M_max, int N, int K, hipStream_t stream) {
+  return run(FG_LAYOUT_MASKED, A, sa, B, sb, D, masked_m, M_max, N, K, G, stream);
+}
+
+#ifdef FG_TESTING
+int fgt_force_int8(int tile, int grid) {
+  if (tile < -1 || tile > kRuns || grid < 0) return FG_EINVAL;
+  t_tile = tile;
+  t_grid = grid;
+  return FG_OK;
+}
+#endif
+
+}  // extern "C"

@@ -1,0 +1,460 @@
+// fg_int8_kernel.hpp -- gfx950 kernels of the 8-bit integer product
+//
+//     D[m, n] = bf16( sa[m] sb[n] sum_k A[m, k] B[n, k] )
+//
+// in the dense, contiguous and masked layouts. The sum runs in 32-bit integers on
+// the matrix core (v_mfma_i32_16x16x64_i8) and is exact: 128^2 K < 2^31 up to K =
+// 131071, so the result does not depend on tile, layout or order; the only
+// roundings are the sum's to fp32 (24 bits), the two scales' products in fp32 and
+// the last one to bf16.
+//
+// The tiles move as the E4M3 kernels' do (fg_kernel.hpp: global->LDS DMA into
+// XOR-swizzled rings, loads spread over the MFMAs, B rows in pair_column order for
+// 16-byte stores straight from the accumulators, the next tile's first loads before
+// this tile's stores) and share those helpers. What differs: one scale per row and
+// column means nothing is promoted in the K loop, every MFMA accumulates in place;
+// a tile's scales come once, into an LDS slot of their own, and are applied in the
+// epilogue; and K is any multiple of 16: the chunks of the last K-block past K get
+// offsets past the buffer and read as zeros.
+#pragma once
+
+#include "fg_kernel.hpp"
+#include "fg_wave.hpp"
+
+namespace fg {
+
+// Compile-time tile configuration: as TileCfg, without scales in the rings.
+template <int BM_, int BN_, int WGM_, int WGN_, int STAGES_, int PD_ = 2, bool FA2_ = false, int ASTAGES_ = STAGES_>
+struct Int8Cfg {
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, STAGES = STAGES_, ASTAGES = ASTAGES_;
+  static constexpr int PD = PD_, RING = PD_ + 1;
+  static constexpr bool FA2 = FA2_;
+  static constexpr int W = WGM * WGN, THREADS = 64 * W;
+  static constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
+  static constexpr int A_INSTR = (BM * 8 + 64 * W - 1) / (64 * W);
+  static constexpr int B_INSTR = (BN * 8 + 64 * W - 1) / (64 * W);
+  static constexpr int DMA_PER_STAGE = A_INSTR + B_INSTR;
+  static constexpr int A_BYTES = A_INSTR * W * 1024, B_BYTES = B_INSTR * W * 1024;
+  // two slots of a tile's scales (this tile's and the next one's), then the rings
+  static constexpr int SC_BYTES = (BM + BN) * 4;
+  static constexpr int A_BASE = 2 * SC_BYTES;
+  static constexpr int B_BASE = A_BASE + ASTAGES * A_BYTES;
+  static constexpr int LDS_BYTES = B_BASE + STAGES * B_BYTES;
+  static constexpr int UNROLL = lcm_c(lcm_c(lcm_c(STAGES, ASTAGES), RING / gcd_c(TN, RING)), FA2 ? 2 : 1);
+  static_assert(WM % 16 == 0 && WN % 32 == 0 && BM % 64 == 0 && BN % 64 == 0, "whole sub-tile pairs, scales 64 at a time");
+  static_assert(BM % WGM == 0 && BN % WGN == 0, "waves must split the tile evenly");
+  static_assert(ASTAGES >= 2 && ASTAGES <= STAGES && (STAGES != 2 || ASTAGES == 2), "ring depths");
+  static_assert(STAGES * DMA_PER_STAGE <= 63, "too many DMA instructions in flight per wave");
+  static_assert(LDS_BYTES <= 160 * 1024, "LDS exceeds 160 KB");
+  static_assert(PD >= 1 && PD <= TN - 1, "prefetch distance must leave the barrier inside the K-block");
+};
+
+__device__ __forceinline__ i32x4 mfma_i8_lo(const i32x8& b, const i32x8& a, const i32x4& acc) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{b[0], b[1], b[2], b[3]}, i32x4{a[0], a[1], a[2], a[3]}, acc, 0, 0, 0);
+}
+__device__ __forceinline__ i32x4 mfma_i8_hi(const i32x8& b, const i32x8& a, const i32x4& acc) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{b[4], b[5], b[6], b[7]}, i32x4{a[4], a[5], a[6], a[7]}, acc, 0, 0, 0);
+}
+// One step: its two MFMAs, its LDS reads, then the rest; nothing crosses steps.
+__device__ __forceinline__ void int8_step_fence() {
+  __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+  __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+  __builtin_amdgcn_sched_group_barrier(0x002, 16, 0);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// The tiles a workgroup computes one after another: next(d) fills the next one and
+// returns true, or returns false (uniform over the workgroup).
+template <int LAYOUT, class T, class Next>
+__device__ __forceinline__ void int8_tiles(const Params& p, lds_u8* const lds, Next&& next) {
+  constexpr int BM = T::BM, BN = T::BN, W = T::W, WM = T::WM, WN = T::WN;
+  constexpr int TM = T::TM, TN = T::TN, PD = T::PD, R = T::RING, NA = T::A_INSTR, NB = T::B_INSTR;
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = uniform(t >> 6);
+  const int wm = wave / T::WGN, wn = wave % T::WGN;
+  const int lr = lane & 15, lq = lane >> 4;
+  const int K = p.K, nkb = p.KB, M = p.M;
+  const uint32_t lds_addr = (uint32_t)(uintptr_t)lds;
+  const uint32_t wave_at = lds_addr + wave * 1024;
+
+  auto next_tile = [&](TileDesc& d) {
+    const bool more = uniform(next(d) ? 1 : 0) != 0;
+    d = TileDesc{uniform(d.g), uniform(d.m0), uniform(d.n0), uniform(d.rows_valid)};
+    return more;
+  };
+  TileDesc cur;
+  if (!next_tile(cur)) return;
+
+  // DMA lane sources: slot s of a tile region is its 16-byte chunk s, holding row s / 8,
+  // chunk (s % 8) ^ (row % 8); a lane's chunk is the same for all its instructions.
+  const uint32_t chunk16 = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
+  uint32_t a_off[NA], b_off[NB];
+  auto a_row = [&](int q) { return ((q * W + wave) * 64 + lane) >> 3; };
+#pragma unroll
+  for (int q = 0; q < NA; ++q) {
+    const int row = a_row(q);
+    a_off[q] = row < BM ? (uint32_t)row * (uint32_t)K + chunk16 : kNoRow;
+  }
+#pragma unroll
+  for (int q = 0; q < NB; ++q) {
+    const int row = a_row(q);
+    b_off[q] = row < BN ? (uint32_t)pair_column(row) * (uint32_t)K + chunk16 : kNoRow;
+  }
+  i32x4 rsA, rsB;
+  constexpr int NWIN = (T::LDS_BYTES + 65535) >> 16;
+  LdsAddr<NWIN> aLo, aHi, bLo, bHi;
+  {
+    const uint32_t lane_lo = lr * 128 + ((lq ^ (lr & 7)) << 4);
+    const uint32_t lane_hi = lr * 128 + (((lq + 4) ^ (lr & 7)) << 4);
+    aLo.init(lds_addr + wm * WM * 128 + lane_lo);
+    aHi.init(lds_addr + wm * WM * 128 + lane_hi);
+    bLo.init(lds_addr + wn * WN * 128 + lane_lo);
+    bHi.init(lds_addr + wn * WN * 128 + lane_hi);
+  }
+  // Resources of tile d; rows past its last row with an output and columns past N read
+  // zeros. Its scales go to LDS slot par: loads older than the tile's first stage, so
+  // the wait for that stage covers them.
+  auto setup = [&](const TileDesc& d, int par) {
+    const int g = d.g, m0 = d.m0, n0 = d.n0;
+    const uint8_t* Ag = p.A + (LAYOUT == kMasked ? (size_t)g * M * K : 0);
+    const float* sag = p.sa + (LAYOUT == kMasked ? (size_t)g * M : 0);
+    const uint8_t* Bg = p.B + (LAYOUT != kDense ? (size_t)g * p.N * K : 0);
+    const float* sbg = p.sb + (LAYOUT != kDense ? (size_t)g * p.N : 0);
+    const int rows = max(0, min(d.rows_valid - m0, BM)), cols = max(0, min(p.N - n0, BN));
+    rsA = buffer_rsrc(Ag + (size_t)m0 * K, (uint32_t)rows * (uint32_t)K);
+    rsB = buffer_rsrc(Bg + (size_t)n0 * K, (uint32_t)cols * (uint32_t)K);
+    const i32x4 rsSA = buffer_rsrc(sag + m0, (uint32_t)rows * 4u), rsSB = buffer_rsrc(sbg + n0, (uint32_t)cols * 4u);
+    if constexpr (LAYOUT == kContiguous) {
+      // rows of padding or of another expert load nothing
+#pragma unroll
+      for (int q = 0; q < NA; ++q) {
+        const int row = a_row(q), m = m0 + row;
+        const bool live = row < BM && m < M && p.m_indices[m] == g;
+        a_off[q] = live ? (uint32_t)row * (uint32_t)K + chunk16 : kNoRow;
+        asm volatile("" : "+v"(a_off[q]));   // its load completes before the DMAs below
+      }
+    }
+    const uint32_t at = lds_addr + par * T::SC_BYTES;
+#pragma unroll
+    for (int q = 0; q < ((BM + BN) / 64 + W - 1) / W; ++q) {
+      const int i = q * W + wave;
+      if (i < BM / 64) dma4<0>(rsSA, (uint32_t)(i * 64 + lane) * 4u, 0u, at + i * 256);
+      else if (i < (BM + BN) / 64) dma4<0>(rsSB, (uint32_t)((i - BM / 64) * 64 + lane) * 4u, 0u, at + i * 256);
+    }
+  };
+  // Scalar offsets of one DMA group, A of K-block ka and B of K-block kbb, and what
+  // puts a lane's chunk past the buffer where it lies past K.
+  struct Soff {
+    uint32_t a, b, past_a, past_b;
+  };
+  auto soff_of = [&](int ka, int kbb) {
+    const uint32_t a = (uint32_t)ka * (uint32_t)kKBlock, b = (uint32_t)kbb * (uint32_t)kKBlock;
+    return Soff{a, b, a + chunk16 >= (uint32_t)K ? kNoRow : 0u, b + chunk16 >= (uint32_t)K ? kNoRow : 0u};
+  };
+  auto issue = [&](auto d_c, auto ast_c, auto bst_c, const Soff& o) {
+    constexpr int d = decltype(d_c)::value, AST = decltype(ast_c)::value, BST = decltype(bst_c)::value;
+    if constexpr (d < NA) dma16<T::A_BASE + AST * T::A_BYTES + d * W * 1024>(rsA, a_off[d] | o.past_a, o.a, wave_at);
+    else dma16<T::B_BASE + BST * T::B_BYTES + (d - NA) * W * 1024>(rsB, b_off[d - NA] | o.past_b, o.b, wave_at);
+  };
+  auto fragA = [&](auto st_c, auto i_c) {
+    return frag_at<T::A_BASE + decltype(st_c)::value * T::A_BYTES + decltype(i_c)::value * 2048>(aLo, aHi);
+  };
+  auto fragB = [&](auto st_c, auto j_c) {
+    return frag_at<T::B_BASE + decltype(st_c)::value * T::B_BYTES + decltype(j_c)::value * 2048>(bLo, bHi);
+  };
+
+  // DMA schedule: that of gemm_tiles (fg_kernel.hpp), which states why each wait suffices.
+  using SCH = Sched<T>;
+  constexpr int STEPS = SCH::STEPS, PRE = SCH::PRE, POST = SCH::POST, D = SCH::D;
+  constexpr bool SPLIT = SCH::SPLIT;
+  constexpr int SA = T::ASTAGES, SB = T::STAGES;
+  constexpr int B_AFTER_A = SA == SB ? 0 : NB;
+  constexpr int WAIT_LOOP = SPLIT ? SCH::n_early() : B_AFTER_A + (SA - 2) * D;
+  constexpr int WAIT_PRO = SPLIT ? D : B_AFTER_A + (SA - 2) * D + SCH::n_head();
+  constexpr int NST = TM * (TN / 2);   // output stores per wave and tile
+  static_assert(WAIT_PRO + NST < 64 && WAIT_LOOP < 64, "vmcnt counter range");
+  auto prologue = [&]() {
+    if constexpr (SPLIT) {
+      static_for<2>([&](auto x_c) {
+        const Soff o = soff_of(min((int)decltype(x_c)::value, nkb - 1), min((int)decltype(x_c)::value, nkb - 1));
+        static_for<D>([&](auto d_c) { issue(d_c, x_c, x_c, o); });
+      });
+    } else {
+      static_for<SB>([&](auto x_c) {
+        constexpr int x = decltype(x_c)::value, ka = x - SB + SA;
+        const Soff o = soff_of(min(ka < 0 ? 0 : ka, nkb - 1), min(x, nkb - 1));
+        static_for<D>([&](auto d_c) {
+          constexpr int d = decltype(d_c)::value;
+          if constexpr (!(d < NA && ka < 0) && !(x == SB - 1 && SCH::slot(d) >= POST))
+            issue(d_c, std::integral_constant<int, (ka < 0 ? 0 : ka)>{}, x_c, o);
+        });
+      });
+    }
+  };
+  int par = 0;
+  setup(cur, par);
+  prologue();
+  TileDesc nx = cur;
+  bool after_stores = false;
+  for (;;) {
+    if (after_stores) wait_vm<WAIT_PRO + NST>();
+    else wait_vm<WAIT_PRO>();
+    block_barrier();
+    i32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    i32x8 fbr[R], fa[T::FA2 ? 2 : 1][TM];
+    {
+      using Z = std::integral_constant<int, 0>;
+      if constexpr (T::FA2)
+        static_for<TM>([&](auto i_c) {
+          fa[0][decltype(i_c)::value] = fragA(Z{}, i_c);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      static_for<PD>([&](auto c_c) {
+        fbr[decltype(c_c)::value] = fragB(Z{}, c_c);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (!T::FA2)
+        static_for<TM>([&](auto i_c) {
+          fa[0][decltype(i_c)::value] = fragA(Z{}, i_c);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+    }
+    int kb = 0;
+    auto kblock = [&](auto ph_c) -> bool {
+      constexpr int PH = decltype(ph_c)::value, U = T::UNROLL;
+      constexpr int CA = PH % SA, NXA = (PH + 1) % SA, TA = (PH + U - 1) % SA;
+      constexpr int CB = PH % SB, NXB = (PH + 1) % SB, TB = (PH + U - 1) % SB;
+      constexpr int FSET = T::FA2 ? (PH & 1) : 0, NFSET = T::FA2 ? ((PH + 1) & 1) : 0;
+      using NxtA = std::integral_constant<int, NXA>;
+      using CurA = std::integral_constant<int, CA>;
+      using CurB = std::integral_constant<int, CB>;
+      using NxtB = std::integral_constant<int, NXB>;
+      const Soff head = soff_of(min(kb + SA, nkb - 1), min(kb + SB, nkb - 1));
+      const Soff tail = soff_of(min(kb - 1 + SA, nkb - 1), min(kb - 1 + SB, nkb - 1));
+      (void)tail;
+      static_for<STEPS>([&](auto u_c) {
+        constexpr int u = decltype(u_c)::value, j = u / TM, i = u % TM;
+        if constexpr (SPLIT && u == TM && TM < PRE) block_barrier();   // A half of this stage is free
+        if constexpr (u == PRE) {
+          wait_lgkm0();
+          wait_vm<WAIT_LOOP>();
+          block_barrier();
+          if constexpr (T::FA2)
+            static_for<TM>([&](auto ii_c) { fa[NFSET][decltype(ii_c)::value] = fragA(NxtA{}, ii_c); });
+        }
+        acc[i][j] = mfma_i8_lo(fbr[(PH * TN + j) % R], fa[FSET][i], acc[i][j]);
+        acc[i][j] = mfma_i8_hi(fbr[(PH * TN + j) % R], fa[FSET][i], acc[i][j]);
+        if constexpr (i == 0) {
+          constexpr int jn = j + PD, slot = (PH * TN + jn) % R;
+          if constexpr (jn < TN) fbr[slot] = fragB(CurB{}, std::integral_constant<int, jn>{});
+          else fbr[slot] = fragB(NxtB{}, std::integral_constant<int, jn - TN>{});
+        }
+        if constexpr (!T::FA2 && j == TN - 1) fa[0][i] = fragA(NxtA{}, std::integral_constant<int, i>{});
+        static_for<D>([&](auto d_c) {
+          constexpr int d = decltype(d_c)::value;
+          if constexpr (SPLIT) {
+            if constexpr (SCH::slot(d) == u) issue(d_c, CurA{}, CurB{}, head);
+          } else {
+            if constexpr (u >= PRE && SCH::slot(d) == u - PRE) issue(d_c, CurA{}, CurB{}, head);
+            if constexpr (u < PRE && SCH::slot(d) == POST + u)
+              issue(d_c, std::integral_constant<int, TA>{}, std::integral_constant<int, TB>{}, tail);
+          }
+        });
+        int8_step_fence();
+      });
+      return ++kb == nkb;
+    };
+    bool done = false;
+    for (;;) {
+      static_for<T::UNROLL>([&](auto ph_c) {
+        if (!done) done = kblock(ph_c);
+      });
+      if (done) break;
+    }
+
+    const int g = cur.g, m0 = cur.m0, n0 = cur.n0, rows_valid = cur.rows_valid;
+    uint16_t* Dg = p.D + (LAYOUT == kMasked ? (size_t)g * M * p.N : 0);
+    wait_vm<0>();          // the clamped tail DMAs must land before LDS is reused
+    wait_lgkm0();
+    block_barrier();
+    const int rows_here = max(0, min(rows_valid - m0, BM));
+    const __amdgpu_buffer_rsrc_t rsD =
+        __builtin_amdgcn_make_buffer_rsrc(Dg + (size_t)m0 * p.N, 0, rows_here * p.N * 2, 0x20000);
+    const lds_u8* sc = lds + par * T::SC_BYTES;
+    uint32_t roff[TM];
+    float sa[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int ml = wm * WM + i * 16 + lr, m = m0 + ml;
+      bool ok = m < rows_valid;
+      if (LAYOUT == kContiguous && ok) ok = p.m_indices[m] == g;
+      roff[i] = ok ? (uint32_t)ml * (uint32_t)p.N * 2u : kNoRow;
+      asm volatile("" : "+v"(roff[i]));   // any m_indices load completes before the next tile's DMAs
+      sa[i] = *(const lds_f32*)(sc + ml * 4);
+    }
+    const bool more = next_tile(nx);
+    if (more) {
+      setup(nx, par ^ 1);
+      prologue();
+    }
+#pragma unroll
+    for (int q = 0; q < TN / 2; ++q) {
+      const int nl = wn * WN + q * 32 + lq * 8, n = n0 + nl;
+      typedef __attribute__((address_space(3))) const f32x4 lds_f32x4c;
+      const f32x4 s0 = *(lds_f32x4c*)(sc + (BM + nl) * 4), s1 = *(lds_f32x4c*)(sc + (BM + nl) * 4 + 16);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const uint32_t off = n < p.N ? roff[i] + (uint32_t)n * 2u : kNoRow;
+        const i32x4& x = acc[i][2 * q];
+        const i32x4& y = acc[i][2 * q + 1];
+        float f[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          f[c] = (float)x[c] * sa[i] * s0[c];
+          f[4 + c] = (float)y[c] * sa[i] * s1[c];
+        }
+        const i32x4 v = {(int)bf16_pair(f[0], f[1]), (int)bf16_pair(f[2], f[3]), (int)bf16_pair(f[4], f[5]),
+                         (int)bf16_pair(f[6], f[7])};
+        __builtin_amdgcn_raw_buffer_store_b128(v, rsD, off, 0, 0);
+      }
+    }
+    if (!more) break;
+    cur = nx;
+    par ^= 1;
+    after_stores = true;
+  }
+}
+
+// One tile per workgroup.
+template <int LAYOUT, class T>
+__global__ __launch_bounds__(T::THREADS) void int8_gemm(Params p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
+  __shared__ int s_group;
+  lds_u8* const lds = (lds_u8*)smem;
+  const int t = threadIdx.x;
+  int tile = xcd_position(blockIdx.x, gridDim.x);
+  int g = 0;
+  if (LAYOUT == kMasked) {
+    const int per = p.tiles_m * p.tiles_n;
+    g = tile / per;
+    tile -= g * per;
+  }
+  int mb, nbk;
+  raster(tile, p.tiles_m, p.tiles_n, mb, nbk);
+  const int m0 = mb * T::BM, n0 = nbk * T::BN;
+  int rows_valid = p.M;
+  if (LAYOUT == kMasked) {
+    const int mm = p.masked_m[g];
+    rows_valid = mm < 0 ? 0 : (mm > p.M ? p.M : mm);
+    if (m0 >= rows_valid) return;   // uniform over the workgroup
+  }
+  if (LAYOUT == kContiguous) {
+    if (t == 0) s_group = -1;
+    __syncthreads();
+    if (t < T::BM && m0 + t < p.M) {
+      const int id = p.m_indices[m0 + t];
+      if (id >= 0 && id < p.G) atomicMax(&s_group, id);
+    }
+    __syncthreads();
+    g = s_group;
+    if (g < 0) return;   // all-padding block
+  }
+  bool done = false;
+  int8_tiles<LAYOUT, T>(p, lds, [&](TileDesc& d) {
+    if (done) return false;
+    d = TileDesc{g, m0, n0, rows_valid};
+    done = true;
+    return true;
+  });
+}
+
+// Dense on two tile shapes, contiguous on run-following tiles: the schedules of
+// fp8_bs_gemm_split and fp8_bs_gemm_runs.
+template <class TA, class TB>
+__global__ __launch_bounds__(TA::THREADS) void int8_gemm_split(Params p) {
+  static_assert(TA::THREADS == TB::THREADS, "both tile shapes run with the same workgroup size");
+  constexpr int LDS = TA::LDS_BYTES > TB::LDS_BYTES ? TA::LDS_BYTES : TB::LDS_BYTES;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
+  lds_u8* const lds = (lds_u8*)smem;
+  const int grid = gridDim.x, na = p.tiles_a;
+  const int tma = (p.M + TA::BM - 1) / TA::BM, tna = p.n_split / TA::BN;
+  const int tmb = (p.M + TB::BM - 1) / TB::BM, tnb = (p.N - p.n_split + TB::BN - 1) / TB::BN;
+  const int nb = tmb * tnb;
+  int k = blockIdx.x;
+  int8_tiles<kDense, TA>(p, lds, [&](TileDesc& d) {
+    if (k >= na) return false;
+    int mb, nbk;
+    raster(xcd_position(k, na), tma, tna, mb, nbk);
+    d = TileDesc{0, mb * TA::BM, nbk * TA::BN, p.M};
+    k += grid;
+    return true;
+  });
+  wait_lgkm0();
+  block_barrier();   // no wave still reads the TA tiles' LDS when the TB tiles' DMAs start
+  k = blockIdx.x;
+  int8_tiles<kDense, TB>(p, lds, [&](TileDesc& d) {
+    if (k >= nb) return false;
+    int mb, nbk;
+    raster(xcd_position(k, nb), tmb, tnb, mb, nbk);
+    d = TileDesc{0, mb * TB::BM, p.n_split + nbk * TB::BN, p.M};
+    k += grid;
+    return true;
+  });
+}
+
+template <class TF, class TH>
+__global__ __launch_bounds__(TF::THREADS) void int8_gemm_runs(Params p) {
+  static_assert(TF::BM == 256 && TH::BM == 128 && TF::BN == TH::BN && TF::THREADS == TH::THREADS,
+                "two-block tiles of 256 rows, single-block tiles of 128 rows, same columns and workgroup");
+  constexpr int LDS = TF::LDS_BYTES > TH::LDS_BYTES ? TF::LDS_BYTES : TH::LDS_BYTES;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS + kRunMaxBlocks * 4];
+  __shared__ int s_count[2];
+  lds_u8* const lds = (lds_u8*)smem;
+  int* list = (int*)(smem + LDS);
+  contiguous_run_tiles<TF::THREADS, true>(p, (int*)smem, list, s_count);
+  const int F = s_count[0], S = s_count[1], tn = p.tiles_n;
+  const long grid = gridDim.x;
+  const long full_items = (long)F * tn;
+  long whole = full_items;   // two-block tiles that run as 256-row tiles
+  {
+    const long rounds = full_items / grid, rest = full_items - rounds * grid;
+    if (rest && 2 * rest + (long)S * tn <= grid) whole = rounds * grid;
+  }
+  const long halves = 2 * (full_items - whole);
+  const long items = whole + halves + (long)S * tn;
+  long w = xcd_position(blockIdx.x, gridDim.x);
+  int8_tiles<kContiguous, TF>(p, lds, [&](TileDesc& d) {
+    if (w >= whole) return false;
+    int mb, nbk;
+    raster((int)w, F, tn, mb, nbk);
+    const int e = list[mb];
+    d = TileDesc{e >> 16, (e & 0xffff) * 128, nbk * TF::BN, p.M};
+    w += grid;
+    return true;
+  });
+  wait_lgkm0();
+  block_barrier();   // no wave still reads LDS of the 256-row tiles when the 128-row ones start
+  int8_tiles<kContiguous, TH>(p, lds, [&](TileDesc& d) {
+    if (w >= items) return false;
+    const long h = w - whole;
+    int mb, nbk, e, m0;
+    if (h < halves) {   // one 128-row half of a two-block tile
+      raster((int)(whole + h / 2), F, tn, mb, nbk);
+      e = list[mb];
+      m0 = (e & 0xffff) * 128 + (int)(h & 1) * 128;
+    } else {            // a single-block tile
+      raster((int)(h - halves), S, tn, mb, nbk);
+      e = list[kRunMaxBlocks - 1 - mb];
+      m0 = (e & 0xffff) * 128;
+    }
+    d = TileDesc{e >> 16, m0, nbk * TH::BN, p.M};
+    w += grid;
+    return true;
+  });
+}
+
+}  // namespace fg

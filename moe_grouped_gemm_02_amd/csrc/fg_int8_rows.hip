@@ -1,0 +1,178 @@
+// fg_int8_rows.hip -- rows as 8-bit integers with one scale each, the operands of the
+// 8-bit integer product:
+//
+//     s = max(amax / 127, 2^-126) (1 for a row of zeros),  q = rint(v / s)
+//
+// with amax the row's largest |v|, the quotient rounded to fp32 and ties to even. v is
+// a row as it is, a token's row times a weight in each of its plan rows, or the gated
+// activation silu(gate) up of a first projection whose columns interleave gate and up
+// every 128 (the layout of the fused E4M3 call).
+//
+// All are bound by memory traffic: a row is read once and stays in registers between
+// its largest value and its codes. A lane holds units of 16 elements, 16 bytes of
+// codes; a workgroup (or a wave, for rows of up to 1024) has one row.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "fg.h"
+#include "fg_device.hpp"
+#include "fg_int8_quot.hpp"
+
+namespace {
+
+using namespace fg;
+
+constexpr int kMaxRow = 65536;   // 1024 threads of 4 units
+
+// The row's largest value from its NTH threads' own.
+template <int NTH>
+__device__ __forceinline__ float row_amax(uint32_t m, uint32_t* part) {
+  m = group_max_u32<64>(m);
+  if constexpr (NTH > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < NTH / 64; ++v) m = umax(m, part[v]);
+  }
+  return __uint_as_float(m);
+}
+
+enum Mode { kRows = 0, kDispatch = 1, kSwiglu = 2 };
+
+struct RowArgs {
+  const void* x;
+  const int32_t* index;   // dispatch: rows [T][k]; swiglu: slots [rows] or null
+  const float* w;         // dispatch: [T][k] or null
+  uint8_t* q;
+  float* s;
+  int T, k, H, n_rows;
+};
+
+template <class R>
+__device__ __forceinline__ void unit16(const char* at, float* f) {
+  constexpr int N = 16 / R::kPer16;
+#pragma unroll
+  for (int c = 0; c < N; ++c) R::unpack(((const u32x4*)at)[c], f + c * R::kPer16);
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* at, const float* f, float s, float inv) {
+  uint32_t q[4];
+  int8_encode<16>(f, s, inv, q);
+  __builtin_nontemporal_store(u32x4{q[0], q[1], q[2], q[3]}, (u32x4*)at);
+}
+
+template <class R, int MODE, int NTH, int C>
+__global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void quant_int8(RowArgs a) {
+  __shared__ uint32_t part[NTH / 64];
+  constexpr int kPerGroup = NTH == 64 ? 4 : 1;   // rows of a workgroup
+  const int lane = NTH == 64 ? threadIdx.x & 63 : threadIdx.x;
+  const long row = (long)blockIdx.x * kPerGroup + (NTH == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
+  if (row >= a.T) return;
+  if (MODE == kSwiglu && a.index && a.index[row] < 0) return;   // uniform over the row's threads
+  const int per = a.H >> 4;
+  float f[C][16];
+  uint32_t m = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = c * NTH + lane, at = i < per ? i : per - 1;   // the last unit again: no branch around the loads
+    if constexpr (MODE == kSwiglu) {
+      // unit i: columns 16 i of the activation, gate at 256 (i / 8) + 16 (i % 8), up 128 further
+      const char* g = (const char*)a.x + (row * 2 * a.H + (at >> 3) * 256L + (at & 7) * 16) * R::kBytes;
+      float u[16];
+      unit16<R>(g, f[c]);
+      unit16<R>(g + 128 * R::kBytes, u);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[c][e] = f[c][e] / (1.0f + expf(-f[c][e])) * u[e];
+    } else {
+      unit16<R>((const char*)a.x + (row * a.H + 16L * at) * R::kBytes, f[c]);
+    }
+    m = amax_bits<16>(f[c], m);
+  }
+  const float amax = row_amax<NTH>(m, part);
+  if constexpr (MODE != kDispatch) {
+    const float s = int8_scale(amax), inv = 1.0f / s;
+    if (lane == 0) a.s[row] = s;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int i = c * NTH + lane;
+      if (i < per) store_codes(a.q + row * a.H + 16L * i, f[c], s, inv);
+    }
+  } else {
+    for (int j = 0; j < a.k; ++j) {
+      const int to = a.index[row * a.k + j];
+      if ((unsigned)to >= (unsigned)a.n_rows) continue;
+      const float wj = a.w ? a.w[row * a.k + j] : 1.0f;
+      // rounding is monotone: the largest |w v| as rounded is |w| times the largest |v|, rounded
+      const float s = int8_scale(fabsf(wj) * amax), inv = 1.0f / s;
+      if (lane == 0) a.s[to] = s;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = f[c][e] * wj;
+        const int i = c * NTH + lane;
+        if (i < per) store_codes(a.q + (long)to * a.H + 16L * i, v, s, inv);
+      }
+    }
+  }
+}
+
+template <class R, int MODE, int NTH, int C>
+int launch_one(const RowArgs& a, hipStream_t s) {
+  const long groups = NTH == 64 ? (a.T + 3L) / 4 : a.T;
+  hipLaunchKernelGGL((quant_int8<R, MODE, NTH, C>), dim3((unsigned)groups), dim3(NTH == 64 ? 256 : NTH), 0, s, a);
+  return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
+}
+
+template <class R, int MODE>
+int launch_rows(const RowArgs& a, hipStream_t s) {
+  const int per = a.H / 16;
+  if (per <= 64) return launch_one<R, MODE, 64, 1>(a, s);
+  if (per <= 256) return launch_one<R, MODE, 256, 1>(a, s);
+  if (per <= 512) return launch_one<R, MODE, 256, 2>(a, s);
+  if (per <= 1024) return launch_one<R, MODE, 256, 4>(a, s);
+  return launch_one<R, MODE, 1024, 4>(a, s);
+}
+
+int check(int dtype, int T, int H) {
+  return T < 0 || H < 16 || H % 16 || H > kMaxRow || (dtype != FG_BF16 && dtype != FG_FP32) ? FG_EINVAL : FG_OK;
+}
+
+template <int MODE>
+int run(int dtype, const RowArgs& a, hipStream_t stream) {
+  if (!a.x || !a.q || !a.s || !aligned(a.x, 16) || !aligned(a.q, 16) || !aligned(a.s, 4)) return FG_EINVAL;
+  const int st = current_device(nullptr);
+  if (st != FG_OK) return st;
+  return dtype == FG_BF16 ? launch_rows<RowBf16, MODE>(a, stream) : launch_rows<RowF32, MODE>(a, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fg_quant_int8(const void* x, int dtype, void* q, float* s, int M, int K, hipStream_t stream) {
+  const int rc = check(dtype, M, K);
+  if (rc != FG_OK || M == 0) return rc;
+  return run<kRows>(dtype, RowArgs{x, nullptr, nullptr, static_cast<uint8_t*>(q), s, M, 1, K, M}, stream);
+}
+
+int fg_dispatch_quant_int8(const void* x, int dtype, const int32_t* rows, const float* w, void* Q, float* s, int T,
+                           int k, int H, int n_rows, hipStream_t stream) {
+  const int rc = check(dtype, T, H);
+  if (rc != FG_OK || k < 1 || n_rows < 0) return FG_EINVAL;
+  if (T == 0 || n_rows == 0) return FG_OK;
+  if (!rows || !aligned(rows, 4) || !aligned(w, 4)) return FG_EINVAL;
+  return run<kDispatch>(dtype, RowArgs{x, rows, w, static_cast<uint8_t*>(Q), s, T, k, H, n_rows}, stream);
+}
+
+int fg_swiglu_quant_int8(const void* h, int dtype, const int32_t* slots, void* Q, float* s, int rows, int I,
+                         hipStream_t stream) {
+  const int rc = check(dtype, rows, I);
+  if (rc != FG_OK || I % 128) return FG_EINVAL;
+  if (rows == 0) return FG_OK;
+  if (!aligned(slots, 4)) return FG_EINVAL;
+  return run<kSwiglu>(dtype, RowArgs{h, slots, nullptr, static_cast<uint8_t*>(Q), s, rows, 1, I, rows}, stream);
+}
+
+}  // extern "C"
