@@ -997,9 +997,11 @@ def block_norm_grad(r, dh=None, dr=None, y=None, pre=None, post=None, gate=None,
         dy = _new(dy, "dy", (T, N), r.dtype, dev)
     elif dy is not None:
         raise ValueError("dy is y's gradient, and there is no y")
-    dgate = None if gate is None else torch.empty(gate.shape, dtype=f32, device=dev)
-    dpre = None if pre is None else torch.empty(N, dtype=f32, device=dev)
-    dpost = None if post is None else torch.empty(N, dtype=f32, device=dev)
+    # the vectors' gradients in one allocation
+    sizes = (N if pre is not None else 0, N if post is not None else 0, gate.numel() if gate is not None else 0)
+    dpre, dpost, dgate = torch.empty(sum(sizes), dtype=f32, device=dev).split_with_sizes(sizes)
+    dpre, dpost = dpre if pre is not None else None, dpost if post is not None else None
+    dgate = dgate.view(gate.shape) if gate is not None else None
     ws = torch.empty(_block_norm_grad_workspace(T, N), dtype=torch.uint8, device=dev)
     _call("fg_block_norm_grad", dev, _ptr(r), _opt_ptr(dh), _opt_ptr(dr), _opt_ptr(y), dt, _opt_ptr(pre), _opt_ptr(post),
           _opt_ptr(gate), kind, _ptr(dx), _opt_ptr(dy), _opt_ptr(dgate), _opt_ptr(dpre), _opt_ptr(dpost), _ptr(ws), T, N,

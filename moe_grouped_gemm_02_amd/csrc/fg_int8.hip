@@ -45,11 +45,35 @@ struct Choice {
   int n_split = 0;
 };
 
+// The kernel that streams the weights (int8_skinny), or none where tiles are faster. By the
+// workgroups w of 128 rows and 64 columns: enough of them share a CU's time, few need narrower
+// columns to reach all CUs. Measured, us, K 7168, 16 / 32 / 64 columns and the best tile:
+//   M 16   N 2048 (w 32) 5.3 / 6.4 / 8.5 / 17.9    N 4096 (64) 6.9 / 7.1 / 8.8 / 18.1    N 7168 (112) 10.9 / 9.9 / 10.1 / 18.6
+//          N 14336 (224) 24.4 / 21.1 / 17.6 / 28.7    N 28672 (448) 46.9 / 42.7 / 37.6 / 37.6
+//   M 64   N 4096 9.6 / 10.5 / 17.5 / 18.6    N 7168 16.5 / 11.9 / 17.6 / 19.0    N 14336 42.9 / 29.8 / 25.4 / 32.9
+//          N 28672 77.9 / 58.9 / 46.7 / 42.4
+//   M 128  N 4096 14.5 / 15.9 / - / 18.6    N 7168 25.6 / 17.1 / - / 19.2    N 14336 62.7 / 41.4 / - / 33.5
+Choice skinny(int layout, int M, int N, int G, int force = -1) {
+  Choice c;
+  if (layout != FG_LAYOUT_MASKED) G = 1;
+  const long w = ceil_div(M, kSkinnyRows) * ceil_div(N, 64) * G;
+  int i = w <= 80 ? 0 : w <= 160 ? 1 : (w <= 320 && M <= 96) || M <= 16 ? 2 : -1;
+  if (force >= 0) i = force;
+  if (i < 0) return c;
+  int steps = (int)ceil_div(M < kSkinnyRows ? M : kSkinnyRows, 16);
+  if (steps > 4) steps = steps <= 6 ? 6 : 8;
+  c.tile = kSkinny + 3 * (steps - 1) + i;
+  c.grid = ceil_div(M, 16 * steps) * ceil_div(N, 16 << i) * G;
+  return c;
+}
+
 // The shape whose tiles, in rounds over the compute units, take the fewest estimated
 // cycles; dense problems also try whole rounds of 256x256 tiles with the remaining
 // columns on 256x128, contiguous ones the run-following kernel.
 Choice choose(int layout, int M, int N, int K, int G, int cus) {
   Choice best;
+  if (layout != FG_LAYOUT_CONTIGUOUS) best = skinny(layout, M, N, G);
+  if (best.tile >= 0) return best;
   double cost = 0.0;
   const double kb = (double)ceil_div(K, 128);
   for (int i = 0; i < kNumTiles; ++i) {
@@ -106,6 +130,10 @@ bool forced(int layout, int M, int N, int G, int cus, Choice& c) {
     c.grid = ceil_div(M, t.bm) * ceil_div(N, t.bn) * (layout == FG_LAYOUT_MASKED ? G : 1);
     return layout != FG_LAYOUT_CONTIGUOUS || t.bm <= 128;
   }
+  if (t_tile >= kSkinny) {
+    c = skinny(layout, M, N, G, t_tile - kSkinny);
+    return layout != FG_LAYOUT_CONTIGUOUS && !(M > 96 && t_tile == kSkinny + 2);
+  }
   c.grid = t_grid > 0 ? t_grid : cus;
   if (t_tile == kRuns) return layout == FG_LAYOUT_CONTIGUOUS;
   c.n_split = N / 512 * 256;
@@ -122,7 +150,7 @@ int run(int layout, const void* A, const float* sa, const void* B, const float* 
   if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(index, 4))
     return FG_EINVAL;
   // the smallest tiles' number, a bound of every choice's
-  if ((layout == FG_LAYOUT_MASKED ? G : 1) * ceil_div(M, 64) * ceil_div(N, 128) > 0x7fffffffL) return FG_EINVAL;
+  if ((layout == FG_LAYOUT_MASKED ? G : 1) * ceil_div(M, 64) * ceil_div(N, 16) > 0x7fffffffL) return FG_EINVAL;
   int cus = 0;
   const int st = current_device(&cus);
   if (st != FG_OK) return st;
@@ -143,8 +171,8 @@ int run(int layout, const void* A, const float* sa, const void* B, const float* 
   p.K = K;
   p.G = G;
   p.KB = (int)ceil_div(K, 128);
-  p.tiles_m = (int)ceil_div(M, t.bm);
-  p.tiles_n = (int)ceil_div(N, t.bn);
+  p.tiles_m = (int)ceil_div(M, c.tile >= kSkinny ? 16 * ((c.tile - kSkinny) / 3 + 1) : t.bm);
+  p.tiles_n = (int)ceil_div(N, c.tile >= kSkinny ? 16 << (c.tile - kSkinny) % 3 : t.bn);
   p.n_split = c.n_split;
   p.tiles_a = (int)c.tiles_a;
   hipError_t e;
@@ -177,7 +205,7 @@ int fg_grouped_masked_int8(const void* A, const float* sa, const void* B, const 
 
 #ifdef FG_TESTING
 int fgt_force_int8(int tile, int grid) {
-  if (tile < -1 || tile > kRuns || grid < 0) return FG_EINVAL;
+  if (tile < -1 || tile > kSkinny + 2 || grid < 0) return FG_EINVAL;
   t_tile = tile;
   t_grid = grid;
   return FG_OK;

@@ -49,6 +49,9 @@ struct Int8Cfg {
   static_assert(PD >= 1 && PD <= TN - 1, "prefetch distance must leave the barrier inside the K-block");
 };
 
+__device__ __forceinline__ i32x4 mfma_i8(const i32x4& b, const i32x4& a, const i32x4& acc) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, acc, 0, 0, 0);
+}
 __device__ __forceinline__ i32x4 mfma_i8_lo(const i32x8& b, const i32x8& a, const i32x4& acc) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{b[0], b[1], b[2], b[3]}, i32x4{a[0], a[1], a[2], a[3]}, acc, 0, 0, 0);
 }
@@ -455,6 +458,149 @@ __global__ __launch_bounds__(TF::THREADS) void int8_gemm_runs(Params p) {
     w += grid;
     return true;
   });
+}
+
+// Few rows: the product is a stream of the weights. A workgroup has 16 TN columns and 16 TM
+// rows, all of them where there are so few; its waves take 128-byte pieces of K in turn and add their sums up
+// through LDS at the end -- exact in any order, so K needs no split over workgroups and no
+// workspace. Each wave moves its pieces through a ring of STAGES slots of its own in LDS
+// (whole 128-byte lines a load; straight into the matrix core's registers a load takes 16
+// half lines, which the CU fetches at a third of the rate: M 64, N 7168, K 7168 22.7 us),
+// so nothing but the end needs a barrier. Chunks past the last row, column or K get
+// offsets past the buffer: zeros, and no memory access.
+template <int TM_, int TN_, int WAVES_, int STAGES_>
+struct SkinnyCfg {
+  static constexpr int TM = TM_, TN = TN_, WAVES = WAVES_, STAGES = STAGES_;
+  static constexpr int LOADS = 2 * (TM + TN);                   // of a piece, a kilobyte each
+  static constexpr int RING = STAGES * LOADS * 1024;            // of a wave
+  static constexpr int BLOCKS = (TM * TN + WAVES - 1) / WAVES;  // 16x16 blocks of D a wave finishes
+  static constexpr int LDS_BYTES = WAVES * RING > WAVES * TM * TN * 1024 ? WAVES * RING : WAVES * TM * TN * 1024;
+  static_assert(LDS_BYTES <= 160 * 1024 && STAGES * LOADS < 48, "LDS and the loads in flight");
+};
+template <int LAYOUT, class T>
+__global__ __launch_bounds__(64 * T::WAVES) void int8_skinny(Params p) {
+  constexpr int TM = T::TM, TN = T::TN, W = T::WAVES, S = T::STAGES, U = T::BLOCKS;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
+  lds_u8* const lds = (lds_u8*)smem;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
+  // row blocks of the same columns follow one another on one XCD, whose L2 has the weights then
+  int g = 0, tile = p.tiles_m == 1 ? blockIdx.x : xcd_position(blockIdx.x, gridDim.x);
+  if (LAYOUT == kMasked) {
+    const int per = p.tiles_m * p.tiles_n;
+    g = tile / per;
+    tile -= g * per;
+  }
+  const int n0 = tile / p.tiles_m * 16 * TN, m0 = tile % p.tiles_m * 16 * TM;
+  int rows = p.M;
+  if (LAYOUT == kMasked) {
+    const int mm = p.masked_m[g];
+    rows = mm < 0 ? 0 : (mm > p.M ? p.M : mm);
+    if (m0 >= rows) return;   // uniform over the workgroup
+  }
+  rows = min(rows - m0, 16 * TM);
+  const int K = p.K, cols = min(p.N - n0, 16 * TN);
+  const size_t row0 = (LAYOUT == kMasked ? (size_t)g * p.M : 0) + m0;   // of A, sa and D
+  const uint8_t* Ag = p.A + row0 * K;
+  const uint8_t* Bg = p.B + ((LAYOUT == kMasked ? (size_t)g * p.N : 0) + (size_t)n0) * K;
+  const float* sag = p.sa + row0;
+  const float* sbg = p.sb + (LAYOUT == kMasked ? (size_t)g * p.N : 0);
+  // the scales of the D that this lane finishes
+  float sa[U], sb[U][4];
+#pragma unroll
+  for (int c = 0; c < U; ++c) {
+    const int u = min(wave + c * W, TM * TN - 1);
+    sa[c] = sag[min(u / TN * 16 + lr, rows - 1)];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sb[c][e] = sbg[min(n0 + u % TN * 16 + lq * 4 + e, p.N - 1)];
+  }
+#pragma unroll
+  for (int c = 0; c < U; ++c) {   // loaded before the first DMA: a wait for them is none for the stream
+    asm volatile("" : "+v"(sa[c]), "+v"(sb[c][0]), "+v"(sb[c][1]), "+v"(sb[c][2]), "+v"(sb[c][3]));
+  }
+  const i32x4 rsA = buffer_rsrc(Ag, (uint32_t)rows * (uint32_t)K), rsB = buffer_rsrc(Bg, (uint32_t)cols * (uint32_t)K);
+  // A load brings 8 rows: lane l chunk (l % 8) ^ (l / 8) of row l / 8, to 16-byte slot l.
+  const uint32_t chunk16 = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16), row_off = (uint32_t)(lane >> 3) * (uint32_t)K + chunk16;
+  const uint32_t ring = (uint32_t)(uintptr_t)lds + wave * T::RING;
+  auto load = [&](uint32_t slot, int x) {
+    const uint32_t k = (uint32_t)(x * W + wave) * 128u;
+    const uint32_t off = row_off | (k + chunk16 < (uint32_t)K ? 0u : kNoRow), step = 8u * (uint32_t)K;
+    static_for<2 * TM>([&](auto q) { dma16<decltype(q)::value * 1024>(rsA, off + decltype(q)::value * step, k, ring + slot); });
+    static_for<2 * TN>([&](auto q) {
+      dma16<(2 * TM + decltype(q)::value) * 1024>(rsB, off + decltype(q)::value * step, k, ring + slot);
+    });
+  };
+  i32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  const lds_u8* const mine = lds + wave * T::RING + lr * 128;
+  const int lo = (lq ^ (lr & 7)) << 4, hi = ((lq + 4) ^ (lr & 7)) << 4;
+  // A slot's piece into registers, the slot's next one on its way (if any), the products.
+  auto piece = [&](uint32_t slot, int next) {
+    typedef __attribute__((address_space(3))) const i32x4 lds_i32x4;
+    i32x4 a[TM][2], b[TN][2];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      a[i][0] = *(lds_i32x4*)(mine + slot + i * 2048 + lo);
+      a[i][1] = *(lds_i32x4*)(mine + slot + i * 2048 + hi);
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      b[j][0] = *(lds_i32x4*)(mine + slot + (TM + j) * 2048 + lo);
+      b[j][1] = *(lds_i32x4*)(mine + slot + (TM + j) * 2048 + hi);
+    }
+    if (next >= 0) {
+      wait_lgkm0();
+      load(slot, next);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma_i8(b[j][h], a[i][h], acc[i][j]);
+  };
+  const int pieces = (K + 128 * W - 1) / (128 * W);   // of a wave
+  static_for<S>([&](auto s) { load(decltype(s)::value * T::LOADS * 1024, decltype(s)::value); });
+  uint32_t slot = 0;
+  auto advance = [&]() { slot = slot == (S - 1) * T::LOADS * 1024 ? 0 : slot + T::LOADS * 1024; };
+  for (int x = 0; x + S < pieces; ++x) {
+    wait_vm<(S - 1) * T::LOADS>();
+    piece(slot, x + S);
+    advance();
+  }
+  static_for<S>([&](auto s) {
+    wait_vm<(S - 1 - decltype(s)::value) * T::LOADS>();
+    piece(slot, -1);
+    advance();
+  });
+  wait_lgkm0();
+  block_barrier();   // the rings are free
+  typedef __attribute__((address_space(3))) i32x4 lds_i32x4w;
+  lds_i32x4w* sums = (lds_i32x4w*)lds;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) sums[(wave * TM * TN + i * TN + j) * 64 + lane] = acc[i][j];
+  wait_lgkm0();
+  block_barrier();
+  uint16_t* Dg = p.D + row0 * p.N;
+#pragma unroll
+  for (int c = 0; c < U; ++c) {
+    const int u = wave + c * W;
+    if (u >= TM * TN) break;
+    const int m = u / TN * 16 + lr, n = n0 + u % TN * 16 + lq * 4;
+    i32x4 v = sums[u * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += sums[(w * TM * TN + u) * 64 + lane];
+    if (m >= rows || n >= p.N) continue;
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = (float)v[e] * sa[c] * sb[c][e];
+    *(u32x2*)(Dg + (size_t)m * p.N + n) = u32x2{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])};
+  }
 }
 
 }  // namespace fg

@@ -20,6 +20,25 @@ hipError_t launch_tile(const Params& p, int grid, hipStream_t s) {
     return hipGetLastError();
   }
 }
+template <int LAYOUT, class C>
+hipError_t launch_one_skinny(const Params& p, int grid, hipStream_t s) {
+  if constexpr (LAYOUT == kContiguous) {
+    return hipErrorInvalidValue;
+  } else {
+    hipLaunchKernelGGL((int8_skinny<LAYOUT, C>), dim3(grid), dim3(64 * C::WAVES), 0, s, p);
+    return hipGetLastError();
+  }
+}
+template <int LAYOUT, int TM>
+hipError_t launch_skinny(int i, const Params& p, int grid, hipStream_t s) {
+  switch (i) {
+    case 0: return launch_one_skinny<LAYOUT, int8_cfg::Skinny<TM, 0>>(p, grid, s);
+    case 1: return launch_one_skinny<LAYOUT, int8_cfg::Skinny<TM, 1>>(p, grid, s);
+    default:
+      if constexpr (TM <= 6) return launch_one_skinny<LAYOUT, int8_cfg::Skinny<TM, 2>>(p, grid, s);
+      else return hipErrorInvalidValue;
+  }
+}
 }  // namespace
 
 template <int LAYOUT>
@@ -45,6 +64,16 @@ hipError_t launch_int8(int tile, const Params& p, int grid, hipStream_t s) {
       } else {
         return hipErrorInvalidValue;
       }
+    default: break;
+  }
+  const int i = (tile - kSkinny) % 3;
+  switch ((tile - kSkinny) / 3 + 1) {
+    case 1: return launch_skinny<LAYOUT, 1>(i, p, grid, s);
+    case 2: return launch_skinny<LAYOUT, 2>(i, p, grid, s);
+    case 3: return launch_skinny<LAYOUT, 3>(i, p, grid, s);
+    case 4: return launch_skinny<LAYOUT, 4>(i, p, grid, s);
+    case 6: return launch_skinny<LAYOUT, 6>(i, p, grid, s);
+    case 8: return launch_skinny<LAYOUT, 8>(i, p, grid, s);
     default: return hipErrorInvalidValue;
   }
 }

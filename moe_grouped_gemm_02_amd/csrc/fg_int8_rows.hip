@@ -38,6 +38,17 @@ __device__ __forceinline__ float row_amax(uint32_t m, uint32_t* part) {
   return __uint_as_float(m);
 }
 
+// x / (1 + exp(-x)) to about 3 ulp. exp(-x) = 2^h 2^l with h the rounded product -x log2 e
+// and l what it misses (the hardware's 2^h alone is off by |x| 2^-24); the reciprocal is
+// the hardware's. Below x = -87.3 (h >= 126) silu is under 1e-36 and taken as 0.
+__device__ __forceinline__ float silu(float x) {
+  constexpr float kLog2e = 1.44269502f, kLow = 1.92596299e-8f, kLn2 = 0.693147182f;
+  const float h = -x * kLog2e, l = fmaf(-x, kLow, fmaf(-x, kLog2e, -h));
+  const float e = __builtin_amdgcn_exp2f(h);
+  const float s = __builtin_amdgcn_rcpf(1.0f + fmaf(e, l * kLn2, e));
+  return x * (h < 126.0f ? s : 0.0f);
+}
+
 enum Mode { kRows = 0, kDispatch = 1, kSwiglu = 2 };
 
 struct RowArgs {
@@ -56,9 +67,7 @@ __device__ __forceinline__ void unit16(const char* at, float* f) {
   for (int c = 0; c < N; ++c) R::unpack(((const u32x4*)at)[c], f + c * R::kPer16);
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* at, const float* f, float s, float inv) {
-  uint32_t q[4];
-  int8_encode<16>(f, s, inv, q);
+__device__ __forceinline__ void store_codes(uint8_t* at, const uint32_t* q) {
   __builtin_nontemporal_store(u32x4{q[0], q[1], q[2], q[3]}, (u32x4*)at);
 }
 
@@ -83,7 +92,7 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void quant_int8(RowArgs a) {
       unit16<R>(g, f[c]);
       unit16<R>(g + 128 * R::kBytes, u);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) f[c][e] = f[c][e] / (1.0f + expf(-f[c][e])) * u[e];
+      for (int e = 0; e < 16; ++e) f[c][e] = silu(f[c][e]) * u[e];
     } else {
       unit16<R>((const char*)a.x + (row * a.H + 16L * at) * R::kBytes, f[c]);
     }
@@ -96,23 +105,47 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void quant_int8(RowArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * NTH + lane;
-      if (i < per) store_codes(a.q + row * a.H + 16L * i, f[c], s, inv);
+      uint32_t q[4];
+      int8_encode<16>(f[c], s, inv, q);
+      if (i < per) store_codes(a.q + row * a.H + 16L * i, q);
     }
   } else {
-    for (int j = 0; j < a.k; ++j) {
-      const int to = a.index[row * a.k + j];
-      if ((unsigned)to >= (unsigned)a.n_rows) continue;
-      const float wj = a.w ? a.w[row * a.k + j] : 1.0f;
-      // rounding is monotone: the largest |w v| as rounded is |w| times the largest |v|, rounded
-      const float s = int8_scale(fabsf(wj) * amax), inv = 1.0f / s;
-      if (lane == 0) a.s[to] = s;
+    // the choices' rows and weights in one load, a choice a lane; without weights all get
+    // the same codes
+    uint32_t q[C][4];
+    float s = int8_scale(amax);
+    const float inv = 1.0f / s;
+    if (!a.w) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float v[16];
+      for (int c = 0; c < C; ++c) int8_encode<16>(f[c], s, inv, q[c]);
+    }
+    for (int j0 = 0; j0 < a.k; j0 += 64) {
+      const int n = a.k - j0 < 64 ? a.k - j0 : 64;
+      const int mine = (threadIdx.x & 63) < n ? (threadIdx.x & 63) : 0;
+      const int rows = a.index[row * a.k + j0 + mine];
+      const float weights = a.w ? a.w[row * a.k + j0 + mine] : 1.0f;
+      for (int j = 0; j < n; ++j) {
+        const int to = __builtin_amdgcn_readlane(rows, j);
+        if ((unsigned)to >= (unsigned)a.n_rows) continue;
+        if (a.w) {
+          // rounding is monotone: the largest |w v| as rounded is |w| times the largest |v|, rounded
+          const float wj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(weights), j));
+          s = int8_scale(fabsf(wj) * amax);
+          const float winv = 1.0f / s;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = f[c][e] * wj;
-        const int i = c * NTH + lane;
-        if (i < per) store_codes(a.q + (long)to * a.H + 16L * i, v, s, inv);
+          for (int c = 0; c < C; ++c) {
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = f[c][e] * wj;
+            int8_encode<16>(v, s, winv, q[c]);
+          }
+        }
+        if (lane == 0) a.s[to] = s;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int i = c * NTH + lane;
+          if (i < per) store_codes(a.q + (long)to * a.H + 16L * i, q[c]);
+        }
       }
     }
   }
@@ -129,6 +162,7 @@ template <class R, int MODE>
 int launch_rows(const RowArgs& a, hipStream_t s) {
   const int per = a.H / 16;
   if (per <= 64) return launch_one<R, MODE, 64, 1>(a, s);
+  if (per <= 128) return launch_one<R, MODE, 128, 1>(a, s);
   if (per <= 256) return launch_one<R, MODE, 256, 1>(a, s);
   if (per <= 512) return launch_one<R, MODE, 256, 2>(a, s);
   if (per <= 1024) return launch_one<R, MODE, 256, 4>(a, s);

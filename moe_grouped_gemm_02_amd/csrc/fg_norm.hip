@@ -33,13 +33,14 @@ using namespace fg;
 
 constexpr int kMaxCols = 16384;   // 1024 threads of 2 units
 constexpr int kCUs = 256;
+constexpr int kNontemporal = 2;   // of a buffer access
 
 struct NormArgs {
   const void *x, *y;
   const float *pre, *post, *gate;
   void *r, *h;
   float* s;
-  int T, N, gate_kind, out;
+  int T, N, rows, gate_kind, out;   // rows: of a workgroup, one after another
   float alpha, beta, eps, inv_n;
 };
 
@@ -48,24 +49,39 @@ struct NormArgs {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void* base, long byte, int n) {
   return __builtin_amdgcn_make_buffer_rsrc((char*)base + byte, 0, n, 0x20000);
 }
-// Unit i of it: 8 elements.
-template <class R>
-__device__ __forceinline__ void load8(__amdgpu_buffer_rsrc_t row, int i, float* f) {
+// Unit i of it, 8 elements, as loaded and as floats. (Rows wait in registers as loaded:
+// bf16 takes half the room that way.) STREAM: past the caches, for batches that do not
+// fit them (kStreamBytes): T 8192, N 7168, bf16 93 -> 86 us forward, 155 -> 152 back.
+template <class R, bool STREAM = false>
+struct Unit {
+  u32x4 raw[8 / R::kPer16];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int i) {
 #pragma unroll
-  for (int c = 0; c < 8 / R::kPer16; ++c)
-    R::unpack(__builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row, i * 8 * R::kBytes + 16 * c, 0, 0)),
-              f + c * R::kPer16);
-}
-template <class R>
+    for (int c = 0; c < 8 / R::kPer16; ++c)
+      raw[c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row, i * 8 * R::kBytes + 16 * c, 0, STREAM ? kNontemporal : 0));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int c = 0; c < 8 / R::kPer16; ++c) raw[c] = u32x4{0u, 0u, 0u, 0u};
+  }
+  __device__ __forceinline__ void unpack(float* f) const {
+#pragma unroll
+    for (int c = 0; c < 8 / R::kPer16; ++c) R::unpack(raw[c], f + c * R::kPer16);
+  }
+};
+template <class R, bool STREAM = false>
 __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t row, int i, const float* f) {
 #pragma unroll
   for (int c = 0; c < 8 / R::kPer16; ++c)
-    __builtin_amdgcn_raw_buffer_store_b128(R::pack(f + c * R::kPer16), row, i * 8 * R::kBytes + 16 * c, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(R::pack(f + c * R::kPer16), row, i * 8 * R::kBytes + 16 * c, 0,
+                                           STREAM ? kNontemporal : 0);
 }
 // 8 weights of the lane's columns, `other` where there is no such vector.
 __device__ __forceinline__ void weights8(const float* w, int n, int i, float other, float* f) {
   if (w) {
-    load8<RowF32>(row_of(w, 0, n * 4), i, f);
+    Unit<RowF32> u;
+    u.load(row_of(w, 0, n * 4), i);
+    u.unpack(f);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = other;
@@ -101,7 +117,7 @@ struct BlockSum {
 
 __device__ __forceinline__ float rstd_of(float sum, float inv_n, float eps) { return 1.0f / sqrtf(fmaf(sum, inv_n, eps)); }
 
-template <class R, int NTH, int C>
+template <class R, int NTH, int C, bool STREAM>
 __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
   __shared__ float part[2][1][NTH / 64];
   __shared__ uint32_t top[2][NTH / 64];
@@ -119,31 +135,51 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
     for (int e = 0; e < 8; ++e) cw[c][e] *= g[e] * a.beta;
   }
   int flip = 0;
-  for (long t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float r[C][8], y[C][8];
-    const long at = t * a.N;
-    const int bytes = a.N * R::kBytes;
+  const int bytes = a.N * R::kBytes;
+  const long t0 = (long)blockIdx.x * a.rows, t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
+  Unit<R, STREAM> nx[C], ny[C];   // the next row, on its way
+  auto fetch = [&](long t) {
+    const long at = t * a.N * R::kBytes;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      load8<R>(row_of(a.x, at * R::kBytes, bytes), c * NTH + lane, r[c]);
-      if (a.y) load8<R>(row_of(a.y, at * R::kBytes, bytes), c * NTH + lane, y[c]);
+      nx[c].load(row_of(a.x, at, bytes), c * NTH + lane);
+      if (a.y) ny[c].load(row_of(a.y, at, bytes), c * NTH + lane);
     }
+  };
+  fetch(t0);
+  for (long t = t0; t < t1; ++t) {
+    const long at = t * a.N;
+    Unit<R, STREAM> x[C], y[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      x[c] = nx[c];
+      y[c] = ny[c];
+    }
+    if (t + 1 < t1) fetch(t + 1);
+    float r[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) x[c].unpack(r[c]);
     if (a.y) {
       float k = a.gate_kind == FG_GATE_TOKEN ? a.gate[t] : 1.0f;
       if (a.post) {
         float v[1] = {0.0f};
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+          float f[8];
+          y[c].unpack(f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[0] = fmaf(y[c][e], y[c][e], v[0]);
+          for (int e = 0; e < 8; ++e) v[0] = fmaf(f[e], f[e], v[0]);
+        }
         sum(v);
         k *= rstd_of(v[0], a.inv_n, a.eps);
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
+        float f[8];
+        y[c].unpack(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[c][e] = fmaf(y[c][e] * k, cw[c][e], a.alpha * r[c][e]);
-        store8<R>(row_of(a.r, at * R::kBytes, bytes), c * NTH + lane, r[c]);
+        for (int e = 0; e < 8; ++e) r[c][e] = fmaf(f[e] * k, cw[c][e], a.alpha * r[c][e]);
+        store8<R, STREAM>(row_of(a.r, at * R::kBytes, bytes), c * NTH + lane, r[c]);
       }
     }
     if (!a.pre) continue;
@@ -161,7 +197,7 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
     const __amdgpu_buffer_rsrc_t codes = row_of(a.h, at, a.N);   // 8-bit outputs
     if (a.out == FG_OUT_SAME) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) store8<R>(row_of(a.h, at * R::kBytes, bytes), c * NTH + lane, r[c]);
+      for (int c = 0; c < C; ++c) store8<R, STREAM>(row_of(a.h, at * R::kBytes, bytes), c * NTH + lane, r[c]);
     } else if (a.out == FG_OUT_INT8) {
       uint32_t m = 0;
 #pragma unroll
@@ -181,7 +217,7 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
         const int i = c * NTH + lane;
         uint32_t q[2];
         int8_encode<8>(r[c], s, inv, q);
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2v{q[0], q[1]}, codes, i * 8, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2v{q[0], q[1]}, codes, i * 8, 0, STREAM ? kNontemporal : 0);
       }
     } else {
       // 16 lanes have a 1x128 block; a group is wholly inside the row or past it
@@ -202,7 +238,7 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
           q[0] = e4m3x4_div(r[c][0], r[c][1], r[c][2], r[c][3], s);
           q[1] = e4m3x4_div(r[c][4], r[c][5], r[c][6], r[c][7], s);
         }
-        __builtin_amdgcn_raw_buffer_store_b64(q, codes, i * 8, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(q, codes, i * 8, 0, STREAM ? kNontemporal : 0);
         if (i < per && (lane & 15) == 0) a.s[(long)(i >> 4) * a.T + t] = s;
       }
     }
@@ -215,99 +251,140 @@ struct GradArgs {
   void *dx, *dy;
   float* dgate;   // per token
   float* ws;      // [workgroups][2][N]: sum dh rh, S
-  int T, N, gate_kind;
+  int T, N, rows, gate_kind;
   float alpha, beta, eps, inv_n;
 };
 
-template <class R, int NTH, int C>
+// LEAN: rows of more than 8192, whose 1024 threads have 128 registers each: the weights are
+// read again for each row (from the L2) and the next row is not fetched ahead.
+template <class R, int NTH, int C, bool LEAN, bool STREAM>
 __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
   __shared__ float part3[2][3][NTH / 64], part1[2][1][NTH / 64];
   const int lane = threadIdx.x;
   BlockSum<NTH, 3> sum3{part3};
   BlockSum<NTH, 1> sum1{part1};
-  float cw[C][8], pre[C][8], P[C][8], S[C][8];
+  float cw[LEAN ? 1 : C][8], pre[LEAN ? 1 : C][8], P[C][8], S[C][8];
+  auto read_pre = [&](int c) { weights8(a.pre, a.N, c * NTH + lane, 0.0f, pre[LEAN ? 0 : c]); };
+  auto read_cw = [&](int c) {
+    float g[8], *w = cw[LEAN ? 0 : c];
+    weights8(a.post, a.N, c * NTH + lane, 1.0f, w);
+    weights8(a.gate_kind == FG_GATE_CHANNEL ? a.gate : nullptr, a.N, c * NTH + lane, 1.0f, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] *= g[e] * a.beta;
+  };
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int i = c * NTH + lane;
-    float g[8];
-    weights8(a.post, a.N, i, 1.0f, cw[c]);
-    weights8(a.gate_kind == FG_GATE_CHANNEL ? a.gate : nullptr, a.N, i, 1.0f, g);
-    weights8(a.pre, a.N, i, 0.0f, pre[c]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cw[c][e] *= g[e] * a.beta;
-      P[c][e] = S[c][e] = 0.0f;
+    if (!LEAN) {
+      read_pre(c);
+      read_cw(c);
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) P[c][e] = S[c][e] = 0.0f;
   }
-  for (long t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float r[C][8], dh[C][8], d[C][8], y[C][8];
+  const int bytes = a.N * R::kBytes;
+  const long t0 = (long)blockIdx.x * a.rows, t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
+  Unit<R, STREAM> nr[C], nh[C], nd[C], ny[C];   // the next row, on its way
+#pragma unroll
+  for (int c = 0; c < C; ++c) nd[c].zero();
+  auto fetch = [&](long t) {
     const long at = t * a.N * R::kBytes;
-    const int bytes = a.N * R::kBytes;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * NTH + lane;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) d[c][e] = 0.0f;
       if (a.pre) {
-        load8<R>(row_of(a.r, at, bytes), i, r[c]);
-        load8<R>(row_of(a.dh, at, bytes), i, dh[c]);
+        nr[c].load(row_of(a.r, at, bytes), i);
+        nh[c].load(row_of(a.dh, at, bytes), i);
       }
-      if (a.dr) load8<R>(row_of(a.dr, at, bytes), i, d[c]);
-      if (a.y) load8<R>(row_of(a.y, at, bytes), i, y[c]);
+      if (a.y) ny[c].load(row_of(a.y, at, bytes), i);
+      if (a.dr) nd[c].load(row_of(a.dr, at, bytes), i);
     }
+  };
+  if (!LEAN) fetch(t0);
+  for (long t = t0; t < t1; ++t) {
+    const long at = t * bytes;
+    Unit<R, STREAM> r[C], dh[C], y[C];
+    float d[C][8];
+    if (LEAN) fetch(t);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      r[c] = nr[c];
+      dh[c] = nh[c];
+      y[c] = ny[c];
+      nd[c].unpack(d[c]);
+    }
+    if (!LEAN && t + 1 < t1) fetch(t + 1);
     float v[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+      float f[8], g[8];
+      if (a.pre) {
+        if (LEAN) read_pre(c);
+        r[c].unpack(f);
+        dh[c].unpack(g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (a.pre) {
-          v[0] = fmaf(r[c][e], r[c][e], v[0]);
-          v[1] = fmaf(dh[c][e] * pre[c][e], r[c][e], v[1]);
+        for (int e = 0; e < 8; ++e) {
+          v[0] = fmaf(f[e], f[e], v[0]);
+          v[1] = fmaf(g[e] * pre[LEAN ? 0 : c][e], f[e], v[1]);
         }
-        if (a.post) v[2] = fmaf(y[c][e], y[c][e], v[2]);
       }
+      if (a.post) {
+        y[c].unpack(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[2] = fmaf(f[e], f[e], v[2]);
+      }
+    }
     if (a.pre || a.post) sum3(v);
     if (a.pre) {
       const float rx = rstd_of(v[0], a.inv_n, a.eps);
       const float m = v[1] * rx * a.inv_n;   // mean of z rh
 #pragma unroll
-      for (int c = 0; c < C; ++c)
+      for (int c = 0; c < C; ++c) {
+        float f[8], g[8];
+        if (LEAN) read_pre(c);
+        r[c].unpack(f);
+        dh[c].unpack(g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float rh = r[c][e] * rx;
-          d[c][e] = fmaf(rx, fmaf(-rh, m, dh[c][e] * pre[c][e]), d[c][e]);
-          P[c][e] = fmaf(dh[c][e], rh, P[c][e]);
+          const float rh = f[e] * rx;
+          d[c][e] = fmaf(rx, fmaf(-rh, m, g[e] * pre[LEAN ? 0 : c][e]), d[c][e]);
+          P[c][e] = fmaf(g[e], rh, P[c][e]);
         }
+      }
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       float o[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = a.alpha * d[c][e];
-      store8<R>(row_of(a.dx, at, bytes), c * NTH + lane, o);
+      store8<R, STREAM>(row_of(a.dx, at, bytes), c * NTH + lane, o);
     }
     if (!a.y) continue;
     const float ry = a.post ? rstd_of(v[2], a.inv_n, a.eps) : 1.0f;
     const float gt = a.gate_kind == FG_GATE_TOKEN ? a.gate[t] : 1.0f;
     float q[1] = {0.0f};   // sum of dR yh, times the folded weights
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+      float f[8];
+      if (LEAN) read_cw(c);
+      y[c].unpack(f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        y[c][e] *= ry;
-        S[c][e] = fmaf(gt * d[c][e], y[c][e], S[c][e]);
-        d[c][e] *= cw[c][e];
-        q[0] = fmaf(d[c][e], y[c][e], q[0]);
+        const float yh = f[e] * ry;
+        S[c][e] = fmaf(gt * d[c][e], yh, S[c][e]);
+        d[c][e] *= cw[LEAN ? 0 : c][e];
+        q[0] = fmaf(d[c][e], yh, q[0]);
       }
+    }
     if (a.post || a.gate_kind == FG_GATE_TOKEN) sum1(q);
     if (a.gate_kind == FG_GATE_TOKEN && lane == 0) a.dgate[t] = q[0];
     const float m = a.post ? q[0] * a.inv_n : 0.0f, k = ry * gt;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float o[8];
+      float f[8], o[8];
+      y[c].unpack(f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = k * fmaf(-y[c][e], m, d[c][e]);
-      store8<R>(row_of(a.dy, at, bytes), c * NTH + lane, o);
+      for (int e = 0; e < 8; ++e) o[e] = k * fmaf(-f[e] * ry, m, d[c][e]);
+      store8<R, STREAM>(row_of(a.dy, at, bytes), c * NTH + lane, o);
     }
   }
 #pragma unroll
@@ -317,74 +394,85 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
   }
 }
 
-// The workgroups' sums added up: 32 columns a workgroup, 8 threads a column.
+// The workgroups' sums added up in a fixed order: 16 columns of P or of S a workgroup, 16
+// threads a column.
 struct SumArgs {
   const float *ws, *post, *gate;
   float *dpre, *dpost, *dgate;   // null: not asked for
   int groups, N;
   float beta;
 };
-constexpr int kSumCols = 32, kSumParts = 8;
+constexpr int kSumCols = 16, kSumParts = 16;
 __global__ __launch_bounds__(kSumCols * kSumParts) void block_norm_sums(SumArgs a) {
-  __shared__ float part[2][kSumParts][kSumCols];
+  __shared__ float part[kSumParts][kSumCols + 1];
+  const bool of_s = blockIdx.y != 0;
+  if (of_s ? !a.dpost && !a.dgate : !a.dpre) return;
   const int col = threadIdx.x % kSumCols, p = threadIdx.x / kSumCols;
   const int n = blockIdx.x * kSumCols + col, at = n < a.N ? n : 0;
-  float P = 0.0f, S = 0.0f;
-  for (int g = p; g < a.groups; g += kSumParts) {
-    P += a.ws[(long)g * 2 * a.N + at];
-    S += a.ws[((long)g * 2 + 1) * a.N + at];
-  }
-  part[0][p][col] = P;
-  part[1][p][col] = S;
+  const float* w = a.ws + (of_s ? a.N : 0) + at;
+  float s = 0.0f;
+#pragma unroll 8
+  for (int g = p; g < a.groups; g += kSumParts) s += w[(long)g * 2 * a.N];
+  part[p][col] = s;
   __syncthreads();
   if (p != 0 || n >= a.N) return;
-  P = S = 0.0f;
+  s = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kSumParts; ++k) {
-    P += part[0][k][col];
-    S += part[1][k][col];
-  }
-  if (a.dpre) a.dpre[n] = P;
-  if (a.dpost) a.dpost[n] = a.beta * (a.gate ? a.gate[n] : 1.0f) * S;
-  if (a.dgate) a.dgate[n] = a.beta * (a.post ? a.post[n] : 1.0f) * S;
+  for (int k = 0; k < kSumParts; ++k) s += part[k][col];
+  if (!of_s) a.dpre[n] = s;
+  if (of_s && a.dpost) a.dpost[n] = a.beta * (a.gate ? a.gate[n] : 1.0f) * s;
+  if (of_s && a.dgate) a.dgate[n] = a.beta * (a.post ? a.post[n] : 1.0f) * s;
 }
 
-// Workgroups of the gradient for T rows of N columns.
-int grad_threads(int N) { return N <= 512 ? 64 : N <= 2048 ? 256 : N <= 8192 ? 512 : 1024; }
-int grad_groups(int T, int N) {
-  const int most = kCUs * (1024 / grad_threads(N));
-  return T < most ? T : most;
+// Threads of a workgroup and rows it takes one after another, for T rows of N columns: as
+// many workgroups as are resident together, so each has a run of neighbouring rows (whose
+// E4M3 scales are neighbours in memory and meet in one XCD's L2).
+int norm_threads(int N) { return N <= 512 ? 64 : N <= 2048 ? 256 : N <= 8192 ? 512 : 1024; }
+int norm_rows(int T, int N) {
+  const int most = kCUs * (1024 / norm_threads(N));
+  return T <= most ? 1 : (T + most - 1) / most;
 }
+int grad_rows(int T, int N) {
+  const int most = kCUs * (N <= 2048 ? 512 / norm_threads(N) : 1);
+  return T <= most ? 1 : (T + most - 1) / most;
+}
+int grad_groups(int T, int N) { return (T + grad_rows(T, N) - 1) / grad_rows(T, N); }
+
+template <class R>
+bool streams(int T, int N) { return (long long)T * N * R::kBytes > kStreamBytes; }
 
 template <class R, int NTH, int C>
-int launch_norm(const NormArgs& a, hipStream_t s) {
-  const int most = kCUs * (1024 / NTH);
-  hipLaunchKernelGGL((block_norm<R, NTH, C>), dim3(a.T < most ? a.T : most), dim3(NTH), 0, s, a);
+int launch_norm(NormArgs a, hipStream_t s) {
+  a.rows = norm_rows(a.T, a.N);
+  const dim3 g((a.T + a.rows - 1) / a.rows), b(NTH);
+  if (streams<R>(a.T, a.N)) hipLaunchKernelGGL((block_norm<R, NTH, C, true>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((block_norm<R, NTH, C, false>), g, b, 0, s, a);
   return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
 }
 template <class R>
 int launch_norm_of(const NormArgs& a, hipStream_t s) {
-  const int per = a.N / 8;
-  if (per <= 64) return launch_norm<R, 64, 1>(a, s);
-  if (per <= 256) return launch_norm<R, 256, 1>(a, s);
-  if (per <= 512) return launch_norm<R, 256, 2>(a, s);
-  if (per <= 1024) return launch_norm<R, 256, 4>(a, s);
+  if (a.N <= 512) return launch_norm<R, 64, 1>(a, s);
+  if (a.N <= 2048) return launch_norm<R, 256, 1>(a, s);
+  if (a.N <= 4096) return launch_norm<R, 512, 1>(a, s);
+  if (a.N <= 8192) return launch_norm<R, 512, 2>(a, s);
   return launch_norm<R, 1024, 2>(a, s);
 }
 
-template <class R, int NTH, int C>
-int launch_grad(const GradArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((block_norm_grad<R, NTH, C>), dim3(grad_groups(a.T, a.N)), dim3(NTH), 0, s, a);
+template <class R, int NTH, int C, bool LEAN = false>
+int launch_grad(GradArgs a, hipStream_t s) {
+  a.rows = grad_rows(a.T, a.N);
+  const dim3 g(grad_groups(a.T, a.N)), b(NTH);
+  if (streams<R>(a.T, a.N)) hipLaunchKernelGGL((block_norm_grad<R, NTH, C, LEAN, true>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((block_norm_grad<R, NTH, C, LEAN, false>), g, b, 0, s, a);
   return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
 }
 template <class R>
 int launch_grad_of(const GradArgs& a, hipStream_t s) {
-  switch (grad_threads(a.N)) {
-    case 64: return launch_grad<R, 64, 1>(a, s);
-    case 256: return launch_grad<R, 256, 1>(a, s);
-    case 512: return launch_grad<R, 512, 2>(a, s);
-    default: return launch_grad<R, 1024, 2>(a, s);
-  }
+  if (a.N <= 512) return launch_grad<R, 64, 1>(a, s);
+  if (a.N <= 2048) return launch_grad<R, 256, 1>(a, s);
+  if (a.N <= 4096) return launch_grad<R, 512, 1>(a, s);
+  if (a.N <= 8192) return launch_grad<R, 512, 2>(a, s);
+  return launch_grad<R, 1024, 2, true>(a, s);
 }
 
 bool sizes_ok(int dtype, int T, int N, int gate_kind, float eps) {
@@ -411,7 +499,7 @@ int fg_block_norm(const void* x, const void* y, int dtype, const float* pre, con
     return FG_EINVAL;
   const int st = current_device(nullptr);
   if (st != FG_OK) return st;
-  const NormArgs a = {x, y, pre, post, gate, r, h, s, T, N, gate_kind, out, alpha, beta, eps, 1.0f / (float)N};
+  const NormArgs a = {x, y, pre, post, gate, r, h, s, T, N, 1, gate_kind, out, alpha, beta, eps, 1.0f / (float)N};
   return dtype == FG_BF16 ? launch_norm_of<RowBf16>(a, stream) : launch_norm_of<RowF32>(a, stream);
 }
 
@@ -439,7 +527,7 @@ int fg_block_norm_grad(const void* r, const void* dh, const void* dr, const void
   const int st = current_device(nullptr);
   if (st != FG_OK) return st;
   if (T > 0) {
-    const GradArgs a = {r, dh, dr, y, pre, post, gate, dx, dy, dgate, static_cast<float*>(ws), T, N, gate_kind,
+    const GradArgs a = {r, dh, dr, y, pre, post, gate, dx, dy, dgate, static_cast<float*>(ws), T, N, 1, gate_kind,
                         alpha, beta, eps, 1.0f / (float)N};
     const int rc = dtype == FG_BF16 ? launch_grad_of<RowBf16>(a, stream) : launch_grad_of<RowF32>(a, stream);
     if (rc != FG_OK) return rc;
@@ -447,7 +535,7 @@ int fg_block_norm_grad(const void* r, const void* dh, const void* dr, const void
   if (!sums) return FG_OK;
   const SumArgs b = {static_cast<const float*>(ws), post, channel ? gate : nullptr, pre ? dpre : nullptr,
                      post ? dpost : nullptr, channel ? dgate : nullptr, grad_groups(T, N), N, beta};
-  hipLaunchKernelGGL(block_norm_sums, dim3((N + kSumCols - 1) / kSumCols), dim3(kSumCols * kSumParts), 0, stream, b);
+  hipLaunchKernelGGL(block_norm_sums, dim3((N + kSumCols - 1) / kSumCols, 2), dim3(kSumCols * kSumParts), 0, stream, b);
   return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
 }
 

@@ -187,6 +187,20 @@ def test_dense_on_every_kernel(M, N, K, kernel):
         assert np.array_equal(d_bits(D), want), grid
 
 
+@pytest.mark.parametrize("columns", ["16 columns", "32 columns", "64 columns"])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (16, 72, 2064), (31, 136, 128), (33, 64, 1040), (48, 200, 1024), (61, 128, 7168),
+                                   (96, 264, 4112), (80, 64, 272), (128, 72, 3088), (300, 136, 1168)])
+def test_dense_streamed(M, N, K, columns):
+    """The weight-streaming kernel at each width, K from less than one piece of one wave to many rounds of all."""
+    if columns == "64 columns" and M > 96:
+        pytest.skip("up to 96 rows")
+    print(f"gemm_int8_nt {M}x{N}x{K} streamed, {columns}", flush=True)
+    a = operands((M,), 0, N, K, M + N + K)
+    with forced_int8(columns):
+        D = fg.gemm_int8_nt(*on_gpu(*a), new_out((M, N)))
+    assert np.array_equal(d_bits(D), ref_product(*a))
+
+
 def contiguous_rows(G, counts, seed, extra=128):
     """m_indices of experts with so many rows each, segments padded to 128, the tail all padding; a few rows
     inside the segments are padding too, and some padding ids are out of range."""
@@ -246,7 +260,9 @@ def test_masked(G, M_max, N, K, counts):
         c = min(max(c, 0), M_max)
         want[g, :c] = ref_product(A[g, :c], sa[g, :c], B[g], sb[g])
     a, mm = on_gpu(A, sa, B, sb), to_dev(np.array(counts, np.int32))
-    for kernel in (None, "256x256", "256x128", "128x256", "128x128", "64x128"):
+    for kernel in (None, "256x256", "256x128", "128x256", "128x128", "64x128", "16 columns", "32 columns", "64 columns"):
+        if kernel == "64 columns" and M_max > 96:
+            continue
         D = new_out((G, M_max, N))
         if kernel is None:
             fg.grouped_masked_int8(*a, D, mm)
