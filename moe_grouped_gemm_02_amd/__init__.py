@@ -890,6 +890,14 @@ def swiglu_quant_int8(h, plan=None, Q=None, s=None):
 
 
 # ---------------------------------------------------------------- norms around a block
+def _new_like(t, name, like):
+    """An output of a checked (contiguous) tensor's shape, type and device; empty_like costs half of empty."""
+    if t is None:
+        return _torch().empty_like(like)
+    _dev(t, name, like.shape, like.dtype, like.device)
+    return t
+
+
 NORM_OUTPUTS = {None: 0, "e4m3": 1, "e4m3_pow2": 2, "int8": 3}
 
 
@@ -944,16 +952,15 @@ def block_norm(x, y=None, pre=None, post=None, gate=None, alpha=1.0, beta=1.0, e
     if pre is None and quant is not None:
         raise ValueError("quant is for h, which needs pre")
     if y is not None:
-        r = _new(r, "r", (T, N), x.dtype, dev)
+        r = _new_like(r, "r", x)
     elif r is not None and r is not x:
         raise ValueError("without y the stream is x itself")
     if pre is None:
         h = s = None
     elif out == 0:
-        h, s = _new(h, "h", (T, N), x.dtype, dev), None
+        h, s = _new_like(h, "h", x), None
     elif out == 3:
         h, s = _int8_rows((T,), N, h, s, dev)
-        h = h.view(T, N)
     else:
         if N % 128:
             raise ValueError("E4M3 rows must be a multiple of 128 long")
@@ -981,7 +988,6 @@ def block_norm_grad(r, dh=None, dr=None, y=None, pre=None, post=None, gate=None,
     Returns (dx, dy, dgate, dpre, dpost): dx and dy in r's type, the vectors fp32; None where the forward call
     had no such input. dx may be dr or dh, dy may be y (in place)."""
     torch = _torch()
-    f32 = torch.float32
     if (dh is None) != (pre is None):
         raise ValueError("dh and pre belong together")
     if dh is None and dr is None:
@@ -992,16 +998,12 @@ def block_norm_grad(r, dh=None, dr=None, y=None, pre=None, post=None, gate=None,
         _dev(dh, "dh", (T, N), r.dtype, dev)
     if dr is not None:
         _dev(dr, "dr", (T, N), r.dtype, dev)
-    dx = _new(dx, "dx", (T, N), r.dtype, dev)
+    dx = _new_like(dx, "dx", r)
     if y is not None:
-        dy = _new(dy, "dy", (T, N), r.dtype, dev)
+        dy = _new_like(dy, "dy", r)
     elif dy is not None:
         raise ValueError("dy is y's gradient, and there is no y")
-    # the vectors' gradients in one allocation
-    sizes = (N if pre is not None else 0, N if post is not None else 0, gate.numel() if gate is not None else 0)
-    dpre, dpost, dgate = torch.empty(sum(sizes), dtype=f32, device=dev).split_with_sizes(sizes)
-    dpre, dpost = dpre if pre is not None else None, dpost if post is not None else None
-    dgate = dgate.view(gate.shape) if gate is not None else None
+    dgate, dpre, dpost = (None if v is None else torch.empty_like(v) for v in (gate, pre, post))
     ws = torch.empty(_block_norm_grad_workspace(T, N), dtype=torch.uint8, device=dev)
     _call("fg_block_norm_grad", dev, _ptr(r), _opt_ptr(dh), _opt_ptr(dr), _opt_ptr(y), dt, _opt_ptr(pre), _opt_ptr(post),
           _opt_ptr(gate), kind, _ptr(dx), _opt_ptr(dy), _opt_ptr(dgate), _opt_ptr(dpre), _opt_ptr(dpost), _ptr(ws), T, N,
