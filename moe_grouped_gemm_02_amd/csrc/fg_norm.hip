@@ -117,7 +117,8 @@ struct BlockSum {
 
 __device__ __forceinline__ float rstd_of(float sum, float inv_n, float eps) { return 1.0f / sqrtf(fmaf(sum, inv_n, eps)); }
 
-template <class R, int NTH, int C, bool STREAM>
+// Y: with a block's output.
+template <class R, int NTH, int C, bool Y, bool STREAM>
 __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
   __shared__ float part[2][1][NTH / 64];
   __shared__ uint32_t top[2][NTH / 64];
@@ -127,12 +128,14 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = c * NTH + lane;
-    float g[8];
-    weights8(a.post, a.N, i, 1.0f, cw[c]);
-    weights8(a.gate_kind == FG_GATE_CHANNEL ? a.gate : nullptr, a.N, i, 1.0f, g);
     weights8(a.pre, a.N, i, 0.0f, pre[c]);
+    if (Y) {
+      float g[8];
+      weights8(a.post, a.N, i, 1.0f, cw[c]);
+      weights8(a.gate_kind == FG_GATE_CHANNEL ? a.gate : nullptr, a.N, i, 1.0f, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) cw[c][e] *= g[e] * a.beta;
+      for (int e = 0; e < 8; ++e) cw[c][e] *= g[e] * a.beta;
+    }
   }
   int flip = 0;
   const int bytes = a.N * R::kBytes;
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       nx[c].load(row_of(a.x, at, bytes), c * NTH + lane);
-      if (a.y) ny[c].load(row_of(a.y, at, bytes), c * NTH + lane);
+      if (Y) ny[c].load(row_of(a.y, at, bytes), c * NTH + lane);
     }
   };
   fetch(t0);
@@ -159,7 +162,7 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
     float r[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) x[c].unpack(r[c]);
-    if (a.y) {
+    if (Y) {
       float k = a.gate_kind == FG_GATE_TOKEN ? a.gate[t] : 1.0f;
       if (a.post) {
         float v[1] = {0.0f};
@@ -394,7 +397,7 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
   }
 }
 
-// The workgroups' sums added up in a fixed order: 16 columns of P or of S a workgroup, 16
+// The workgroups' sums added up in a fixed order: 16 columns of P or of S a workgroup, 64
 // threads a column.
 struct SumArgs {
   const float *ws, *post, *gate;
@@ -402,7 +405,7 @@ struct SumArgs {
   int groups, N;
   float beta;
 };
-constexpr int kSumCols = 16, kSumParts = 16;
+constexpr int kSumCols = 16, kSumParts = 64;
 __global__ __launch_bounds__(kSumCols * kSumParts) void block_norm_sums(SumArgs a) {
   __shared__ float part[kSumParts][kSumCols + 1];
   const bool of_s = blockIdx.y != 0;
@@ -415,10 +418,14 @@ __global__ __launch_bounds__(kSumCols * kSumParts) void block_norm_sums(SumArgs 
   for (int g = p; g < a.groups; g += kSumParts) s += w[(long)g * 2 * a.N];
   part[p][col] = s;
   __syncthreads();
-  if (p != 0 || n >= a.N) return;
+  if (p >= 4) return;
   s = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kSumParts; ++k) s += part[k][col];
+  for (int k = 0; k < kSumParts / 4; ++k) s += part[p * (kSumParts / 4) + k][col];
+  // four lanes of the first wave have a column's quarters, 16 lanes apart
+  s += __shfl_xor(s, 16);
+  s += __shfl_xor(s, 32);
+  if (p != 0 || n >= a.N) return;
   if (!of_s) a.dpre[n] = s;
   if (of_s && a.dpost) a.dpost[n] = a.beta * (a.gate ? a.gate[n] : 1.0f) * s;
   if (of_s && a.dgate) a.dgate[n] = a.beta * (a.post ? a.post[n] : 1.0f) * s;
@@ -428,8 +435,8 @@ __global__ __launch_bounds__(kSumCols * kSumParts) void block_norm_sums(SumArgs 
 // many workgroups as are resident together, so each has a run of neighbouring rows (whose
 // E4M3 scales are neighbours in memory and meet in one XCD's L2).
 int norm_threads(int N) { return N <= 512 ? 64 : N <= 2048 ? 256 : N <= 8192 ? 512 : 1024; }
-int norm_rows(int T, int N) {
-  const int most = kCUs * (1024 / norm_threads(N));
+int norm_rows(int T, int N, bool y) {
+  const int most = kCUs * ((y ? 1024 : 1536) / norm_threads(N));
   return T <= most ? 1 : (T + most - 1) / most;
 }
 int grad_rows(int T, int N) {
@@ -443,10 +450,13 @@ bool streams(int T, int N) { return (long long)T * N * R::kBytes > kStreamBytes;
 
 template <class R, int NTH, int C>
 int launch_norm(NormArgs a, hipStream_t s) {
-  a.rows = norm_rows(a.T, a.N);
+  a.rows = norm_rows(a.T, a.N, a.y != nullptr);
   const dim3 g((a.T + a.rows - 1) / a.rows), b(NTH);
-  if (streams<R>(a.T, a.N)) hipLaunchKernelGGL((block_norm<R, NTH, C, true>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((block_norm<R, NTH, C, false>), g, b, 0, s, a);
+  const bool stream = streams<R>(a.T, a.N);
+  if (a.y && stream) hipLaunchKernelGGL((block_norm<R, NTH, C, true, true>), g, b, 0, s, a);
+  else if (a.y) hipLaunchKernelGGL((block_norm<R, NTH, C, true, false>), g, b, 0, s, a);
+  else if (stream) hipLaunchKernelGGL((block_norm<R, NTH, C, false, true>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((block_norm<R, NTH, C, false, false>), g, b, 0, s, a);
   return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
 }
 template <class R>
