@@ -18,7 +18,7 @@ struct Tile {
   double eff;   // fraction of the matrix-core rate the tile's K loop sustains
 };
 constexpr Tile kTiles[] = {{256, 256, Cfg0::W, 0.80}, {256, 128, Cfg1::W, 0.75}, {128, 256, Cfg2::W, 0.75},
-                           {128, 128, Cfg3::W, 0.70}, {64, 128, Cfg4::W, 0.60}};
+                           {128, 128, Cfg3::W, 0.70}, {64, 128, Cfg4::W, 0.60}, {128, 160, Cfg5::W, 0.70}};
 constexpr int kNumTiles = sizeof(kTiles) / sizeof(kTiles[0]);
 constexpr int kWide = 0, kNarrow = 1, kHalf = 2;
 constexpr int kMaxK = 131056;     // 128^2 K < 2^31: the 32-bit sum is exact
@@ -53,11 +53,12 @@ struct Choice {
 //   M 64   N 4096 9.6 / 10.5 / 17.5 / 18.6    N 7168 16.5 / 11.9 / 17.6 / 19.0    N 14336 42.9 / 29.8 / 25.4 / 32.9
 //          N 28672 77.9 / 58.9 / 46.7 / 42.4
 //   M 128  N 4096 14.5 / 15.9 / - / 18.6    N 7168 25.6 / 17.1 / - / 19.2    N 14336 62.7 / 41.4 / - / 33.5
+//   M 512  N 1024 13.7 / 15.9 / - / 18.3    M 2048, N 256 19.8 / 20.9 / - / 18.4    M 4096, N 128, K 1024 8.6 / 7.3 / - / 5.2
 Choice skinny(int layout, int M, int N, int G, int force = -1) {
   Choice c;
   if (layout != FG_LAYOUT_MASKED) G = 1;
   const long w = ceil_div(M, kSkinnyRows) * ceil_div(N, 64) * G;
-  int i = w <= 80 ? 0 : w <= 160 ? 1 : (w <= 320 && M <= 96) || M <= 16 ? 2 : -1;
+  int i = M > 4 * kSkinnyRows ? -1 : w <= 64 ? 0 : w <= 128 ? 1 : (w <= 320 && M <= 96) || M <= 16 ? 2 : -1;
   if (force >= 0) i = force;
   if (i < 0) return c;
   int steps = (int)ceil_div(M < kSkinnyRows ? M : kSkinnyRows, 16);

@@ -36,12 +36,13 @@ struct Int8Cfg {
   static constexpr int DMA_PER_STAGE = A_INSTR + B_INSTR;
   static constexpr int A_BYTES = A_INSTR * W * 1024, B_BYTES = B_INSTR * W * 1024;
   // two slots of a tile's scales (this tile's and the next one's), then the rings
-  static constexpr int SC_BYTES = (BM + BN) * 4;
+  static constexpr int SC_LOADS = BM / 64 + (BN + 63) / 64;   // 64 scales a load
+  static constexpr int SC_BYTES = SC_LOADS * 256;
   static constexpr int A_BASE = 2 * SC_BYTES;
   static constexpr int B_BASE = A_BASE + ASTAGES * A_BYTES;
   static constexpr int LDS_BYTES = B_BASE + STAGES * B_BYTES;
   static constexpr int UNROLL = lcm_c(lcm_c(lcm_c(STAGES, ASTAGES), RING / gcd_c(TN, RING)), FA2 ? 2 : 1);
-  static_assert(WM % 16 == 0 && WN % 32 == 0 && BM % 64 == 0 && BN % 64 == 0, "whole sub-tile pairs, scales 64 at a time");
+  static_assert(WM % 16 == 0 && WN % 32 == 0 && BM % 64 == 0, "whole sub-tile pairs, scales 64 at a time");
   static_assert(BM % WGM == 0 && BN % WGN == 0, "waves must split the tile evenly");
   static_assert(ASTAGES >= 2 && ASTAGES <= STAGES && (STAGES != 2 || ASTAGES == 2), "ring depths");
   static_assert(STAGES * DMA_PER_STAGE <= 63, "too many DMA instructions in flight per wave");
@@ -139,10 +140,10 @@ __device__ __forceinline__ void int8_tiles(const Params& p, lds_u8* const lds, N
     }
     const uint32_t at = lds_addr + par * T::SC_BYTES;
 #pragma unroll
-    for (int q = 0; q < ((BM + BN) / 64 + W - 1) / W; ++q) {
+    for (int q = 0; q < (T::SC_LOADS + W - 1) / W; ++q) {
       const int i = q * W + wave;
       if (i < BM / 64) dma4<0>(rsSA, (uint32_t)(i * 64 + lane) * 4u, 0u, at + i * 256);
-      else if (i < (BM + BN) / 64) dma4<0>(rsSB, (uint32_t)((i - BM / 64) * 64 + lane) * 4u, 0u, at + i * 256);
+      else if (i < T::SC_LOADS) dma4<0>(rsSB, (uint32_t)((i - BM / 64) * 64 + lane) * 4u, 0u, at + i * 256);
     }
   };
   // Scalar offsets of one DMA group, A of K-block ka and B of K-block kbb, and what

@@ -50,6 +50,7 @@ hipError_t launch_int8(int tile, const Params& p, int grid, hipStream_t s) {
     case 2: return launch_tile<LAYOUT, Cfg2>(p, grid, s);
     case 3: return launch_tile<LAYOUT, Cfg3>(p, grid, s);
     case 4: return launch_tile<LAYOUT, Cfg4>(p, grid, s);
+    case 5: return launch_tile<LAYOUT, Cfg5>(p, grid, s);
     case kSplit:
       if constexpr (LAYOUT == kDense) {
         hipLaunchKernelGGL((int8_gemm_split<Cfg0, Cfg1>), dim3(grid), dim3(Cfg0::THREADS), 0, s, p);

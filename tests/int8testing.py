@@ -7,8 +7,8 @@ import ctypes
 import moe_grouped_gemm_02_amd as fg
 from fgtesting import testing_lib
 
-TILES = {"256x256": 0, "256x128": 1, "128x256": 2, "128x128": 3, "64x128": 4, "split": 5, "runs": 6,
-         "16 columns": 7, "32 columns": 8, "64 columns": 9}
+TILES = {"256x256": 0, "256x128": 1, "128x256": 2, "128x128": 3, "64x128": 4, "128x160": 5,
+         "split": 6, "runs": 7, "16 columns": 8, "32 columns": 9, "64 columns": 10}
 
 
 @contextlib.contextmanager

@@ -174,7 +174,7 @@ def test_dense(M, N, K):
     assert np.array_equal(d_bits(D), ref_product(*a))
 
 
-@pytest.mark.parametrize("kernel", ["256x256", "256x128", "128x256", "128x128", "64x128", "split"])
+@pytest.mark.parametrize("kernel", ["256x256", "256x128", "128x256", "128x128", "64x128", "128x160", "split"])
 @pytest.mark.parametrize("M,N,K", [(1, 520, 16), (70, 520, 128), (257, 776, 272), (300, 1032, 400), (513, 520, 1168)])
 def test_dense_on_every_kernel(M, N, K, kernel):
     print(f"gemm_int8_nt {M}x{N}x{K} on {kernel}", flush=True)
@@ -239,7 +239,7 @@ def check_contiguous(G, N, K, counts, kernels):
                                           (5, 136, 1040, [0, 0, 640, 7, 128]), (2, 1032, 400, [700, 300])])
 def test_contiguous(G, N, K, counts):
     print(f"grouped_contiguous_int8 G={G} {N}x{K} {counts}", flush=True)
-    check_contiguous(G, N, K, counts, [(None, 0), ("128x256", 0), ("128x128", 0), ("64x128", 0), ("runs", 1), ("runs", 5),
+    check_contiguous(G, N, K, counts, [(None, 0), ("128x256", 0), ("128x128", 0), ("64x128", 0), ("128x160", 0), ("runs", 1), ("runs", 5),
                                        ("runs", 0)])
 
 
@@ -260,7 +260,7 @@ def test_masked(G, M_max, N, K, counts):
         c = min(max(c, 0), M_max)
         want[g, :c] = ref_product(A[g, :c], sa[g, :c], B[g], sb[g])
     a, mm = on_gpu(A, sa, B, sb), to_dev(np.array(counts, np.int32))
-    for kernel in (None, "256x256", "256x128", "128x256", "128x128", "64x128", "16 columns", "32 columns", "64 columns"):
+    for kernel in (None, "256x256", "256x128", "128x256", "128x128", "64x128", "128x160", "16 columns", "32 columns", "64 columns"):
         if kernel == "64 columns" and M_max > 96:
             continue
         D = new_out((G, M_max, N))
