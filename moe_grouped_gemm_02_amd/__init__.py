@@ -135,9 +135,15 @@ def _check(code, what):
         raise FGError(f"{what}: {strerror(code)} (code {code})")
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 _raw_stream = None
@@ -169,11 +175,10 @@ def _call(fn, dev, *args):
     """Calls entry point `fn` with `dev` as the current device (the library
     launches on the current device, on the stream passed last) and raises
     FGError on a nonzero return code."""
-    torch = _torch()
     if _current_device is not None and _current_device() == dev.index:
         code = getattr(_lib, fn)(*args)
     else:
-        with torch.cuda.device(dev):
+        with _torch().cuda.device(dev):
             code = getattr(lib(), fn)(*args)
     if code:
         _check(code, fn)
@@ -777,67 +782,84 @@ def adapters(D, x, A, B, scales, plan, out=None):
 
 
 # ---------------------------------------------------------------- 8-bit integers
-def _int8(t, name, shape, dev=None):
-    _dev(t, name, shape, _torch().int8, dev)
+# These calls check their tensors in one expression of plain attributes (a third of the time of a
+# check each, and a quarter of a small call); where it fails, _dev names the tensor and what is wrong.
+def _is(t, dtype, shape, index):
+    """Whether t is a contiguous tensor of this type and shape on GPU `index`."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
-def _int8_product(A, sa, B, sb, D, lead, N, K):
-    """Checks of the operands of an integer product; lead: the leading dimensions of A and D."""
+def _int8_product(fn, A, sa, B, sb, D, lead, N, K, index, *sizes):
+    """Checks and makes the call of an integer product; lead: the leading dimensions of A and D, index: the
+    layout's tensor with its name and shape (None: dense), sizes: the call's."""
     torch = _torch()
-    dev = A.device
-    _int8(A, "A", lead + (K,))
-    _int8(B, "B", B.shape, dev)
+    d = A.get_device()
+    i8, f32 = torch.int8, torch.float32
+    if not (d >= 0 and A.dtype is i8 and A.is_contiguous() and _is(B, i8, B.shape, d) and _is(sa, f32, lead, d)
+            and _is(sb, f32, B.shape[:-1], d) and _is(D, torch.bfloat16, lead + (N,), d)
+            and (index is None or _is(index[0], torch.int32, index[2], d))):
+        dev = A.device
+        _dev(A, "A", lead + (K,), i8)
+        _dev(B, "B", B.shape, i8, dev)
+        _dev(sa, "sa", lead, f32, dev)
+        _dev(sb, "sb", B.shape[:-1], f32, dev)
+        _dev(D, "D", lead + (N,), torch.bfloat16, dev)
+        if index is not None:
+            _dev(index[0], index[1], index[2], torch.int32, dev)
     if K % 16 or not 16 <= K <= 131056 or N % 8:
         raise ValueError("K must be a multiple of 16 from 16 to 131056 and N of 8")
-    _dev(sa, "sa", lead, torch.float32, dev)
-    _dev(sb, "sb", B.shape[:-1], torch.float32, dev)
-    _dev(D, "D", lead + (N,), torch.bfloat16, dev)
-    return dev
+    stream = _raw_stream(d) if _raw_stream is not None else _stream(A)
+    if index is None:
+        _call(fn, A.device, A.data_ptr(), sa.data_ptr(), B.data_ptr(), sb.data_ptr(), D.data_ptr(), *sizes, stream)
+    else:
+        _call(fn, A.device, A.data_ptr(), sa.data_ptr(), B.data_ptr(), sb.data_ptr(), D.data_ptr(), index[0].data_ptr(),
+              *sizes, stream)
+    return D
 
 
 def gemm_int8_nt(A, sa, B, sb, D):
     """Dense D[m, n] = sa[m] sb[n] sum_k A[m, k] B[n, k]: A [M, K] and B [N, K] int8, sa [M] and
     sb [N] float32, the sum exact in 32-bit integers; writes D [M, N] bfloat16 in place."""
-    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
-        raise ValueError(f"A must be [M, K] and B [N, K], got {tuple(A.shape)} and {tuple(B.shape)}")
-    (M, K), N = A.shape, B.shape[0]
-    dev = _int8_product(A, sa, B, sb, D, (M,), N, K)
-    _call("fg_gemm_int8_nt", dev, _ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(D), M, N, K, _stream(A))
-    return D
+    a, b = A.shape, B.shape
+    if len(a) != 2 or len(b) != 2 or a[1] != b[1]:
+        raise ValueError(f"A must be [M, K] and B [N, K], got {tuple(a)} and {tuple(b)}")
+    (M, K), N = a, b[0]
+    return _int8_product("fg_gemm_int8_nt", A, sa, B, sb, D, (M,), N, K, None, M, N, K)
 
 
 def grouped_contiguous_int8(A, sa, B, sb, D, m_indices):
     """gemm_int8_nt in the contiguous layout: rows of A belong to expert m_indices[row] (-1 =
     padding, not written); B [G, N, K], sb [G, N]."""
-    if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
-        raise ValueError(f"A must be [M, K] and B [G, N, K], got {tuple(A.shape)} and {tuple(B.shape)}")
-    (M, K), (G, N) = A.shape, B.shape[:2]
-    dev = _int8_product(A, sa, B, sb, D, (M,), N, K)
-    _dev(m_indices, "m_indices", (M,), _torch().int32, dev)
-    _call("fg_grouped_contiguous_int8", dev, _ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(D), _ptr(m_indices), M, N, K, G,
-          _stream(A))
-    return D
+    a, b = A.shape, B.shape
+    if len(a) != 2 or len(b) != 3 or a[1] != b[2]:
+        raise ValueError(f"A must be [M, K] and B [G, N, K], got {tuple(a)} and {tuple(b)}")
+    (M, K), (G, N, _) = a, b
+    return _int8_product("fg_grouped_contiguous_int8", A, sa, B, sb, D, (M,), N, K, (m_indices, "m_indices", (M,)),
+                         M, N, K, G)
 
 
 def grouped_masked_int8(A, sa, B, sb, D, masked_m):
     """gemm_int8_nt in the masked layout: expert g has masked_m[g] valid rows of A[g], and only
     those of D[g] are written; A [G, M_max, K], sa [G, M_max], B [G, N, K], sb [G, N]."""
-    if A.dim() != 3 or B.dim() != 3 or A.shape[2] != B.shape[2] or A.shape[0] != B.shape[0]:
-        raise ValueError(f"A must be [G, M_max, K] and B [G, N, K], got {tuple(A.shape)} and {tuple(B.shape)}")
-    (G, M_max, K), N = A.shape, B.shape[1]
-    dev = _int8_product(A, sa, B, sb, D, (G, M_max), N, K)
-    _dev(masked_m, "masked_m", (G,), _torch().int32, dev)
-    _call("fg_grouped_masked_int8", dev, _ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(D), _ptr(masked_m), G, M_max, N, K,
-          _stream(A))
-    return D
+    a, b = A.shape, B.shape
+    if len(a) != 3 or len(b) != 3 or a[2] != b[2] or a[0] != b[0]:
+        raise ValueError(f"A must be [G, M_max, K] and B [G, N, K], got {tuple(a)} and {tuple(b)}")
+    (G, M_max, K), N = a, b[1]
+    return _int8_product("fg_grouped_masked_int8", A, sa, B, sb, D, (G, M_max), N, K, (masked_m, "masked_m", (G,)),
+                         G, M_max, N, K)
 
 
-def _int8_rows(lead, K, q, s, dev):
-    """Outputs of an integer quantiser: codes [*lead, K] and scales lead."""
+def _int8_rows(x, lead, K, q, s):
+    """Outputs of an integer quantiser on x's device: codes [*lead, K] and scales lead."""
     torch = _torch()
     if K % 16 or not 16 <= K <= 65536:
         raise ValueError("rows must be a multiple of 16 long, from 16 to 65536")
-    return _new(q, "q", lead + (K,), torch.int8, dev), _new(s, "s", lead, torch.float32, dev)
+    shape = tuple(lead) + (K,)
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.int8) if x.shape == shape else torch.empty(shape, dtype=torch.int8, device=x.device)
+    else:
+        _dev(q, "q", shape, torch.int8, x.device)
+    return q, _new(s, "s", tuple(lead), torch.float32, x.device)
 
 
 def quant_int8(x, q=None, s=None):
@@ -848,8 +870,8 @@ def quant_int8(x, q=None, s=None):
         raise ValueError("x must be [..., rows, K]")
     lead, K = x.shape[:-1], x.shape[-1]
     _dev(x, "x", x.shape)
-    q, s = _int8_rows(lead, K, q, s, x.device)
-    _call("fg_quant_int8", x.device, _ptr(x), dt, _ptr(q), _ptr(s), lead.numel(), K, _stream(x))
+    q, s = _int8_rows(x, lead, K, q, s)
+    _call("fg_quant_int8", x.device, _ptr(x), dt, _ptr(q), _ptr(s), s.numel(), K, _stream(x))
     return q, s
 
 
@@ -865,7 +887,7 @@ def dispatch_quant_int8(x, plan, w=None, Q=None, s=None):
     _dev(x, "x", (T, H), None, dev)
     if w is not None:
         _dev(w, "w", (T, k), _torch().float32, dev)
-    Q, s = _int8_rows(plan.lead, H, Q, s, dev)
+    Q, s = _int8_rows(x, plan.lead, H, Q, s)
     _call("fg_dispatch_quant_int8", dev, _ptr(x), dt, _ptr(plan.rows), _opt_ptr(w), _ptr(Q), _ptr(s), T, k, H,
           plan.capacity, _stream(x))
     return Q, s
@@ -879,13 +901,12 @@ def swiglu_quant_int8(h, plan=None, Q=None, s=None):
     if h.dim() < 2 or h.shape[-1] % 256:
         raise ValueError("h must be [..., rows, 2 I] with 2 I a multiple of 256")
     lead, I = h.shape[:-1], h.shape[-1] // 2
-    dev = h.device
     _dev(h, "h", h.shape)
-    if plan is not None and (lead != plan.lead or dev != plan.device):
-        raise ValueError(f"h has shape {tuple(h.shape)} on {dev}, the plan's rows are {plan.lead} on {plan.device}")
-    Q, s = _int8_rows(lead, I, Q, s, dev)
-    _call("fg_swiglu_quant_int8", dev, _ptr(h), dt, None if plan is None else _ptr(plan.slots), _ptr(Q), _ptr(s),
-          lead.numel(), I, _stream(h))
+    if plan is not None and (lead != plan.lead or h.device != plan.device):
+        raise ValueError(f"h has shape {tuple(h.shape)} on {h.device}, the plan's rows are {plan.lead} on {plan.device}")
+    Q, s = _int8_rows(h, lead, I, Q, s)
+    _call("fg_swiglu_quant_int8", h.device, _ptr(h), dt, None if plan is None else _ptr(plan.slots), _ptr(Q), _ptr(s),
+          s.numel(), I, _stream(h))
     return Q, s
 
 
@@ -902,33 +923,33 @@ NORM_OUTPUTS = {None: 0, "e4m3": 1, "e4m3_pow2": 2, "int8": 3}
 
 
 def _norm_args(x, name, y, pre, post, gate, eps):
-    """Checks what block_norm and its gradient share: (element type, T, N, gate kind)."""
-    dt = _elem(x, name)
-    f32 = _torch().float32
-    if x.dim() != 2:
-        raise ValueError(f"{name} must be [T, N], got {tuple(x.shape)}")
-    T, N = x.shape
-    dev = x.device
-    _dev(x, name, (T, N))
+    """Checks what block_norm and its gradient share: (element type, T, N, gate kind, GPU)."""
+    torch = _torch()
+    dt, shape, f32, d = _elem(x, name), x.shape, torch.float32, x.get_device()
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be [T, N], got {tuple(shape)}")
+    T, N = shape
+    if not (d >= 0 and x.is_contiguous()):
+        _dev(x, name, shape)
     if N % 8 or not 8 <= N <= 16384:
         raise ValueError("N must be a multiple of 8 from 8 to 16384")
     if not eps > 0:
         raise ValueError("eps must be positive")
     if y is not None:
-        _dev(y, "y", (T, N), x.dtype, dev)
+        if not _is(y, x.dtype, shape, d):
+            _dev(y, "y", shape, x.dtype, x.device)
     elif post is not None or gate is not None:
         raise ValueError("post and gate belong to a block's output y")
-    if pre is not None:
-        _dev(pre, "pre", (N,), f32, dev)
-    if post is not None:
-        _dev(post, "post", (N,), f32, dev)
+    if pre is not None and not _is(pre, f32, (N,), d):
+        _dev(pre, "pre", (N,), f32, x.device)
+    if post is not None and not _is(post, f32, (N,), d):
+        _dev(post, "post", (N,), f32, x.device)
     if gate is None:
-        return dt, T, N, 0
-    if gate.dim() == 1:
-        _dev(gate, "gate", (N,), f32, dev)
-        return dt, T, N, 1
-    _dev(gate, "gate", (T, 1), f32, dev)
-    return dt, T, N, 2
+        return dt, T, N, 0, d
+    kind = 1 if gate.dim() == 1 else 2
+    if not _is(gate, f32, (N,) if kind == 1 else (T, 1), d):
+        _dev(gate, "gate", (N,) if kind == 1 else (T, 1), f32, x.device)
+    return dt, T, N, kind, d
 
 
 def block_norm(x, y=None, pre=None, post=None, gate=None, alpha=1.0, beta=1.0, eps=1e-6, quant=None, r=None, h=None, s=None):
@@ -947,8 +968,8 @@ def block_norm(x, y=None, pre=None, post=None, gate=None, alpha=1.0, beta=1.0, e
         raise ValueError(f"quant must be one of {list(NORM_OUTPUTS)}, got {quant!r}")
     if y is None and pre is None:
         raise ValueError("block_norm needs a block's output y, the next norm's weight pre, or both")
-    dt, T, N, kind = _norm_args(x, "x", y, pre, post, gate, eps)
-    dev, out = x.device, NORM_OUTPUTS[quant]
+    dt, T, N, kind, d = _norm_args(x, "x", y, pre, post, gate, eps)
+    out = NORM_OUTPUTS[quant]
     if pre is None and quant is not None:
         raise ValueError("quant is for h, which needs pre")
     if y is not None:
@@ -960,17 +981,18 @@ def block_norm(x, y=None, pre=None, post=None, gate=None, alpha=1.0, beta=1.0, e
     elif out == 0:
         h, s = _new_like(h, "h", x), None
     elif out == 3:
-        h, s = _int8_rows((T,), N, h, s, dev)
+        h, s = _int8_rows(x, (T,), N, h, s)
     else:
         if N % 128:
             raise ValueError("E4M3 rows must be a multiple of 128 long")
         if h is None:
-            h = torch.empty((T, N), dtype=torch.uint8, device=dev)
+            h = torch.empty_like(x, dtype=torch.uint8)
         else:
-            _fp8(h, "h", (T, N), dev)
-        s = _new(s, "s", (N // 128, T), torch.float32, dev)
-    _call("fg_block_norm", dev, _ptr(x), _opt_ptr(y), dt, _opt_ptr(pre), _opt_ptr(post), _opt_ptr(gate), kind,
-          None if y is None else _ptr(r), _opt_ptr(h), _opt_ptr(s), out, T, N, alpha, beta, eps, _stream(x))
+            _fp8(h, "h", (T, N), x.device)
+        s = _new(s, "s", (N // 128, T), torch.float32, x.device)
+    _call("fg_block_norm", x.device, _ptr(x), _opt_ptr(y), dt, _opt_ptr(pre), _opt_ptr(post), _opt_ptr(gate), kind,
+          None if y is None else _ptr(r), _opt_ptr(h), _opt_ptr(s), out, T, N, alpha, beta, eps,
+          _raw_stream(d) if _raw_stream is not None else _stream(x))
     return (x if y is None else r), h, s
 
 
@@ -992,20 +1014,20 @@ def block_norm_grad(r, dh=None, dr=None, y=None, pre=None, post=None, gate=None,
         raise ValueError("dh and pre belong together")
     if dh is None and dr is None:
         raise ValueError("block_norm_grad needs dh, dr, or both")
-    dt, T, N, kind = _norm_args(r, "r", y, pre, post, gate, eps)
-    dev = r.device
-    if dh is not None:
-        _dev(dh, "dh", (T, N), r.dtype, dev)
-    if dr is not None:
-        _dev(dr, "dr", (T, N), r.dtype, dev)
+    dt, T, N, kind, d = _norm_args(r, "r", y, pre, post, gate, eps)
+    if dh is not None and not _is(dh, r.dtype, (T, N), d):
+        _dev(dh, "dh", (T, N), r.dtype, r.device)
+    if dr is not None and not _is(dr, r.dtype, (T, N), d):
+        _dev(dr, "dr", (T, N), r.dtype, r.device)
     dx = _new_like(dx, "dx", r)
     if y is not None:
         dy = _new_like(dy, "dy", r)
     elif dy is not None:
         raise ValueError("dy is y's gradient, and there is no y")
     dgate, dpre, dpost = (None if v is None else torch.empty_like(v) for v in (gate, pre, post))
+    dev = r.device
     ws = torch.empty(_block_norm_grad_workspace(T, N), dtype=torch.uint8, device=dev)
     _call("fg_block_norm_grad", dev, _ptr(r), _opt_ptr(dh), _opt_ptr(dr), _opt_ptr(y), dt, _opt_ptr(pre), _opt_ptr(post),
           _opt_ptr(gate), kind, _ptr(dx), _opt_ptr(dy), _opt_ptr(dgate), _opt_ptr(dpre), _opt_ptr(dpost), _ptr(ws), T, N,
-          alpha, beta, eps, _stream(r))
+          alpha, beta, eps, _raw_stream(d) if _raw_stream is not None else _stream(r))
     return dx, dy, dgate, dpre, dpost
