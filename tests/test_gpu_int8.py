@@ -109,6 +109,22 @@ def test_dispatch(T, k, E, G, H, weighted, dtype):
         assert np.array_equal(host(Q).reshape(-1, H)[finite], wantQ[finite])
 
 
+@pytest.mark.parametrize("weighted", [False, True])
+def test_dispatch_of_many_choices(weighted):
+    """More choices than a wave has lanes."""
+    test_dispatch(5, 70, 80, 80, 272, weighted, "fp32")
+
+
+def test_swiglu_at_the_ends_of_the_range():
+    """Gates so negative that exp overflows give 0, so positive that it vanishes give the gate itself."""
+    g = torch.tensor([-3e38, -1e30, -1e5, -200.0, -104.0, -89.0, -80.0, 40.0, 90.0, 1e5] + [0.0] * 118)
+    h = torch.cat([g, torch.ones(128)])[None].to(dev())
+    h[0, 9] = 1e4
+    Q, s = fg.swiglu_quant_int8(h)
+    assert float(s) == float(np.float32(1e4) / np.float32(127))
+    assert host(Q)[0].tolist() == [0] * 7 + [1, 1, 127] + [0] * 118
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("T,I", [(1, 128), (6, 384), (5, 1024), (4, 1152), (3, 4096), (3, 8192), (2, 18432)])
 def test_swiglu(T, I, dtype):
@@ -300,6 +316,54 @@ def test_operands_past_2_31_bytes():
     assert bool((D[zero] == 0).all())
     q, s = fg.quant_int8(torch.ones(3, 16, device=dev()))   # nothing is left in flight that faults
     assert bool((q == 127).all())
+
+
+def test_columns_up_to_the_limit():
+    """The most columns there may be: 256 rows of D are just below 2^31 bytes, all 257 above."""
+    M, N, K = 257, 4194296, 16
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    A = torch.randint(-128, 128, (M, K), device=dev(), generator=gen).to(torch.int8)
+    B = torch.randint(-128, 128, (N, K), device=dev(), generator=gen).to(torch.int8)
+    sa, sb = torch.rand(M, device=dev(), generator=gen), torch.rand(N, device=dev(), generator=gen)
+    D = fg.gemm_int8_nt(A, sa, B, sb, new_out((M, N)))
+    at = torch.tensor([0, 1, 255, 4096, 2097152, N - 256, N - 9, N - 8, N - 1], device=dev())
+    assert np.array_equal(d_bits(D[:, at].contiguous()), ref_product(host(A), host(sa), host(B[at]), host(sb[at])))
+    one = fg.gemm_int8_nt(A[:1], sa[:1], B, sb, new_out((1, N)))     # the kernel of few rows
+    assert torch.equal(one, D[:1])
+
+
+def test_contiguous_rows_past_the_run_list():
+    """More 128-row blocks than the run-following kernel lists: tiles of at most 128 rows."""
+    G, N, K, M = 3, 24, 32, 2048 * 128 + 384
+    m = torch.arange(M, device=dev()) // 128 % 4 - 1                  # every fourth block is padding
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    A = torch.randint(-128, 128, (M, K), device=dev(), generator=gen).to(torch.int8)
+    B = torch.randint(-128, 128, (G, N, K), device=dev(), generator=gen).to(torch.int8)
+    sa, sb = torch.rand(M, device=dev(), generator=gen), torch.rand(G, N, device=dev(), generator=gen)
+    D = host(fg.grouped_contiguous_int8(A, sa, B, sb, new_out((M, N)), m.to(torch.int32)).view(torch.int16)).view(np.uint16)
+    m = host(m)
+    assert np.all(D[m < 0] == SENTINEL)
+    for g in range(G):
+        assert np.array_equal(D[m == g], ref_product(host(A)[m == g], host(sa)[m == g], host(B)[g], host(sb)[g]))
+
+
+def test_concurrent_streams():
+    """Calls in flight together on several streams give bit for bit what they give one after another."""
+    jobs = []
+    for M, N, K in ((24, 2056, 2064), (300, 1032, 1040), (1001, 520, 528)):
+        a = on_gpu(*operands((M,), 0, N, K, M))
+        jobs.append((lambda D, a=a: fg.gemm_int8_nt(*a, D), (M, N)))
+    want = [run(new_out(shape)) for run, shape in jobs]
+    outs = [[new_out(shape) for _ in range(4)] for _, shape in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for r in range(4):
+        for (run, _), o, stream in zip(jobs, outs, streams):
+            with torch.cuda.stream(stream):
+                run(o[r])
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, D) for D in o)
 
 
 def test_refusals():

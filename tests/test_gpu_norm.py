@@ -178,6 +178,34 @@ def test_in_place():
         assert all(torch.equal(a, b) for a, b in zip(got[2:], vectors))
 
 
+def test_norm_alone_in_place():
+    s = inputs(20, 520, "fp32", False, True, False, "none", 3)
+    want = fg.block_norm(s["x"], pre=s["pre"])[1]
+    x = s["x"].clone()
+    r, h, _ = fg.block_norm(x, pre=s["pre"], h=x)
+    assert r is x and h is x and torch.equal(h, want)
+
+
+def test_rows_past_4_gib():
+    """Byte offsets past 2^32: sampled rows against the same rows alone, the sums over all rows against theirs in
+    blocks (fp32 sums of 300000 terms in another order: (T + 40) u of the terms' absolute sum, normref's bound)."""
+    T, N = 300000, 8192
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    base = torch.randn(1000, N, device=dev(), generator=gen).bfloat16()
+    x = base.repeat(T // 1000, 1)
+    pre = torch.rand(N, device=dev(), generator=gen) + 0.5
+    _, h, s = fg.block_norm(x, pre=pre, quant="e4m3")
+    _, h0, s0 = fg.block_norm(base, pre=pre, quant="e4m3")
+    for t in (0, 1, 131071, 262143, 262144, 299999):
+        assert torch.equal(h[t], h0[t % 1000]) and torch.equal(s[:, t], s0[:, t % 1000]), t
+    del h, s
+    dx, _, _, dpre, _ = fg.block_norm_grad(x, dh=x, pre=pre)
+    dx0, _, _, dpre0, _ = fg.block_norm_grad(base, dh=base, pre=pre)
+    for t in (0, 1, 131071, 262143, 262144, 299999):
+        assert torch.equal(dx[t], dx0[t % 1000]), t
+    assert bool((dpre / (T // 1000) - dpre0).abs().le((T + 1100) * U32 * dpre0).all())    # dh = x: all terms positive
+
+
 def test_infinities_and_nan_stay_in_their_rows():
     s = inputs(30, 520, "fp32", True, True, True, "token", 6)
     how = dict(pre=s["pre"], post=s["post"], gate=s["gate"])
