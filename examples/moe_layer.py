@@ -1,6 +1,8 @@
 """One mixture-of-experts layer on the library's calls: forward in the contiguous layout
 (training, prefill) with the backward of its routing, forward in the masked layout (decode),
-and a shared projection with the low-rank adapters of many requests beside it.
+and a shared projection with the low-rank adapters of many requests beside it. Then the layer
+as a block of a residual stream, its experts in 8-bit integers: the norms before and after it
+with its gate, forward and back.
 
     python examples/moe_layer.py [--tokens 512] [--experts 8] [--hidden 1024] [--inner 512]
 
@@ -80,6 +82,39 @@ def decode(layer, x, k, adapter_ids, M_max):
     return fg.combine(y, plan, w=w, base=shared_with_adapters(layer, x, adapter_ids))
 
 
+def int8_experts(layer, x, ids, w, up, down):
+    """The routed experts in 8-bit integers, contiguous layout; up and down as quant_int8 gives them. (The whole
+    forward is dispatch, product, gated activation, product, combine: one scale per token and output channel.)"""
+    plan = fg.plan_contiguous(ids, layer.experts)
+    A, sa = fg.dispatch_quant_int8(x, plan)
+    h = torch.empty(plan.capacity, up[0].shape[1], dtype=torch.bfloat16, device=x.device)
+    fg.grouped_contiguous_int8(A, sa, *up, h, plan.m_indices)
+    Q, sq = fg.swiglu_quant_int8(h, plan)
+    y = torch.empty(plan.capacity, x.shape[1], dtype=torch.bfloat16, device=x.device)
+    fg.grouped_contiguous_int8(Q, sq, *down, y, plan.m_indices)
+    return fg.combine(y, plan, w=w)
+
+
+def block(layer, stream, k, norms, up, down):
+    """stream -> norm -> experts -> norm, gate, residual: the new stream, the next block's operand in 8-bit
+    integers with its scales, and what the backward needs."""
+    pre, post, gate, following = norms
+    _, x, _ = fg.block_norm(stream, pre=pre)
+    logits = (x.float() @ layer.router.t()).contiguous()
+    ids, w = fg.route_topk(logits, k, bias=layer.balance, **ROUTER)
+    y = int8_experts(layer, x, ids, w, up, down)
+    out, h, s = fg.block_norm(stream, y, pre=following, post=post, gate=gate, quant="int8")
+    return out, h, s, (out, y)
+
+
+def block_backward(saved, dh, dout, norms):
+    """Gradients of the block's tail: the incoming stream's (its direct path), the experts' output's, and those of
+    the gate and the two norms' weights."""
+    out, y = saved
+    _, post, gate, following = norms
+    return fg.block_norm_grad(out, dh=dh, dr=dout, y=y, pre=following, post=post, gate=gate)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--tokens", type=int, default=512)
@@ -102,6 +137,16 @@ def main(argv=None):
           f"logits' rms {float(dlogits.square().mean().sqrt()):.3f}")
     same = decode(layer, x, a.choices, adapter_ids, M_max=a.tokens)
     print(f"masked: largest difference from the contiguous layout {float((same.float() - out.float()).abs().max()):.1e}")
+    new = lambda *s, fan: torch.randn(*s, device="cuda", generator=gen) * fan ** -0.5  # noqa: E731
+    up = fg.quant_int8(new(a.experts, 2 * a.inner, a.hidden, fan=a.hidden))
+    down = fg.quant_int8(new(a.experts, a.hidden, a.inner, fan=a.inner))
+    norms = [torch.ones(a.hidden, device="cuda") for _ in range(2)] + [torch.full((a.hidden,), 0.5, device="cuda"),
+                                                                      torch.ones(a.hidden, device="cuda")]
+    stream, h, s, saved = block(layer, x, a.choices, norms, up, down)
+    dx, dy, dgate, dpre, dpost = block_backward(saved, torch.randn_like(stream), torch.randn_like(stream), norms)
+    print(f"block in 8-bit integers: stream rms {float(stream.float().square().mean().sqrt()):.3f}, operand {tuple(h.shape)} with "
+          f"{s.numel()} scales; backward: experts' output gradient rms {float(dy.float().square().mean().sqrt()):.3f}, "
+          f"gate's {float(dgate.square().mean().sqrt()):.3f}")
     return out, same, dw, dlogits
 
 
