@@ -514,7 +514,7 @@ int fgt_force_runs(int on) {
 const char* fg_strerror(int code) {
   switch (code) {
     case FG_OK: return "success";
-    case FG_EINVAL: return "invalid argument (null pointer, negative size, K not a multiple of 128, N not a multiple of 8 (256 for the fused epilogue), K < 128, misaligned pointer, G < 1, unknown layout or scale kind, an operand of 2^31 bytes or more, N > 4194296; for the row operators: E or G > 1024, k > min(E, 64), rank not a multiple of 8 up to 128, a missing workspace)";
+    case FG_EINVAL: return "invalid argument (null pointer, negative size, K not a multiple of 128, N not a multiple of 8 (256 for the fused epilogue), K < 128, misaligned pointer, G < 1, unknown layout or scale kind, an operand of 2^31 bytes or more, N > 4194296; for the row operators: E or G > 1024, k > min(E, 64), rank not a multiple of 8 up to 128, a missing workspace; for the integer products: K not a multiple of 16 up to 131056, rows to quantise not of 16 up to 65536; for the block norms: N not a multiple of 8 up to 16384, an output or gradient without its input, eps not positive)";
     case FG_EUNSUPPORTED: return "unsupported device (gfx950 required)";
     case FG_ELAUNCH: return "kernel launch failed";
     case FG_EDEVICE: return "HIP device query failed";

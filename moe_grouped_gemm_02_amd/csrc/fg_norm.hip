@@ -441,13 +441,13 @@ __global__ __launch_bounds__(kSumCols * kSumParts) void block_norm_sums(SumArgs 
 int norm_threads(int N) { return N <= 512 ? 64 : N <= 2048 ? 256 : N <= 8192 ? 512 : 1024; }
 int norm_rows(int T, int N, bool y) {
   const int most = kCUs * ((y ? 1024 : 1536) / norm_threads(N));
-  return T <= most ? 1 : (T + most - 1) / most;
+  return T <= most ? 1 : (int)(((long long)T + most - 1) / most);
 }
 int grad_rows(int T, int N) {
   const int most = kCUs * (N <= 2048 ? 512 / norm_threads(N) : 1);
-  return T <= most ? 1 : (T + most - 1) / most;
+  return T <= most ? 1 : (int)(((long long)T + most - 1) / most);
 }
-int grad_groups(int T, int N) { return (T + grad_rows(T, N) - 1) / grad_rows(T, N); }
+int grad_groups(int T, int N) { return (int)(((long long)T + grad_rows(T, N) - 1) / grad_rows(T, N)); }
 
 template <class R>
 bool streams(int T, int N) { return (long long)T * N * R::kBytes > kStreamBytes; }
@@ -455,7 +455,7 @@ bool streams(int T, int N) { return (long long)T * N * R::kBytes > kStreamBytes;
 template <class R, int NTH, int C>
 int launch_norm(NormArgs a, hipStream_t s) {
   a.rows = norm_rows(a.T, a.N, a.y != nullptr);
-  const dim3 g((a.T + a.rows - 1) / a.rows), b(NTH);
+  const dim3 g((unsigned)(((long long)a.T + a.rows - 1) / a.rows)), b(NTH);
   const bool stream = streams<R>(a.T, a.N);
   if (a.y && stream) hipLaunchKernelGGL((block_norm<R, NTH, C, true, true>), g, b, 0, s, a);
   else if (a.y) hipLaunchKernelGGL((block_norm<R, NTH, C, true, false>), g, b, 0, s, a);

@@ -78,6 +78,8 @@ def test_gradient_workspace():
     assert L.fg_block_norm_grad_workspace(1, 8, ctypes.byref(size)) == OK and size.value >= 2 * 8 * 4
     assert L.fg_block_norm_grad_workspace(0, 8, ctypes.byref(size)) == OK
     assert L.fg_block_norm_grad_workspace(8192, 7168, ctypes.byref(size)) == OK and size.value >= 2 * 7168 * 4
+    # the most rows there may be: no more partial sums than there are workgroups
+    assert L.fg_block_norm_grad_workspace(2147483647, 8, ctypes.byref(size)) == OK and 0 < size.value <= 2048 * 2 * 8 * 4
     assert L.fg_block_norm_grad_workspace(4, 12, ctypes.byref(size)) == EINVAL
     assert L.fg_block_norm_grad_workspace(-1, 8, ctypes.byref(size)) == EINVAL
     assert L.fg_block_norm_grad_workspace(4, 8, None) == EINVAL

@@ -203,13 +203,13 @@ def test_dense_on_every_kernel(M, N, K, kernel):
         assert np.array_equal(d_bits(D), want), grid
 
 
-@pytest.mark.parametrize("columns", ["16 columns", "32 columns", "64 columns"])
-@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (16, 72, 2064), (31, 136, 128), (33, 64, 1040), (48, 200, 1024), (61, 128, 7168),
-                                   (96, 264, 4112), (80, 64, 272), (128, 72, 3088), (300, 136, 1168)])
+@pytest.mark.parametrize("M,N,K,columns", [
+    (*size, columns) for columns in ("16 columns", "32 columns", "64 columns")
+    for size in ((1, 8, 16), (16, 72, 2064), (31, 136, 128), (33, 64, 1040), (48, 200, 1024), (61, 128, 7168), (96, 264, 4112),
+                 (80, 64, 272), (128, 72, 3088), (300, 136, 1168))
+    if columns != "64 columns" or size[0] <= 96])                  # that width has kernels of up to 96 rows
 def test_dense_streamed(M, N, K, columns):
     """The weight-streaming kernel at each width, K from less than one piece of one wave to many rounds of all."""
-    if columns == "64 columns" and M > 96:
-        pytest.skip("up to 96 rows")
     print(f"gemm_int8_nt {M}x{N}x{K} streamed, {columns}", flush=True)
     a = operands((M,), 0, N, K, M + N + K)
     with forced_int8(columns):
@@ -364,6 +364,20 @@ def test_concurrent_streams():
     torch.cuda.synchronize()
     for w, o in zip(want, outs):
         assert all(torch.equal(w, D) for D in o)
+
+
+@pytest.mark.parametrize("M", [9, 300])
+def test_scales_of_any_alignment(M):
+    A, sa, B, sb = on_gpu(*operands((M,), 0, 264, 144, 9))
+    odd = lambda v: torch.cat([v.new_zeros(1), v])[1:]  # noqa: E731
+    assert torch.equal(fg.gemm_int8_nt(A, odd(sa), B, odd(sb), new_out((M, 264))), fg.gemm_int8_nt(A, sa, B, sb, new_out((M, 264))))
+    mm = torch.tensor([7, M - 2], dtype=torch.int32, device=dev())[1:]
+    got = fg.grouped_masked_int8(A[None], odd(sa)[None], B[None], odd(sb)[None], new_out((1, M, 264)), mm)
+    want = fg.grouped_masked_int8(A[None], sa[None], B[None], sb[None], new_out((1, M, 264)), mm.clone())
+    assert torch.equal(got, want)
+    shifted = torch.zeros(M * 144 + 1, dtype=torch.int8, device=dev())[1:].view(M, 144)
+    with pytest.raises(fg.FGError):
+        fg.gemm_int8_nt(shifted, sa, B, sb, new_out((M, 264)))
 
 
 def test_refusals():

@@ -120,9 +120,32 @@ def test_tiny_streams_quantise():
         q, s = fg.block_norm(x, pre=pre, quant="int8")[1:]
         rq, rs = fg.quant_int8(want)
         assert torch.equal(q, rq) and torch.equal(s, rs)
-        q, s = fg.block_norm(x, pre=pre, quant="e4m3_pow2")[1:]
-        rq, rs = fg.quant_act_1x128_pow2(want)
-        assert torch.equal(q, rq) and torch.equal(s, rs)
+        for quant, alone in (("e4m3", fg.quant_act_1x128), ("e4m3_pow2", fg.quant_act_1x128_pow2)):
+            q, s = fg.block_norm(x, pre=pre, quant=quant)[1:]
+            rq, rs = alone(want)
+            assert torch.equal(q, rq) and torch.equal(s, rs), quant
+
+
+def test_vectors_of_any_alignment():
+    """Weights, gates and scales start at any float; rows at 16 bytes, or the call is refused."""
+    s = inputs(9, 264, "bf16", True, True, True, "channel", 4)
+    odd = lambda v: torch.cat([v.new_zeros(1), v])[1:]  # noqa: E731
+    how = dict(pre=s["pre"], post=s["post"], gate=s["gate"])
+    shifted = {k: odd(v) for k, v in how.items()}
+    want, got = fg.block_norm(s["x"], s["y"], **how), fg.block_norm(s["x"], s["y"], **shifted)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    rest = dict(dh=s["dh"], dr=s["dr"], y=s["y"])
+    assert all(torch.equal(a, b) for a, b in zip(fg.block_norm_grad(want[0], **rest, **how),
+                                                 fg.block_norm_grad(want[0], **rest, **shifted)))
+    scales = torch.zeros(10, device=dev())[1:]
+    q, got = fg.block_norm(s["x"][:, :256].contiguous(), pre=odd(s["pre"][:256]), quant="int8", s=scales)[1:]
+    want = fg.block_norm(s["x"][:, :256].contiguous(), pre=s["pre"][:256].contiguous(), quant="int8")
+    assert got is scales and torch.equal(got, want[2]) and torch.equal(q, want[1])
+    x = torch.zeros(9 * 264 + 1, dtype=torch.bfloat16, device=dev())[1:].view(9, 264)
+    with pytest.raises(fg.FGError):
+        fg.block_norm(x, pre=s["pre"])
+    with pytest.raises(fg.FGError):
+        fg.block_norm_grad(s["x"], dr=x)
 
 
 @pytest.mark.parametrize("parts", PARTS[:4], ids=lambda p: "-".join(f"{k}={v}" for k, v in p.items()))
