@@ -263,14 +263,32 @@ struct GradArgs {
 };
 
 // LEAN: rows of more than 8192, whose 1024 threads have 128 registers each: the weights are
-// read again for each row (from the L2) and the next row is not fetched ahead.
+// read again for each row (from the L2), the columns' sums are kept in LDS (each thread its
+// own, no barrier), and fp32 rows are not fetched ahead. T 4096, N 16384 bf16 / fp32 245 / 594
+// us with the sums in registers (which spill), 184 / 375 so.
 template <class R, int NTH, int C, bool LEAN, bool STREAM>
 __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
   __shared__ float part3[2][3][NTH / 64], part1[2][1][NTH / 64];
   const int lane = threadIdx.x;
   BlockSum<NTH, 3> sum3{part3};
   BlockSum<NTH, 1> sum1{part1};
-  float cw[LEAN ? 1 : C][8], pre[LEAN ? 1 : C][8], P[C][8], S[C][8];
+  constexpr bool AHEAD = !LEAN || R::kBytes == 2;
+  constexpr int kSums = LEAN ? C * 2 * NTH : 1;   // in pieces of four columns
+  __shared__ f32x4v lds_sums[2][kSums];
+  float cw[LEAN ? 1 : C][8], pre[LEAN ? 1 : C][8], P[LEAN ? 1 : C][8], S[LEAN ? 1 : C][8];
+  // adds v to the sums of the lane's columns: P (which = 0) or S
+  auto add_sums = [&](int which, float (*reg)[8], int c, const float* v) {
+    if constexpr (LEAN) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x4v& at = lds_sums[which][(c * 2 + h) * NTH + lane];
+        at += f32x4v{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) reg[c][e] += v[e];
+    }
+  };
   auto read_pre = [&](int c) { weights8(a.pre, a.N, c * NTH + lane, 0.0f, pre[LEAN ? 0 : c]); };
   auto read_cw = [&](int c) {
     float g[8], *w = cw[LEAN ? 0 : c];
@@ -285,8 +303,14 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
       read_pre(c);
       read_cw(c);
     }
+    if constexpr (LEAN) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) P[c][e] = S[c][e] = 0.0f;
+      for (int h = 0; h < 2; ++h)
+        lds_sums[0][(c * 2 + h) * NTH + lane] = lds_sums[1][(c * 2 + h) * NTH + lane] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) P[c][e] = S[c][e] = 0.0f;
+    }
   }
   const int bytes = a.N * R::kBytes;
   const long t0 = (long)blockIdx.x * a.rows, t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
@@ -306,12 +330,12 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
       if (a.dr) nd[c].load(row_of(a.dr, at, bytes), i);
     }
   };
-  if (!LEAN) fetch(t0);
+  if (AHEAD) fetch(t0);
   for (long t = t0; t < t1; ++t) {
     const long at = t * bytes;
     Unit<R, STREAM> r[C], dh[C], y[C];
     float d[C][8];
-    if (LEAN) fetch(t);
+    if (!AHEAD) fetch(t);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       r[c] = nr[c];
@@ -319,7 +343,7 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
       y[c] = ny[c];
       nd[c].unpack(d[c]);
     }
-    if (!LEAN && t + 1 < t1) fetch(t + 1);
+    if (AHEAD && t + 1 < t1) fetch(t + 1);
     float v[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -346,7 +370,7 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
       const float m = v[1] * rx * a.inv_n;   // mean of z rh
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float f[8], g[8];
+        float f[8], g[8], s[8];
         if (LEAN) read_pre(c);
         r[c].unpack(f);
         dh[c].unpack(g);
@@ -354,8 +378,9 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
         for (int e = 0; e < 8; ++e) {
           const float rh = f[e] * rx;
           d[c][e] = fmaf(rx, fmaf(-rh, m, g[e] * pre[LEAN ? 0 : c][e]), d[c][e]);
-          P[c][e] = fmaf(g[e], rh, P[c][e]);
+          s[e] = g[e] * rh;
         }
+        add_sums(0, P, c, s);
       }
     }
 #pragma unroll
@@ -371,16 +396,17 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
     float q[1] = {0.0f};   // sum of dR yh, times the folded weights
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float f[8];
+      float f[8], s[8];
       if (LEAN) read_cw(c);
       y[c].unpack(f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float yh = f[e] * ry;
-        S[c][e] = fmaf(gt * d[c][e], yh, S[c][e]);
+        s[e] = gt * d[c][e] * yh;
         d[c][e] *= cw[LEAN ? 0 : c][e];
         q[0] = fmaf(d[c][e], yh, q[0]);
       }
+      add_sums(1, S, c, s);
     }
     if (a.post || a.gate_kind == FG_GATE_TOKEN) sum1(q);
     if (a.gate_kind == FG_GATE_TOKEN && lane == 0) a.dgate[t] = q[0];
@@ -395,10 +421,15 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
     }
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    store8<RowF32>(row_of(a.ws, (long)blockIdx.x * 8 * a.N, a.N * 4), c * NTH + lane, P[c]);
-    store8<RowF32>(row_of(a.ws, (long)blockIdx.x * 8 * a.N + 4L * a.N, a.N * 4), c * NTH + lane, S[c]);
-  }
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = LEAN ? lds_sums[which][LEAN ? (c * 2 + e / 4) * NTH + lane : 0][e % 4] : (which ? S : P)[LEAN ? 0 : c][e];
+      store8<RowF32>(row_of(a.ws, ((long)blockIdx.x * 2 + which) * 4 * a.N, a.N * 4), c * NTH + lane, v);
+    }
 }
 
 // The workgroups' sums added up in a fixed order: 16 columns of P or of S a workgroup, 64
