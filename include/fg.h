@@ -381,7 +381,7 @@ int fg_adapters(const void* D, const void* x, const void* A, const void* B, cons
  * 8-bit integer products, an alternative to the E4M3 ones with one fp32 scale per
  * row of A (token) and per row of B (output channel):
  *   D[m, n] = sa[m] * sb[n] * sum_k A[m, k] * B[n, k],
- * the sum in 32-bit integers (exact), then fp32, rounded once to bf16. Layouts,
+ * the sum in 32-bit integers (exact), then (sum * sa) * sb in fp32, rounded once to bf16. Layouts,
  * ownership and row rules as fg_gemm_fp8_nt, fg_grouped_contiguous and
  * fg_grouped_masked, except:
  *   A, B: signed 8-bit integers (any value, -128 too); sa [M] fp32 (masked [G][M_max]), sb [N]
@@ -426,7 +426,7 @@ int fg_swiglu_quant_int8(const void* h, int dtype, const int32_t* slots, void* Q
  *   h = r / sqrt(mean(r^2) + eps) * pre        (pre NULL: no h), of r before its rounding
  * x (the residual stream), y (a block's output), r [T][N], bf16 or fp32 (dtype), 16-byte aligned; pre,
  * post [N] fp32; gate fp32, [N] (FG_GATE_CHANNEL) or [T] (FG_GATE_TOKEN), NULL for FG_GATE_NONE.
- * r may be x or y, and h may be either where it has their type.
+ * r may be x or y, and h may be either where it has their type, but not both the same.
  *   out: FG_OUT_SAME: h [T][N] in x's type, s unused. FG_OUT_E4M3 / FG_OUT_E4M3_POW2: codes
  *   h [T][N] and scales s [N/128][T] as fg_quant_act_1x128(_pow2) makes them (N % 128 == 0; r finite).
  *   FG_OUT_INT8: codes h [T][N] and s [T] as fg_quant_int8 (N % 16 == 0).

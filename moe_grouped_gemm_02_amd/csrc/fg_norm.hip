@@ -539,6 +539,7 @@ int fg_block_norm(const void* x, const void* y, int dtype, const float* pre, con
   // something to do, and what each part needs
   if (!x || (!y && !pre) || (y && !r) || (!y && (post || gate_kind != FG_GATE_NONE))) return FG_EINVAL;
   if ((gate_kind != FG_GATE_NONE) != (gate != nullptr) || (pre && (!h || (out != FG_OUT_SAME && !s)))) return FG_EINVAL;
+  if (y && pre && r == h) return FG_EINVAL;   // two outputs
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(r, 16) || !aligned(h, 16) || !aligned(pre, 4) || !aligned(post, 4) ||
       !aligned(gate, 4) || !aligned(s, 4))
     return FG_EINVAL;
@@ -563,7 +564,7 @@ int fg_block_norm_grad(const void* r, const void* dh, const void* dr, const void
   if (T > 0) {   // without rows only the vectors matter
     if ((dh != nullptr) != (pre != nullptr) || (pre && !r) || (!dh && !dr) || !dx || !ws) return FG_EINVAL;
     if ((y != nullptr) != (dy != nullptr) || (!y && (post || gate_kind != FG_GATE_NONE))) return FG_EINVAL;
-    if ((gate_kind != FG_GATE_NONE) != (gate != nullptr) || (gate && !dgate)) return FG_EINVAL;
+    if ((gate_kind != FG_GATE_NONE) != (gate != nullptr) || (gate && !dgate) || dx == dy) return FG_EINVAL;
   }
   if (!aligned(r, 16) || !aligned(dh, 16) || !aligned(dr, 16) || !aligned(y, 16) || !aligned(dx, 16) || !aligned(dy, 16) ||
       !aligned(pre, 4) || !aligned(post, 4) || !aligned(gate, 4) || !aligned(dgate, 4) || !aligned(dpre, 4) ||

@@ -8,6 +8,7 @@ import moe_grouped_gemm_02_amd as fg
 
 EINVAL, OK = -1, 0
 P = ctypes.c_void_p(0x100000)    # aligned, never dereferenced
+P2 = ctypes.c_void_p(0x200000)
 ODD = ctypes.c_void_p(0x100001)
 
 
@@ -24,9 +25,9 @@ MASKED = dict(A=P, sa=P, B=P, sb=P, D=P, masked_m=P, G=2, M_max=8, N=64, K=128, 
 QUANT = dict(x=P, dtype=0, q=P, s=P, M=4, K=128, stream=None)
 DISPATCH = dict(x=P, dtype=0, rows=P, w=None, Q=P, s=P, T=4, k=2, H=128, n_rows=16, stream=None)
 SWIGLU = dict(h=P, dtype=0, slots=None, Q=P, s=P, rows=4, I=128, stream=None)
-NORM = dict(x=P, y=P, dtype=0, pre=P, post=P, gate=P, gate_kind=1, r=P, h=P, s=P, out=0, T=4, N=128, alpha=1.0, beta=1.0,
+NORM = dict(x=P, y=P, dtype=0, pre=P, post=P, gate=P, gate_kind=1, r=P, h=P2, s=P, out=0, T=4, N=128, alpha=1.0, beta=1.0,
             eps=1e-6, stream=None)
-GRAD = dict(r=P, dh=P, dr=P, y=P, dtype=0, pre=P, post=P, gate=P, gate_kind=1, dx=P, dy=P, dgate=P, dpre=P, dpost=P, ws=P,
+GRAD = dict(r=P, dh=P, dr=P, y=P, dtype=0, pre=P, post=P, gate=P, gate_kind=1, dx=P, dy=P2, dgate=P, dpre=P, dpost=P, ws=P,
             T=4, N=128, alpha=1.0, beta=1.0, eps=1e-6, stream=None)
 SIZES = [dict(N=-8), dict(N=60), dict(N=4194304), dict(K=0), dict(K=8), dict(K=24), dict(K=131072), dict(A=None), dict(A=ODD),
          dict(sa=None), dict(sa=ODD), dict(B=None), dict(B=ODD), dict(sb=None), dict(sb=ODD), dict(D=None), dict(D=ODD)]
@@ -49,13 +50,13 @@ SIZES = [dict(N=-8), dict(N=60), dict(N=4194304), dict(K=0), dict(K=8), dict(K=2
                                  dict(out=1, N=64), dict(out=3, N=72), dict(out=1, s=None), dict(eps=0.0), dict(eps=-1.0),
                                  dict(eps=float("nan")), dict(x=None), dict(x=ODD), dict(y=None), dict(y=ODD), dict(r=None),
                                  dict(r=ODD), dict(h=None), dict(h=ODD), dict(gate=None), dict(gate_kind=0), dict(gate_kind=3),
-                                 dict(pre=ODD), dict(post=ODD), dict(gate=ODD), dict(s=ODD),
+                                 dict(pre=ODD), dict(post=ODD), dict(gate=ODD), dict(s=ODD), dict(h=P),
                                  dict(y=None, post=None, gate=None, gate_kind=0, pre=None)]),
         ("fg_block_norm_grad", GRAD, [dict(T=-1), dict(N=100), dict(N=16392), dict(dtype=3), dict(eps=0.0), dict(r=None),
                                       dict(dh=None), dict(pre=None), dict(y=None), dict(dy=None), dict(dx=None), dict(dpre=None),
                                       dict(dpost=None), dict(dgate=None), dict(gate=None), dict(gate_kind=0), dict(ws=None),
                                       dict(r=ODD), dict(dh=ODD), dict(dr=ODD), dict(y=ODD), dict(dx=ODD), dict(dy=ODD),
-                                      dict(ws=ODD), dict(dpre=ODD), dict(dh=None, pre=None, dr=None)]),
+                                      dict(ws=ODD), dict(dpre=ODD), dict(dh=None, pre=None, dr=None), dict(dy=P)]),
     ] for c in cs], ids=lambda v: v if isinstance(v, str) else ",".join(v) if isinstance(v, dict) and len(v) < 4 else "")
 def test_bad_arguments_are_refused(name, good, changes):
     assert call(name, good, **changes) == EINVAL
