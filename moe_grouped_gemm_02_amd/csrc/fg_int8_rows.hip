@@ -44,10 +44,11 @@ __device__ __forceinline__ float row_amax(uint32_t m, uint32_t* part) {
 
 // x / (1 + exp(-x)) to about 3 ulp. exp(-x) = 2^h 2^l with h the rounded product -x log2 e
 // and l what it misses (the hardware's 2^h alone is off by |x| 2^-24); the reciprocal is
-// the hardware's. Below x = -87.3 (h >= 126) silu is under 1e-36 and taken as 0.
+// the hardware's. Below x = -87.3 (h >= 126) silu is under 1e-36 and taken as 0; from 88 on
+// 1 + exp(-x) is 1, and h and l stay finite.
 __device__ __forceinline__ float silu(float x) {
   constexpr float kLog2e = 1.44269502f, kLow = 1.92596299e-8f, kLn2 = 0.693147182f;
-  const float h = -x * kLog2e, l = fmaf(-x, kLow, fmaf(-x, kLog2e, -h));
+  const float z = -fminf(x, 88.0f), h = z * kLog2e, l = fmaf(z, kLow, fmaf(z, kLog2e, -h));
   const float e = __builtin_amdgcn_exp2f(h);
   const float s = __builtin_amdgcn_rcpf(1.0f + fmaf(e, l * kLn2, e));
   return x * (h < 126.0f ? s : 0.0f);

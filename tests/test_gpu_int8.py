@@ -126,6 +126,20 @@ def test_swiglu_at_the_ends_of_the_range():
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_swiglu_of_gates_near_the_largest_float(dtype):
+    """Their silu is the gate itself, an infinite one's infinity: the scale shows it."""
+    g = torch.zeros(3, 128)
+    g[0, :3] = torch.tensor([2.0 ** 127, 1.5 * 2.0 ** 127, -3e38])
+    g[1, 0] = float("inf")
+    g[2, 0] = float("nan")
+    up = torch.full((3, 128), 0.5)
+    Q, s = fg.swiglu_quant_int8(torch.cat([g, up], 1).to(dev(), torch.bfloat16 if dtype == "bf16" else torch.float32))
+    assert float(s[0]) == float(np.float32(1.5 * 2.0 ** 126) / np.float32(127))
+    assert host(Q)[0].tolist() == [85, 127] + [0] * 126    # 127 * 2 / 3 = 84.67
+    assert float(s[1]) == float("inf") and bool(s[2].isnan())
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("T,I", [(1, 128), (6, 384), (5, 1024), (4, 1152), (3, 4096), (3, 8192), (2, 18432)])
 def test_swiglu(T, I, dtype):
     print(f"swiglu_quant_int8 {T}x{I} {dtype}", flush=True)
