@@ -387,7 +387,8 @@ int fg_adapters(const void* D, const void* x, const void* A, const void* B, cons
  *   A, B: signed 8-bit integers (any value, -128 too); sa [M] fp32 (masked [G][M_max]), sb [N]
  *   (grouped [G][N]).
  *   K is a multiple of 16 up to 131056, N a multiple of 8 up to 4194296. M * K and
- *   N * K have no limit of their own.
+ *   N * K have no limit of their own; D has fewer than 2^23 tiles of 256 x 256 (masked: of all
+ *   experts; contiguous: of 128 x 256).
  * Results are bitwise reproducible and do not depend on the tile or the layout.
  */
 int fg_gemm_int8_nt(const void* A, const float* sa, const void* B, const float* sb, void* D, int M, int N, int K,

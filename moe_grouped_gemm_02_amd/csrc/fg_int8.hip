@@ -24,6 +24,10 @@ constexpr int kWide = 0, kNarrow = 1, kHalf = 2;
 constexpr int kMaxK = 131056;     // 128^2 K < 2^31: the 32-bit sum is exact
 constexpr int kMaxN = 4194296;    // 256 rows of N bf16 stay below 2^31 bytes
 
+// A grid has fewer than 2^32 threads (past that the runtime drops workgroups without a word),
+// a tile at most 512.
+constexpr long kMaxTiles = (1L << 23) - 1;
+
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
 // Estimated cycles of one tile over kblocks K-blocks: its matrix-core time at 8192
@@ -65,7 +69,7 @@ Choice skinny(int layout, int M, int N, int G, int force = -1) {
   if (steps > 4) steps = steps <= 6 ? 6 : 8;
   c.tile = kSkinny + 3 * (steps - 1) + i;
   c.grid = ceil_div(M, 16 * steps) * ceil_div(N, 16 << i) * G;
-  return c;
+  return c.grid <= kMaxTiles ? c : Choice();
 }
 
 // The shape whose tiles, in rounds over the compute units, take the fewest estimated
@@ -81,6 +85,7 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
     const Tile& t = kTiles[i];
     if (layout == FG_LAYOUT_CONTIGUOUS && t.bm > 128) continue;   // a tile's rows are one expert's
     const long tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn) * (layout == FG_LAYOUT_MASKED ? G : 1);
+    if (tiles > kMaxTiles) continue;
     const double c = (double)ceil_div(tiles, cus) * tile_cycles(t, kb);
     if (best.tile < 0 || c < cost) {
       best.tile = i;
@@ -150,14 +155,15 @@ int run(int layout, const void* A, const float* sa, const void* B, const float* 
   if (!A || !sa || !B || !sb || !D || (layout != FG_LAYOUT_DENSE && !index)) return FG_EINVAL;
   if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(index, 4))
     return FG_EINVAL;
-  // the smallest tiles' number, a bound of every choice's
-  if ((layout == FG_LAYOUT_MASKED ? G : 1) * ceil_div(M, 64) * ceil_div(N, 16) > 0x7fffffffL) return FG_EINVAL;
+  // the largest tiles, of which choose() always has one
+  const Tile& top = kTiles[layout == FG_LAYOUT_CONTIGUOUS ? kHalf : kWide];
+  if ((layout == FG_LAYOUT_MASKED ? G : 1) * ceil_div(M, top.bm) * ceil_div(N, top.bn) > kMaxTiles) return FG_EINVAL;
   int cus = 0;
   const int st = current_device(&cus);
   if (st != FG_OK) return st;
   Choice c = choose(layout, M, N, K, G, cus);
 #ifdef FG_TESTING
-  if (t_tile >= 0 && !forced(layout, M, N, G, cus, c)) return FG_EINVAL;
+  if (t_tile >= 0 && (!forced(layout, M, N, G, cus, c) || c.grid > kMaxTiles)) return FG_EINVAL;
 #endif
   const Tile& t = kTiles[c.tile < kNumTiles ? c.tile : kWide];
   Params p = {};

@@ -63,6 +63,7 @@ struct RowArgs {
   uint8_t* q;
   float* s;
   int T, k, H, n_rows;
+  long row0;   // of this launch
 };
 
 template <class R>
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void quant_int8(RowArgs a) {
   __shared__ uint32_t part[NTH / 64];
   constexpr int kPerGroup = NTH == 64 ? 4 : 1;   // rows of a workgroup
   const int lane = NTH == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const long row = (long)blockIdx.x * kPerGroup + (NTH == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
+  const long row = a.row0 + (long)blockIdx.x * kPerGroup + (NTH == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
   if (row >= a.T) return;
   if (MODE == kSwiglu && a.index && a.index[row] < 0) return;   // uniform over the row's threads
   const int per = a.H >> 4;
@@ -156,11 +157,20 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void quant_int8(RowArgs a) {
   }
 }
 
+// A grid has fewer than 2^32 threads (past that the runtime drops workgroups without a word):
+// more rows take more launches.
 template <class R, int MODE, int NTH, int C>
-int launch_one(const RowArgs& a, hipStream_t s) {
-  const long groups = NTH == 64 ? (a.T + 3L) / 4 : a.T;
-  hipLaunchKernelGGL((quant_int8<R, MODE, NTH, C>), dim3((unsigned)groups), dim3(NTH == 64 ? 256 : NTH), 0, s, a);
-  return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
+int launch_one(RowArgs a, hipStream_t s) {
+  constexpr int kThreads = NTH == 64 ? 256 : NTH, kRows = NTH == 64 ? 4 : 1;
+  constexpr long kMost = (1L << 31) / kThreads;
+  const long groups = (a.T + kRows - 1L) / kRows;
+  for (long g = 0; g < groups; g += kMost) {
+    a.row0 = g * kRows;
+    const long n = groups - g < kMost ? groups - g : kMost;
+    hipLaunchKernelGGL((quant_int8<R, MODE, NTH, C>), dim3((unsigned)n), dim3(kThreads), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return FG_ELAUNCH;
+  }
+  return FG_OK;
 }
 
 template <class R, int MODE>
@@ -193,7 +203,7 @@ extern "C" {
 int fg_quant_int8(const void* x, int dtype, void* q, float* s, int M, int K, hipStream_t stream) {
   const int rc = check(dtype, M, K);
   if (rc != FG_OK || M == 0) return rc;
-  return run<kRows>(dtype, RowArgs{x, nullptr, nullptr, static_cast<uint8_t*>(q), s, M, 1, K, M}, stream);
+  return run<kRows>(dtype, RowArgs{x, nullptr, nullptr, static_cast<uint8_t*>(q), s, M, 1, K, M, 0}, stream);
 }
 
 int fg_dispatch_quant_int8(const void* x, int dtype, const int32_t* rows, const float* w, void* Q, float* s, int T,
@@ -202,7 +212,7 @@ int fg_dispatch_quant_int8(const void* x, int dtype, const int32_t* rows, const 
   if (rc != FG_OK || k < 1 || n_rows < 0) return FG_EINVAL;
   if (T == 0 || n_rows == 0) return FG_OK;
   if (!rows || !aligned(rows, 4) || !aligned(w, 4)) return FG_EINVAL;
-  return run<kDispatch>(dtype, RowArgs{x, rows, w, static_cast<uint8_t*>(Q), s, T, k, H, n_rows}, stream);
+  return run<kDispatch>(dtype, RowArgs{x, rows, w, static_cast<uint8_t*>(Q), s, T, k, H, n_rows, 0}, stream);
 }
 
 int fg_swiglu_quant_int8(const void* h, int dtype, const int32_t* slots, void* Q, float* s, int rows, int I,
@@ -211,7 +221,7 @@ int fg_swiglu_quant_int8(const void* h, int dtype, const int32_t* slots, void* Q
   if (rc != FG_OK || I % 128) return FG_EINVAL;
   if (rows == 0) return FG_OK;
   if (!aligned(slots, 4)) return FG_EINVAL;
-  return run<kSwiglu>(dtype, RowArgs{h, slots, nullptr, static_cast<uint8_t*>(Q), s, rows, 1, I, rows}, stream);
+  return run<kSwiglu>(dtype, RowArgs{h, slots, nullptr, static_cast<uint8_t*>(Q), s, rows, 1, I, rows, 0}, stream);
 }
 
 }  // extern "C"

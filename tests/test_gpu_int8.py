@@ -361,6 +361,32 @@ def test_contiguous_rows_past_the_run_list():
         assert np.array_equal(D[m == g], ref_product(host(A)[m == g], host(sa)[m == g], host(B)[g], host(sb)[g]))
 
 
+def test_rows_past_a_launch():
+    """More rows than one grid's threads can be (2^32, 64 a row): the last ones too."""
+    T, K = (1 << 26) + 5, 16
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device=dev())
+    x[-40:] = torch.randn(40, K, device=dev())
+    q, s = fg.quant_int8(x)
+    want, ws = fg.quant_int8(x[-40:].clone())
+    assert torch.equal(q[-40:], want) and torch.equal(s[-40:], ws)
+    assert int(q[:-40].count_nonzero()) == 0 and bool((s[:-40] == 1).all())
+
+
+def test_experts_past_a_launch():
+    """As many experts' tiles of 16 x 64, a few rows' choice, have more threads than a grid."""
+    G, N, K = 6000000, 136, 16
+    A = torch.ones(G, 1, K, dtype=torch.int8, device=dev())
+    B = torch.zeros(G, N, K, dtype=torch.int8, device=dev())
+    at = torch.tensor([0, 1, G // 2, G - 2, G - 1], device=dev())
+    B[at] = torch.randint(-128, 128, (5, N, K), device=dev()).to(torch.int8)
+    one = torch.ones(G, N, device=dev())
+    D = torch.full((G, 1, N), 3.0, dtype=torch.bfloat16, device=dev())
+    fg.grouped_masked_int8(A, one[:, :1].contiguous(), B, one, D, torch.ones(G, dtype=torch.int32, device=dev()))
+    assert torch.equal(D[at, 0], B[at].int().sum(2).bfloat16())
+    D[at] = 0.0
+    assert int(D.count_nonzero()) == 0
+
+
 def test_concurrent_streams():
     """Calls in flight together on several streams give bit for bit what they give one after another."""
     jobs = []
