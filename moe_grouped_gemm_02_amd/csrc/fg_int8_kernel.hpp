@@ -535,9 +535,10 @@ __global__ __launch_bounds__(64 * T::WAVES) void int8_skinny(Params p) {
   auto load = [&](uint32_t slot, int x) {
     const uint32_t k = (uint32_t)(x * W + wave) * 128u;
     const uint32_t off = row_off | (k + chunk16 < (uint32_t)K ? 0u : kNoRow), step = 8u * (uint32_t)K;
-    static_for<2 * TM>([&](auto q) { dma16<decltype(q)::value * 1024>(rsA, off + decltype(q)::value * step, k, ring + slot); });
+    const uint32_t at = min(k, (uint32_t)K);   // within the buffer, of at least one row
+    static_for<2 * TM>([&](auto q) { dma16<decltype(q)::value * 1024>(rsA, off + decltype(q)::value * step, at, ring + slot); });
     static_for<2 * TN>([&](auto q) {
-      dma16<(2 * TM + decltype(q)::value) * 1024>(rsB, off + decltype(q)::value * step, k, ring + slot);
+      dma16<(2 * TM + decltype(q)::value) * 1024>(rsB, off + decltype(q)::value * step, at, ring + slot);
     });
   };
   i32x4 acc[TM][TN];
