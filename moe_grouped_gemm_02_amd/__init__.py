@@ -972,6 +972,8 @@ def block_norm(x, y=None, pre=None, post=None, gate=None, alpha=1.0, beta=1.0, e
     out = NORM_OUTPUTS[quant]
     if pre is None and quant is not None:
         raise ValueError("quant is for h, which needs pre")
+    if (h is not None and pre is None) or (s is not None and out == 0):
+        raise ValueError("h is written where there is pre, s where there is quant")
     if y is not None:
         r = _new_like(r, "r", x)
     elif r is not None and r is not x:

@@ -316,3 +316,11 @@ def test_refusals():
                       (ValueError, lambda: fg.block_norm_grad(x, dr=x, post=w)), (TypeError, lambda: fg.block_norm_grad(x, dr=x.bfloat16()))]:
         with pytest.raises(err):
             call()
+
+
+def test_outputs_that_would_not_be_written_are_refused():
+    x, w = torch.ones(4, 128, device=dev()), torch.ones(128, device=dev())
+    s = torch.ones(4, device=dev())
+    for call in [lambda: fg.block_norm(x, x, h=x.clone()), lambda: fg.block_norm(x, pre=w, s=s), lambda: fg.block_norm(x, x, s=s)]:
+        with pytest.raises(ValueError):
+            call()
