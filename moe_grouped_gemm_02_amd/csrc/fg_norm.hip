@@ -22,7 +22,7 @@
 // way while this one goes through its barriers. Measured, T 8192, N 7168, bf16: forward to
 // E4M3 84-86 us (4.9 TB/s; a row a workgroup at a time 108), in bf16 92, without y 40;
 // gradient 140 + 6.5 us (4.8 TB/s; without the row ahead, rows as floats 200 + 27). T 32
-// forward 4.2 us, latency. T 1001, N 2048, fp32, gradient 13 + 5.5.
+// forward 4.2 us, latency. T 1001, N 2048, fp32, gradient 12.8 + 3.9.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -474,9 +474,16 @@ int norm_rows(int T, int N, bool y) {
   const int most = kCUs * ((y ? 1024 : 1536) / norm_threads(N));
   return T <= most ? 1 : (int)(((long long)T + most - 1) / most);
 }
+// The gradient's workgroups each write their sums and the second kernel reads them, 16 bytes a
+// column against a row's 10 (bf16) to 20: batches of some size take two or four rows a workgroup
+// at least. us, rows 1 or as the most workgroups give / 2 / 4, bf16: 200 x 2048 8.8 / 8.2 / 9.0,
+// 200 x 7168 20.2 / 16.5 / 16.7, 512 x 1024 9.9 / 9.1 / 10.3, 512 x 64 6.0 / 7.0 / 8.2, 1001 x 2048
+// 18.4 / 18.3 / 14.3, 2048 x 512 17.3 / 12.6 / 11.3, 2048 x 256 12.3 / 9.5 / 9.9.
 int grad_rows(int T, int N) {
   const int most = kCUs * (N <= 2048 ? 512 / norm_threads(N) : 1);
-  return T <= most ? 1 : (int)(((long long)T + most - 1) / most);
+  const int rows = T <= most ? 1 : (int)(((long long)T + most - 1) / most);
+  const int least = T >= 640 && N > 256 ? 4 : T >= (N > 512 ? 192 : 1024) ? 2 : 1;
+  return rows > least ? rows : least;
 }
 int grad_groups(int T, int N) { return (int)(((long long)T + grad_rows(T, N) - 1) / grad_rows(T, N)); }
 
