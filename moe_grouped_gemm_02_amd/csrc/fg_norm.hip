@@ -38,6 +38,7 @@ using namespace fg;
 constexpr int kMaxCols = 16384;   // 1024 threads of 2 units
 constexpr int kCUs = 256;
 constexpr int kNontemporal = 2;   // of a buffer access
+constexpr int kNoUnit = 1 << 24;  // of a row: past its end
 
 struct NormArgs {
   const void *x, *y;
@@ -92,15 +93,33 @@ __device__ __forceinline__ void weights8(const float* w, int n, int i, float oth
   }
 }
 
-// Sums over the workgroup, the same in every thread, in a fixed order. The slots of two
-// calls in a row differ, so one barrier a call is enough.
-template <int NTH, int V>
+// Short rows: a wave has 64 / L of them side by side, L lanes each (16 for up to 128 columns, 32
+// for up to 256), and its sums and largest values are those of L lanes. T 65536, N 128, bf16, 1 / 4
+// rows a wave: 13.2 / 6.9 us, with y 22.1 / 11.7, N 256, 1 / 2 rows 13.9 / 11.5, with y 28.7 / 25.3.
+template <int L>
+__device__ __forceinline__ float row_sum(float v) {
+  if constexpr (L == 64) return wave_sum(v);
+  v = group_sum<16>(v);
+  if constexpr (L == 32) v += __shfl_xor(v, 16);
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t m) {
+  if constexpr (L == 64) return group_max_u32<64>(m);
+  m = group_max_u32<16>(m);
+  if constexpr (L == 32) m = umax(m, (uint32_t)__shfl_xor((int)m, 16));
+  return m;
+}
+
+// Sums over the workgroup (or over a short row's L lanes), the same in every thread, in a fixed
+// order. The slots of two calls in a row differ, so one barrier a call is enough.
+template <int NTH, int V, int L = 64>
 struct BlockSum {
   float (*part)[V][NTH / 64];
   int slot = 0;
   __device__ __forceinline__ void operator()(float* v) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = wave_sum(v[i]);
+    for (int i = 0; i < V; ++i) v[i] = row_sum<L>(v[i]);
     if constexpr (NTH > 64) {
       const int wave = threadIdx.x >> 6;
       if ((threadIdx.x & 63) == 0) {
@@ -122,12 +141,16 @@ struct BlockSum {
 __device__ __forceinline__ float rstd_of(float sum, float inv_n, float eps) { return 1.0f / sqrtf(fmaf(sum, inv_n, eps)); }
 
 // Y: with a block's output.
-template <class R, int NTH, int C, bool Y, bool STREAM>
+template <class R, int NTH, int C, int L, bool Y, bool STREAM>
 __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
+  static_assert(L == 64 || (NTH == 64 && C == 1), "short rows: a wave a workgroup");
+  constexpr int kRows = 64 / L;   // a step's rows
   __shared__ float part[2][1][NTH / 64];
   __shared__ uint32_t top[2][NTH / 64];
-  const int lane = threadIdx.x, per = a.N >> 3;
-  BlockSum<NTH, 1> sum{part};
+  const int lane = L < 64 ? threadIdx.x % L : threadIdx.x, below = L < 64 ? threadIdx.x / L : 0, per = a.N >> 3;
+  BlockSum<NTH, 1, L> sum{part};
+  // the lane's unit c of a step's rows, which follow one another in memory
+  auto unit = [&](int c) { return L == 64 ? c * NTH + lane : lane < per ? below * per + lane : kNoUnit; };
   float cw[C][8], pre[C][8];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
@@ -142,32 +165,34 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
     }
   }
   int flip = 0;
+  auto rows_at = [&](const void* base, long t, int bytes) {   // one step's rows
+    return row_of(base, t * bytes, L == 64 ? bytes : (int)(a.T - t < kRows ? a.T - t : kRows) * bytes);
+  };
   const int bytes = a.N * R::kBytes;
   const long t0 = (long)blockIdx.x * a.rows, t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
   Unit<R, STREAM> nx[C], ny[C];   // the next row, on its way
   auto fetch = [&](long t) {
-    const long at = t * a.N * R::kBytes;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      nx[c].load(row_of(a.x, at, bytes), c * NTH + lane);
-      if (Y) ny[c].load(row_of(a.y, at, bytes), c * NTH + lane);
+      nx[c].load(rows_at(a.x, t, bytes), unit(c));
+      if (Y) ny[c].load(rows_at(a.y, t, bytes), unit(c));
     }
   };
   fetch(t0);
-  for (long t = t0; t < t1; ++t) {
-    const long at = t * a.N;
+  for (long t = t0; t < t1; t += kRows) {
+    const long mine = t + below;   // the lane's row
     Unit<R, STREAM> x[C], y[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       x[c] = nx[c];
       y[c] = ny[c];
     }
-    if (t + 1 < t1) fetch(t + 1);
+    if (t + kRows < t1) fetch(t + kRows);
     float r[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) x[c].unpack(r[c]);
     if (Y) {
-      float k = a.gate_kind == FG_GATE_TOKEN ? a.gate[t] : 1.0f;
+      float k = a.gate_kind == FG_GATE_TOKEN && mine < a.T ? a.gate[mine] : 1.0f;
       if (a.post) {
         float v[1] = {0.0f};
 #pragma unroll
@@ -186,7 +211,7 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
         y[c].unpack(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[c][e] = fmaf(f[e] * k, cw[c][e], a.alpha * r[c][e]);
-        store8<R, STREAM>(row_of(a.r, at * R::kBytes, bytes), c * NTH + lane, r[c]);
+        store8<R, STREAM>(rows_at(a.r, t, bytes), unit(c), r[c]);
       }
     }
     if (!a.pre) continue;
@@ -201,15 +226,15 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int e = 0; e < 8; ++e) r[c][e] = r[c][e] * rx * pre[c][e];
-    const __amdgpu_buffer_rsrc_t codes = row_of(a.h, at, a.N);   // 8-bit outputs
+    const __amdgpu_buffer_rsrc_t codes = rows_at(a.h, t, a.N);   // 8-bit outputs
     if (a.out == FG_OUT_SAME) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) store8<R, STREAM>(row_of(a.h, at * R::kBytes, bytes), c * NTH + lane, r[c]);
+      for (int c = 0; c < C; ++c) store8<R, STREAM>(rows_at(a.h, t, bytes), unit(c), r[c]);
     } else if (a.out == FG_OUT_INT8) {
       uint32_t m = 0;
 #pragma unroll
       for (int c = 0; c < C; ++c) m = amax_bits<8>(r[c], m);
-      m = group_max_u32<64>(m);
+      m = row_max<L>(m);
       if constexpr (NTH > 64) {
         if ((lane & 63) == 0) top[flip][lane >> 6] = m;
         __syncthreads();
@@ -218,13 +243,12 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
         flip ^= 1;
       }
       const float s = int8_scale(__uint_as_float(m)), inv = 1.0f / s;
-      if (lane == 0) a.s[t] = s;
+      if (lane == 0 && mine < a.T) a.s[mine] = s;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int i = c * NTH + lane;
         uint32_t q[2];
         int8_encode<8>(r[c], s, inv, q);
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2v{q[0], q[1]}, codes, i * 8, 0, STREAM ? kNontemporal : 0);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2v{q[0], q[1]}, codes, unit(c) * 8, 0, STREAM ? kNontemporal : 0);
       }
     } else {
       // 16 lanes have a 1x128 block; a group is wholly inside the row or past it
@@ -245,8 +269,8 @@ __global__ __launch_bounds__(NTH) void block_norm(NormArgs a) {
           q[0] = e4m3x4_div(r[c][0], r[c][1], r[c][2], r[c][3], s);
           q[1] = e4m3x4_div(r[c][4], r[c][5], r[c][6], r[c][7], s);
         }
-        __builtin_amdgcn_raw_buffer_store_b64(q, codes, i * 8, 0, STREAM ? kNontemporal : 0);
-        if (i < per && (lane & 15) == 0) a.s[(long)(i >> 4) * a.T + t] = s;
+        __builtin_amdgcn_raw_buffer_store_b64(q, codes, unit(c) * 8, 0, STREAM ? kNontemporal : 0);
+        if (i < per && mine < a.T && (lane & 15) == 0) a.s[(long)(i >> 4) * a.T + mine] = s;
       }
     }
   }
@@ -266,12 +290,15 @@ struct GradArgs {
 // read again for each row (from the L2), the columns' sums are kept in LDS (each thread its
 // own, no barrier), and fp32 rows are not fetched ahead. T 4096, N 16384 bf16 / fp32 245 / 594
 // us with the sums in registers (which spill), 184 / 375 so.
-template <class R, int NTH, int C, bool LEAN, bool STREAM>
+template <class R, int NTH, int C, int L, bool LEAN, bool STREAM>
 __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
+  static_assert(L == 64 || (NTH == 64 && C == 1 && !LEAN), "short rows: a wave a workgroup");
+  constexpr int kRows = 64 / L;   // a step's rows
   __shared__ float part3[2][3][NTH / 64], part1[2][1][NTH / 64];
-  const int lane = threadIdx.x;
-  BlockSum<NTH, 3> sum3{part3};
-  BlockSum<NTH, 1> sum1{part1};
+  const int lane = L < 64 ? threadIdx.x % L : threadIdx.x, below = L < 64 ? threadIdx.x / L : 0, per = a.N >> 3;
+  BlockSum<NTH, 3, L> sum3{part3};
+  BlockSum<NTH, 1, L> sum1{part1};
+  auto unit = [&](int c) { return L == 64 ? c * NTH + lane : lane < per ? below * per + lane : kNoUnit; };
   constexpr bool AHEAD = !LEAN || R::kBytes == 2;
   constexpr int kSums = LEAN ? C * 2 * NTH : 1;   // in pieces of four columns
   __shared__ f32x4v lds_sums[2][kSums];
@@ -313,26 +340,28 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
     }
   }
   const int bytes = a.N * R::kBytes;
+  auto rows_at = [&](const void* base, long t) {   // one step's rows
+    return row_of(base, t * bytes, L == 64 ? bytes : (int)(a.T - t < kRows ? a.T - t : kRows) * bytes);
+  };
   const long t0 = (long)blockIdx.x * a.rows, t1 = t0 + a.rows < a.T ? t0 + a.rows : a.T;
   Unit<R, STREAM> nr[C], nh[C], nd[C], ny[C];   // the next row, on its way
 #pragma unroll
   for (int c = 0; c < C; ++c) nd[c].zero();
   auto fetch = [&](long t) {
-    const long at = t * a.N * R::kBytes;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int i = c * NTH + lane;
+      const int i = unit(c);
       if (a.pre) {
-        nr[c].load(row_of(a.r, at, bytes), i);
-        nh[c].load(row_of(a.dh, at, bytes), i);
+        nr[c].load(rows_at(a.r, t), i);
+        nh[c].load(rows_at(a.dh, t), i);
       }
-      if (a.y) ny[c].load(row_of(a.y, at, bytes), i);
-      if (a.dr) nd[c].load(row_of(a.dr, at, bytes), i);
+      if (a.y) ny[c].load(rows_at(a.y, t), i);
+      if (a.dr) nd[c].load(rows_at(a.dr, t), i);
     }
   };
   if (AHEAD) fetch(t0);
-  for (long t = t0; t < t1; ++t) {
-    const long at = t * bytes;
+  for (long t = t0; t < t1; t += kRows) {
+    const long mine = t + below;   // the lane's row
     Unit<R, STREAM> r[C], dh[C], y[C];
     float d[C][8];
     if (!AHEAD) fetch(t);
@@ -343,7 +372,7 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
       y[c] = ny[c];
       nd[c].unpack(d[c]);
     }
-    if (AHEAD && t + 1 < t1) fetch(t + 1);
+    if (AHEAD && t + kRows < t1) fetch(t + kRows);
     float v[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -388,11 +417,11 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
       float o[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = a.alpha * d[c][e];
-      store8<R, STREAM>(row_of(a.dx, at, bytes), c * NTH + lane, o);
+      store8<R, STREAM>(rows_at(a.dx, t), unit(c), o);
     }
     if (!a.y) continue;
     const float ry = a.post ? rstd_of(v[2], a.inv_n, a.eps) : 1.0f;
-    const float gt = a.gate_kind == FG_GATE_TOKEN ? a.gate[t] : 1.0f;
+    const float gt = a.gate_kind == FG_GATE_TOKEN && mine < a.T ? a.gate[mine] : 1.0f;
     float q[1] = {0.0f};   // sum of dR yh, times the folded weights
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -409,7 +438,7 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
       add_sums(1, S, c, s);
     }
     if (a.post || a.gate_kind == FG_GATE_TOKEN) sum1(q);
-    if (a.gate_kind == FG_GATE_TOKEN && lane == 0) a.dgate[t] = q[0];
+    if (a.gate_kind == FG_GATE_TOKEN && lane == 0 && mine < a.T) a.dgate[mine] = q[0];
     const float m = a.post ? q[0] * a.inv_n : 0.0f, k = ry * gt;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -417,7 +446,7 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
       y[c].unpack(f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = k * fmaf(-f[e] * ry, m, d[c][e]);
-      store8<R, STREAM>(row_of(a.dy, at, bytes), c * NTH + lane, o);
+      store8<R, STREAM>(rows_at(a.dy, t), unit(c), o);
     }
   }
 #pragma unroll
@@ -428,6 +457,10 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         v[e] = LEAN ? lds_sums[which][LEAN ? (c * 2 + e / 4) * NTH + lane : 0][e % 4] : (which ? S : P)[LEAN ? 0 : c][e];
+#pragma unroll
+      for (int d = L; d < 64; d *= 2)   // the rows that were side by side; their lanes then store the same
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += __shfl_xor(v[e], d);
       store8<RowF32>(row_of(a.ws, ((long)blockIdx.x * 2 + which) * 4 * a.N, a.N * 4), c * NTH + lane, v);
     }
 }
@@ -470,9 +503,11 @@ __global__ __launch_bounds__(kSumCols * kSumParts) void block_norm_sums(SumArgs 
 // many workgroups as are resident together, so each has a run of neighbouring rows (whose
 // E4M3 scales are neighbours in memory and meet in one XCD's L2).
 int norm_threads(int N) { return N <= 512 ? 64 : N <= 2048 ? 256 : N <= 8192 ? 512 : 1024; }
+int step_rows(int N) { return N <= 128 ? 4 : N <= 256 ? 2 : 1; }   // 64 / L
 int norm_rows(int T, int N, bool y) {
-  const int most = kCUs * ((y ? 1024 : 1536) / norm_threads(N));
-  return T <= most ? 1 : (int)(((long long)T + most - 1) / most);
+  const int most = kCUs * ((y ? 1024 : 1536) / norm_threads(N)), n = step_rows(N);
+  const long long steps = ((long long)T + n - 1) / n;
+  return n * (int)((steps + most - 1) / most);
 }
 // The gradient's workgroups each write their sums and the second kernel reads them, 16 bytes a
 // column against a row's 10 (bf16) to 20: batches of some size take two or four rows a workgroup
@@ -481,28 +516,32 @@ int norm_rows(int T, int N, bool y) {
 // 18.4 / 18.3 / 14.3, 2048 x 512 17.3 / 12.6 / 11.3, 2048 x 256 12.3 / 9.5 / 9.9.
 int grad_rows(int T, int N) {
   const int most = kCUs * (N <= 2048 ? 512 / norm_threads(N) : 1);
-  const int rows = T <= most ? 1 : (int)(((long long)T + most - 1) / most);
-  const int least = T >= 640 && N > 256 ? 4 : T >= (N > 512 ? 192 : 1024) ? 2 : 1;
-  return rows > least ? rows : least;
+  const int n = step_rows(N);
+  const long long steps = ((long long)T + n - 1) / n;
+  const int each = (int)((steps + most - 1) / most);
+  const int least = steps >= 640 && N > 256 ? 4 : steps >= (N > 512 ? 192 : 1024) ? 2 : 1;
+  return n * (each > least ? each : least);
 }
 int grad_groups(int T, int N) { return (int)(((long long)T + grad_rows(T, N) - 1) / grad_rows(T, N)); }
 
 template <class R>
 bool streams(int T, int N) { return (long long)T * N * R::kBytes > kStreamBytes; }
 
-template <class R, int NTH, int C>
+template <class R, int NTH, int C, int L = 64>
 int launch_norm(NormArgs a, hipStream_t s) {
   a.rows = norm_rows(a.T, a.N, a.y != nullptr);
   const dim3 g((unsigned)(((long long)a.T + a.rows - 1) / a.rows)), b(NTH);
   const bool stream = streams<R>(a.T, a.N);
-  if (a.y && stream) hipLaunchKernelGGL((block_norm<R, NTH, C, true, true>), g, b, 0, s, a);
-  else if (a.y) hipLaunchKernelGGL((block_norm<R, NTH, C, true, false>), g, b, 0, s, a);
-  else if (stream) hipLaunchKernelGGL((block_norm<R, NTH, C, false, true>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((block_norm<R, NTH, C, false, false>), g, b, 0, s, a);
+  if (a.y && stream) hipLaunchKernelGGL((block_norm<R, NTH, C, L, true, true>), g, b, 0, s, a);
+  else if (a.y) hipLaunchKernelGGL((block_norm<R, NTH, C, L, true, false>), g, b, 0, s, a);
+  else if (stream) hipLaunchKernelGGL((block_norm<R, NTH, C, L, false, true>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((block_norm<R, NTH, C, L, false, false>), g, b, 0, s, a);
   return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
 }
 template <class R>
 int launch_norm_of(const NormArgs& a, hipStream_t s) {
+  if (a.N <= 128) return launch_norm<R, 64, 1, 16>(a, s);
+  if (a.N <= 256) return launch_norm<R, 64, 1, 32>(a, s);
   if (a.N <= 512) return launch_norm<R, 64, 1>(a, s);
   if (a.N <= 2048) return launch_norm<R, 256, 1>(a, s);
   if (a.N <= 4096) return launch_norm<R, 512, 1>(a, s);
@@ -510,21 +549,23 @@ int launch_norm_of(const NormArgs& a, hipStream_t s) {
   return launch_norm<R, 1024, 2>(a, s);
 }
 
-template <class R, int NTH, int C, bool LEAN = false>
+template <class R, int NTH, int C, int L = 64, bool LEAN = false>
 int launch_grad(GradArgs a, hipStream_t s) {
   a.rows = grad_rows(a.T, a.N);
   const dim3 g(grad_groups(a.T, a.N)), b(NTH);
-  if (streams<R>(a.T, a.N)) hipLaunchKernelGGL((block_norm_grad<R, NTH, C, LEAN, true>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((block_norm_grad<R, NTH, C, LEAN, false>), g, b, 0, s, a);
+  if (streams<R>(a.T, a.N)) hipLaunchKernelGGL((block_norm_grad<R, NTH, C, L, LEAN, true>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((block_norm_grad<R, NTH, C, L, LEAN, false>), g, b, 0, s, a);
   return hipGetLastError() == hipSuccess ? FG_OK : FG_ELAUNCH;
 }
 template <class R>
 int launch_grad_of(const GradArgs& a, hipStream_t s) {
+  if (a.N <= 128) return launch_grad<R, 64, 1, 16>(a, s);
+  if (a.N <= 256) return launch_grad<R, 64, 1, 32>(a, s);
   if (a.N <= 512) return launch_grad<R, 64, 1>(a, s);
   if (a.N <= 2048) return launch_grad<R, 256, 1>(a, s);
   if (a.N <= 4096) return launch_grad<R, 512, 1>(a, s);
   if (a.N <= 8192) return launch_grad<R, 512, 2>(a, s);
-  return launch_grad<R, 1024, 2, true>(a, s);
+  return launch_grad<R, 1024, 2, 64, true>(a, s);
 }
 
 bool sizes_ok(int dtype, int T, int N, int gate_kind, float eps) {

@@ -76,6 +76,33 @@ def test_forward_and_gradient(T, N, dtype, parts):
     check_gradient(got, r, s, 0.75, -1.5, dtype)
 
 
+# rows side by side in a wave (four up to 128 columns, two up to 256), whole steps of them and not
+SHORT = [(1, 128), (2, 136), (3, 120), (4, 16), (5, 128), (6, 256), (7, 248), (1030, 128), (1027, 264), (2051, 200), (16390, 128),
+         (9001, 72), (9001, 256)]
+
+
+@pytest.mark.parametrize("parts", PARTS, ids=lambda p: "-".join(f"{k}={v}" for k, v in p.items()))
+@pytest.mark.parametrize("T,N", SHORT)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_short_rows(T, N, dtype, parts):
+    test_forward_and_gradient(T, N, dtype, parts)
+
+
+@pytest.mark.parametrize("T,N", [(1, 128), (3, 128), (4, 128), (5, 256), (6, 256), (1001, 128), (7001, 256), (26001, 128)])
+@pytest.mark.parametrize("quant", ["e4m3", "e4m3_pow2", "int8"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("y", [True, False])
+def test_short_rows_quantised(T, N, dtype, quant, y):
+    test_quantised_output(T, N, dtype, quant, y)
+
+
+@pytest.mark.parametrize("T,N", [(2, 16), (5, 48), (9, 112), (11, 144), (33, 240)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_short_rows_of_odd_lengths_as_integers(T, N, dtype):
+    for y in (True, False):
+        test_quantised_output(T, N, dtype, "int8", y)
+
+
 def check_gradient(got, r, s, alpha, beta, dtype):
     ref = normref.backward(host(r), host(s["dh"]), host(s["dr"]), *[host(s[n]) for n in ("y", "pre", "post", "gate")],
                            alpha, beta, EPS)
