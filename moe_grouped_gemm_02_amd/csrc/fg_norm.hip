@@ -510,16 +510,16 @@ int norm_rows(int T, int N, bool y) {
   return n * (int)((steps + most - 1) / most);
 }
 // The gradient's workgroups each write their sums and the second kernel reads them, 16 bytes a
-// column against a row's 10 (bf16) to 20: batches of some size take two or four rows a workgroup
-// at least. us, rows 1 or as the most workgroups give / 2 / 4, bf16: 200 x 2048 8.8 / 8.2 / 9.0,
-// 200 x 7168 20.2 / 16.5 / 16.7, 512 x 1024 9.9 / 9.1 / 10.3, 512 x 64 6.0 / 7.0 / 8.2, 1001 x 2048
-// 18.4 / 18.3 / 14.3, 2048 x 512 17.3 / 12.6 / 11.3, 2048 x 256 12.3 / 9.5 / 9.9.
+// column against a row's 10 (bf16) to 20: batches of some size take two or four steps a workgroup
+// at least. us, 1 (or as the most workgroups give) / 2 / 4 steps, bf16: 200 x 2048 8.8 / 8.2 / 9.0,
+// 200 x 7168 20.2 / 16.5 / 16.7, 512 x 1024 9.9 / 9.1 / 10.3, 1001 x 2048 18.4 / 18.3 / 14.3, 2048 x 512
+// 17.3 / 12.6 / 11.3; 2 / 4: 8192 x 256 15.6 / 13.8, 8192 x 64 8.2 / 9.2.
 int grad_rows(int T, int N) {
   const int most = kCUs * (N <= 2048 ? 512 / norm_threads(N) : 1);
   const int n = step_rows(N);
   const long long steps = ((long long)T + n - 1) / n;
   const int each = (int)((steps + most - 1) / most);
-  const int least = steps >= 640 && N > 256 ? 4 : steps >= (N > 512 ? 192 : 1024) ? 2 : 1;
+  const int least = steps >= (N > 256 ? 640 : 4096) ? 4 : steps >= (N > 512 ? 192 : 1024) ? 2 : 1;
   return n * (each > least ? each : least);
 }
 int grad_groups(int T, int N) { return (int)(((long long)T + grad_rows(T, N) - 1) / grad_rows(T, N)); }
