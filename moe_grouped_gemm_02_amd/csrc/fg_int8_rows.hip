@@ -10,7 +10,8 @@
 //
 // All are bound by memory traffic: a row is read once and stays in registers between
 // its largest value and its codes. A lane holds units of 16 elements, 16 bytes of
-// codes; a workgroup (or a wave, for rows of up to 1024) has one row. Measured: 8192 rows
+// codes; a workgroup (or a wave, for rows of up to 1024) has one row, and a wave 8, 4 or 2 rows
+// of up to 128, 256 or 512 side by side (65536 rows of 128 bf16 5.5 us, one a wave 15.6). Measured: 8192 rows
 // of 7168 bf16 31 us (5.7 TB/s; fp32 51 us), dispatch of 8192 tokens, k 4, H 7168 62 us
 // (weighted 64), of 128 tokens, k 8 4.6 us (latency; 8.9 with a load of each choice's row
 // in turn), silu(gate) up of 2000 rows of 2048 in 5120 7.2 us (14.4 with expf, the IEEE
@@ -32,7 +33,13 @@ constexpr int kMaxRow = 65536;   // 1024 threads of 4 units
 // The row's largest value from its NTH threads' own.
 template <int NTH>
 __device__ __forceinline__ float row_amax(uint32_t m, uint32_t* part) {
-  m = group_max_u32<64>(m);
+  if constexpr (NTH == 8) {
+    m = umax(m, dpp_u32<kQuadXor1>(m));
+    m = umax(m, dpp_u32<kQuadXor2>(m));
+    return __uint_as_float(umax(m, dpp_u32<kHalfMirror>(m)));
+  }
+  m = group_max_u32<NTH < 64 ? 16 : 64>(m);
+  if constexpr (NTH == 32) m = umax(m, (uint32_t)__shfl_xor((int)m, 16));
   if constexpr (NTH > 64) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
     __syncthreads();
@@ -78,11 +85,12 @@ __device__ __forceinline__ void store_codes(uint8_t* at, const uint32_t* q) {
 }
 
 template <class R, int MODE, int NTH, int C>
-__global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void quant_int8(RowArgs a) {
-  __shared__ uint32_t part[NTH / 64];
-  constexpr int kPerGroup = NTH == 64 ? 4 : 1;   // rows of a workgroup
-  const int lane = NTH == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const long row = a.row0 + (long)blockIdx.x * kPerGroup + (NTH == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
+__global__ __launch_bounds__(NTH <= 64 ? 256 : NTH) void quant_int8(RowArgs a) {
+  static_assert(NTH >= 64 || (C == 1 && MODE != kDispatch), "short rows: a unit a lane, no choices over the wave");
+  __shared__ uint32_t part[NTH > 64 ? NTH / 64 : 1];
+  constexpr int kPerGroup = NTH <= 64 ? 256 / NTH : 1;   // rows of a workgroup
+  const int lane = threadIdx.x % NTH, below = threadIdx.x / NTH;
+  const long row = a.row0 + (long)blockIdx.x * kPerGroup + (NTH == 64 ? __builtin_amdgcn_readfirstlane(below) : below);
   if (row >= a.T) return;
   if (MODE == kSwiglu && a.index && a.index[row] < 0) return;   // uniform over the row's threads
   const int per = a.H >> 4;
@@ -161,7 +169,7 @@ __global__ __launch_bounds__(NTH == 64 ? 256 : NTH) void quant_int8(RowArgs a) {
 // more rows take more launches.
 template <class R, int MODE, int NTH, int C>
 int launch_one(RowArgs a, hipStream_t s) {
-  constexpr int kThreads = NTH == 64 ? 256 : NTH, kRows = NTH == 64 ? 4 : 1;
+  constexpr int kThreads = NTH <= 64 ? 256 : NTH, kRows = kThreads / NTH;
   constexpr long kMost = (1L << 31) / kThreads;
   const long groups = (a.T + kRows - 1L) / kRows;
   for (long g = 0; g < groups; g += kMost) {
@@ -176,6 +184,11 @@ int launch_one(RowArgs a, hipStream_t s) {
 template <class R, int MODE>
 int launch_rows(const RowArgs& a, hipStream_t s) {
   const int per = a.H / 16;
+  if constexpr (MODE != kDispatch) {
+    if (per <= 8) return launch_one<R, MODE, 8, 1>(a, s);
+    if (per <= 16) return launch_one<R, MODE, 16, 1>(a, s);
+    if (per <= 32) return launch_one<R, MODE, 32, 1>(a, s);
+  }
   if (per <= 64) return launch_one<R, MODE, 64, 1>(a, s);
   if (per <= 128) return launch_one<R, MODE, 128, 1>(a, s);
   if (per <= 256) return launch_one<R, MODE, 256, 1>(a, s);

@@ -51,6 +51,19 @@ def test_quant_rows(T, K, dtype):
     assert np.array_equal(host(q), rq)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,K", [(8, 128), (33, 112), (31, 32), (14, 144), (130, 256), (67, 208), (9, 272), (13, 512), (131, 400)])
+def test_quant_short_rows(T, K, dtype):
+    """Several rows side by side in a wave, whole waves of them and not."""
+    test_quant_rows(T, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,I", [(37, 128), (9, 256), (35, 384), (17, 512)])
+def test_swiglu_short_rows(T, I, dtype):
+    test_swiglu(T, I, dtype)
+
+
 def test_quant_leading_dimensions_and_given_outputs():
     w = to_dev(awkward_rows(12, 256, 5).reshape(3, 4, 256))
     q = torch.empty(3, 4, 256, dtype=torch.int8, device=dev())
