@@ -76,9 +76,10 @@ def test_forward_and_gradient(T, N, dtype, parts):
     check_gradient(got, r, s, 0.75, -1.5, dtype)
 
 
-# rows side by side in a wave (four up to 128 columns, two up to 256), whole steps of them and not
+# rows side by side in a wave (four up to 128 columns, two up to 256), whole steps of them and not, and rows
+# of two waves, several a workgroup
 SHORT = [(1, 128), (2, 136), (3, 120), (4, 16), (5, 128), (6, 256), (7, 248), (1030, 128), (1027, 264), (2051, 200), (16390, 128),
-         (9001, 72), (9001, 256)]
+         (9001, 72), (9001, 256), (701, 528), (2051, 1000), (5000, 1024)]
 
 
 @pytest.mark.parametrize("parts", PARTS, ids=lambda p: "-".join(f"{k}={v}" for k, v in p.items()))
