@@ -58,11 +58,19 @@ struct Choice {
 //          N 28672 77.9 / 58.9 / 46.7 / 42.4
 //   M 128  N 4096 14.5 / 15.9 / - / 18.6    N 7168 25.6 / 17.1 / - / 19.2    N 14336 62.7 / 41.4 / - / 33.5
 //   M 512  N 1024 13.7 / 15.9 / - / 18.3    M 2048, N 256 19.8 / 20.9 / - / 18.4    M 4096, N 128, K 1024 8.6 / 7.3 / - / 5.2
-Choice skinny(int layout, int M, int N, int G, int force = -1) {
+// A short K leaves most of the waves without a piece: few rows then go by 64 columns, which have
+// the fewest, and more rows by tiles. Same order, us:
+//   M 16   N 4096  K 512 3.7 / 3.6 / 3.2 / 4.2    K 1024 3.7 / 3.6 / 3.2 / 4.9    K 2048 3.7 / 4.0 / 4.3 / 6.6
+//          N 7168  K 512 5.5 / 3.7 / 3.2 / 4.2    K 1024 5.5 / 3.7 / 4.0 / 4.9
+//   M 128  N 1024  K 256 4.2 / 5.2 / - / 3.9    K 512 4.2 / 5.2 / - / 4.3
+//          N 7168  K 512 7.4 / 5.4 / - / 4.5    K 1024 7.8 / 5.6 / - / 5.5
+Choice skinny(int layout, int M, int N, int K, int G, int force = -1) {
   Choice c;
   if (layout != FG_LAYOUT_MASKED) G = 1;
   const long w = ceil_div(M, kSkinnyRows) * ceil_div(N, 64) * G;
   int i = M > 4 * kSkinnyRows ? -1 : w <= 64 ? 0 : w <= 128 ? 1 : (w <= 320 && M <= 96) || M <= 16 ? 2 : -1;
+  if (M <= 16 && K <= 1536 && K * w <= 90000) i = 2;
+  if (M > 32 && K <= (w > 64 ? 768 : 256)) i = -1;
   if (force >= 0) i = force;
   if (i < 0) return c;
   int steps = (int)ceil_div(M < kSkinnyRows ? M : kSkinnyRows, 16);
@@ -77,7 +85,7 @@ Choice skinny(int layout, int M, int N, int G, int force = -1) {
 // columns on 256x128, contiguous ones the run-following kernel.
 Choice choose(int layout, int M, int N, int K, int G, int cus) {
   Choice best;
-  if (layout != FG_LAYOUT_CONTIGUOUS) best = skinny(layout, M, N, G);
+  if (layout != FG_LAYOUT_CONTIGUOUS) best = skinny(layout, M, N, K, G);
   if (best.tile >= 0) return best;
   double cost = 0.0;
   const double kb = (double)ceil_div(K, 128);
@@ -94,8 +102,8 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
     }
   }
   if (layout == FG_LAYOUT_CONTIGUOUS && ceil_div(M, 128) <= kRunMaxBlocks && G <= kRunMaxExperts) {
-    // G runs, half of them odd: full two-block tiles and single blocks per column
-    const long nblk = ceil_div(M, 128), runs = G < nblk ? G : nblk, S = runs / 2, F = (nblk - S) / 2;
+    // G runs, half of them odd (as many as leave whole pairs): full two-block tiles and single blocks per column
+    const long nblk = ceil_div(M, 128), runs = G < nblk ? G : nblk, S = runs / 2 + ((nblk - runs / 2) & 1), F = (nblk - S) / 2;
     const long tn = ceil_div(N, 256), items = nblk * tn, grid = items < cus ? items : cus;
     const double tf = tile_cycles(kTiles[kWide], kb), th = tile_cycles(kTiles[kHalf], kb);
     const long full = F * tn, rest = full % grid;
@@ -128,7 +136,7 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
 }
 
 #ifdef FG_TESTING
-bool forced(int layout, int M, int N, int G, int cus, Choice& c) {
+bool forced(int layout, int M, int N, int K, int G, int cus, Choice& c) {
   c = Choice();
   c.tile = t_tile;
   if (t_tile < kNumTiles) {
@@ -137,7 +145,7 @@ bool forced(int layout, int M, int N, int G, int cus, Choice& c) {
     return layout != FG_LAYOUT_CONTIGUOUS || t.bm <= 128;
   }
   if (t_tile >= kSkinny) {
-    c = skinny(layout, M, N, G, t_tile - kSkinny);
+    c = skinny(layout, M, N, K, G, t_tile - kSkinny);
     return layout != FG_LAYOUT_CONTIGUOUS && !(M > 96 && t_tile == kSkinny + 2);
   }
   c.grid = t_grid > 0 ? t_grid : cus;
@@ -163,7 +171,7 @@ int run(int layout, const void* A, const float* sa, const void* B, const float* 
   if (st != FG_OK) return st;
   Choice c = choose(layout, M, N, K, G, cus);
 #ifdef FG_TESTING
-  if (t_tile >= 0 && (!forced(layout, M, N, G, cus, c) || c.grid > kMaxTiles)) return FG_EINVAL;
+  if (t_tile >= 0 && (!forced(layout, M, N, K, G, cus, c) || c.grid > kMaxTiles)) return FG_EINVAL;
 #endif
   const Tile& t = kTiles[c.tile < kNumTiles ? c.tile : kWide];
   Params p = {};
