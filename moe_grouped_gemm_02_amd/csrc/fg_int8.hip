@@ -64,13 +64,17 @@ struct Choice {
 //          N 7168  K 512 5.5 / 3.7 / 3.2 / 4.2    K 1024 5.5 / 3.7 / 4.0 / 4.9
 //   M 128  N 1024  K 256 4.2 / 5.2 / - / 3.9    K 512 4.2 / 5.2 / - / 4.3
 //          N 7168  K 512 7.4 / 5.4 / - / 4.5    K 1024 7.8 / 5.6 / - / 5.5
+//   masked, 8 experts, N 2048: M_max 64  K 2048 13.9 / 11.0 / 10.6 / 9.0    K 7168 41.0 / 29.2 / 26.3 / 33.1
+//                              M_max 96  K 2048 16.3 / 12.3 / 12.0 / 9.0    K 4608 25.9 / 19.9 / 19.2 / 15.2
+//                                        K 7168 47.9 / 33.5 / 28.8 / 32.6
+//           10 experts, N 1728: M_max 40  K 4608 21.1 / 18.7 / 18.0 / 15.1
 Choice skinny(int layout, int M, int N, int K, int G, int force = -1) {
   Choice c;
   if (layout != FG_LAYOUT_MASKED) G = 1;
   const long w = ceil_div(M, kSkinnyRows) * ceil_div(N, 64) * G;
-  int i = M > 4 * kSkinnyRows ? -1 : w <= 64 ? 0 : w <= 128 ? 1 : (w <= 320 && M <= 96) || M <= 16 ? 2 : -1;
+  int i = M > 4 * kSkinnyRows ? -1 : w <= 64 ? 0 : w <= 128 ? 1 : (w <= 256 && M <= 96) || M <= 16 ? 2 : -1;
   if (M <= 16 && K <= 1536 && K * w <= 90000) i = 2;
-  if (M > 32 && K <= (w > 64 ? 768 : 256)) i = -1;
+  if (M > 32 && K <= (w > 128 ? M > 64 ? 6000 : 20 * w : w > 64 ? 768 : 256)) i = -1;
   if (force >= 0) i = force;
   if (i < 0) return c;
   int steps = (int)ceil_div(M < kSkinnyRows ? M : kSkinnyRows, 16);
