@@ -13,12 +13,14 @@ namespace {
 using namespace fg;
 using namespace fg::int8_cfg;
 
+// A round of a tile over the compute units takes fixed + kblocks * kblock us, measured (200 dense
+// problems of 200 to 8192 rows; the fastest by these times is 0.2% from the fastest measured).
 struct Tile {
-  int bm, bn, waves;
-  double eff;   // fraction of the matrix-core rate the tile's K loop sustains
+  int bm, bn;
+  double fixed, kblock;
 };
-constexpr Tile kTiles[] = {{256, 256, Cfg0::W, 0.80}, {256, 128, Cfg1::W, 0.75}, {128, 256, Cfg2::W, 0.75},
-                           {128, 128, Cfg3::W, 0.70}, {64, 128, Cfg4::W, 0.60}, {128, 160, Cfg5::W, 0.70}};
+constexpr Tile kTiles[] = {{256, 256, 5.0, 1.25}, {256, 128, 3.5, 0.80}, {128, 256, 3.5, 0.78},
+                           {128, 128, 2.6, 0.52}, {64, 128, 1.2, 0.345}, {128, 160, 2.7, 0.60}};
 constexpr int kNumTiles = sizeof(kTiles) / sizeof(kTiles[0]);
 constexpr int kWide = 0, kNarrow = 1, kHalf = 2;
 constexpr int kMaxK = 131056;     // 128^2 K < 2^31: the 32-bit sum is exact
@@ -30,11 +32,21 @@ constexpr long kMaxTiles = (1L << 23) - 1;
 
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
-// Estimated cycles of one tile over kblocks K-blocks: its matrix-core time at 8192
-// operations per clock, or its loads into LDS at what the path sustains, and a start and end.
-double tile_cycles(const Tile& t, double kblocks) {
-  const double mfma = t.bm * t.bn * 256.0 / (8192.0 * t.eff), mem = (t.bm + t.bn) * 128.0 / (t.waves >= 8 ? 30.0 : 24.0);
-  return kblocks * (mfma > mem ? mfma : mem) + 4000.0;
+constexpr double kLaunch = 2.0;
+
+// Estimated us of `tiles` tiles of one shape after the launch; a partial round is faster a K-block.
+double tiles_us(const Tile& t, long tiles, long cus, double kblocks) {
+  const double fill = tiles < cus ? (double)tiles / (double)cus : 1.0;
+  return (double)ceil_div(tiles, cus) * (t.fixed + kblocks * t.kblock * (0.85 + 0.15 * fill));
+}
+
+// Estimated us of weights that come from memory, as `bytes` that no cache keeps do: each of the
+// columns' workgroups fetches at most `rate` GB/s, all 5200 (128 tiles of 64 x 128 28 GB/s each, 256 20).
+double stream_us(long groups, int columns, int K, long cus, double bytes, double rate) {
+  if (bytes < 64.0e6) return 0.0;
+  const double rounds = 0.5 * ((double)ceil_div(groups, cus) + (groups > cus ? (double)groups / (double)cus : 1.0));
+  const double share = 5200.0 / (double)(groups < cus ? groups : cus);
+  return rounds * columns * (double)K * 1e-3 / (rate < share ? rate : share);
 }
 
 #ifdef FG_TESTING
@@ -49,56 +61,84 @@ struct Choice {
   int n_split = 0;
 };
 
-// The kernel that streams the weights (int8_skinny), or none where tiles are faster. By the
-// workgroups w of 128 rows and 64 columns: enough of them share a CU's time, few need narrower
-// columns to reach all CUs. Measured, us, K 7168, 16 / 32 / 64 columns and the best tile:
-//   M 16   N 2048 (w 32) 5.3 / 6.4 / 8.5 / 17.9    N 4096 (64) 6.9 / 7.1 / 8.8 / 18.1    N 7168 (112) 10.9 / 9.9 / 10.1 / 18.6
-//          N 14336 (224) 24.4 / 21.1 / 17.6 / 28.7    N 28672 (448) 46.9 / 42.7 / 37.6 / 37.6
-//   M 64   N 4096 9.6 / 10.5 / 17.5 / 18.6    N 7168 16.5 / 11.9 / 17.6 / 19.0    N 14336 42.9 / 29.8 / 25.4 / 32.9
-//          N 28672 77.9 / 58.9 / 46.7 / 42.4
-//   M 128  N 4096 14.5 / 15.9 / - / 18.6    N 7168 25.6 / 17.1 / - / 19.2    N 14336 62.7 / 41.4 / - / 33.5
-//   M 512  N 1024 13.7 / 15.9 / - / 18.3    M 2048, N 256 19.8 / 20.9 / - / 18.4    M 4096, N 128, K 1024 8.6 / 7.3 / - / 5.2
-// A short K leaves most of the waves without a piece: few rows then go by 64 columns, which have
-// the fewest, and more rows by tiles. Same order, us:
-//   M 16   N 4096  K 512 3.7 / 3.6 / 3.2 / 4.2    K 1024 3.7 / 3.6 / 3.2 / 4.9    K 2048 3.7 / 4.0 / 4.3 / 6.6
-//          N 7168  K 512 5.5 / 3.7 / 3.2 / 4.2    K 1024 5.5 / 3.7 / 4.0 / 4.9
-//   M 128  N 1024  K 256 4.2 / 5.2 / - / 3.9    K 512 4.2 / 5.2 / - / 4.3
-//          N 7168  K 512 7.4 / 5.4 / - / 4.5    K 1024 7.8 / 5.6 / - / 5.5
-//   masked, 8 experts, N 2048: M_max 64  K 2048 13.9 / 11.0 / 10.6 / 9.0    K 7168 41.0 / 29.2 / 26.3 / 33.1
-//                              M_max 96  K 2048 16.3 / 12.3 / 12.0 / 9.0    K 4608 25.9 / 19.9 / 19.2 / 15.2
-//                                        K 7168 47.9 / 33.5 / 28.8 / 32.6
-//           10 experts, N 1728: M_max 40  K 4608 21.1 / 18.7 / 18.0 / 15.1
-Choice skinny(int layout, int M, int N, int K, int G, int force = -1) {
+// The kernel that streams the weights (int8_skinny), by row blocks of 16 tm rows and 16, 32 or 64
+// columns. A workgroup loads its rows and columns once, at some 90 GB/s a CU from the L2s, so a
+// round takes what its rows + columns ask for, and small blocks on all CUs are faster than
+// large ones on a few. Measured, us, K 7168, blocks (rows x columns) and the best tile:
+//   M 16   N 2048  16x16 5.3  16x32 6.4  16x64 8.6  tile 17.9    N 7168  16x16 11.0  16x32 9.9  16x64 10.2  tile 18.6
+//   M 128  N 256  16x16 4.1  32x16 4.9  128x16 10.3  tile 17.5    N 1024  32x16 6.6  32x32 7.5  64x16 8.6  128x16 11.5  tile 18.5
+//          N 4096  64x32 10.6  32x64 11.0  128x16 14.2  tile 18.6    N 7168  128x32 16.7  64x64 17.6  32x64 17.9  tile 19.2
+//   M 1024 N 256  16x64 9.3  32x64 10.8  128x16 18.3  tile 18.4    N 1024  128x32 16.7  64x64 17.9  tile 18.8
+//          N 2048  64x64 23.2  128x32 31.1  tile 20.4
+// and K 1024: M 16, N 4096  16x64 3.2  16x32 3.7  tile 4.9    M 256, N 2048  32x64 4.2  64x32 4.4  tile 5.2
+struct SkinnyTime {
+  int tm;
+  double least[3];   // us at K to 0, for 16, 32 and 64 columns; 0: no such kernel
+};
+constexpr SkinnyTime kSkinnyTimes[] = {{1, {3.5, 3.5, 3.1}}, {2, {3.6, 3.6, 4.0}}, {3, {3.6, 4.0, 5.1}},
+                                       {4, {4.0, 4.2, 5.0}}, {6, {3.8, 4.6, 6.0}}, {8, {4.2, 5.2, 0.0}}};
+
+Choice skinny_choice(int M, int N, int G, int tm, int i) {
   Choice c;
-  if (layout != FG_LAYOUT_MASKED) G = 1;
-  const long w = ceil_div(M, kSkinnyRows) * ceil_div(N, 64) * G;
-  int i = M > 4 * kSkinnyRows ? -1 : w <= 64 ? 0 : w <= 128 ? 1 : (w <= 256 && M <= 96) || M <= 16 ? 2 : -1;
-  if (M <= 16 && K <= 1536 && K * w <= 90000) i = 2;
-  if (M > 32 && K <= (w > 128 ? M > 64 ? 6000 : 20 * w : w > 64 ? 768 : 256)) i = -1;
-  if (force >= 0) i = force;
-  if (i < 0) return c;
-  int steps = (int)ceil_div(M < kSkinnyRows ? M : kSkinnyRows, 16);
-  if (steps > 4) steps = steps <= 6 ? 6 : 8;
-  c.tile = kSkinny + 3 * (steps - 1) + i;
-  c.grid = ceil_div(M, 16 * steps) * ceil_div(N, 16 << i) * G;
-  return c.grid <= kMaxTiles ? c : Choice();
+  c.tile = kSkinny + 3 * (tm - 1) + i;
+  c.grid = ceil_div(M, 16 * tm) * ceil_div(N, 16 << i) * G;
+  return c;
 }
 
-// The shape whose tiles, in rounds over the compute units, take the fewest estimated
-// cycles; dense problems also try whole rounds of 256x256 tiles with the remaining
+// The fastest of them and its estimated time in us (1e30: none); in 400 random problems the choice
+// among these and the tiles is 1.3% from the fastest measured.
+Choice skinny(int M, int N, int K, int G, int cus, double bytes, double& us) {
+  Choice best;
+  us = 1e30;
+  // rows of parts of a 128-byte line take more loads
+  const double k = (double)K / 7168.0 * (K % 128 ? 1.25 : 1.0);
+  for (const SkinnyTime& s : kSkinnyTimes) {
+    if (s.tm > 1 && 8 * s.tm >= M) break;   // half of the rows and more past M
+    for (int i = 0; i < 3; ++i) {
+      if (s.least[i] == 0.0) continue;
+      const Choice c = skinny_choice(M, N, G, s.tm, i);
+      if (c.grid > kMaxTiles) continue;
+      // with two waves (64 columns, 48 rows and more) the loads' latency counts
+      const bool two = s.tm >= 3 && i == 2, wide = s.tm == 8 && i == 1;
+      const double base = two ? 4.7 : wide ? 4.8 : 2.4, sum = (two ? 1.5 : wide ? 1.15 : 1.3) * (s.tm + (1 << i)) * k;
+      double at = base + sum > s.least[i] ? base + sum : s.least[i];
+      if (c.grid > cus) {   // a further round; workgroups of 64 columns are resident in twos
+        const long rounds = ceil_div(c.grid, cus);
+        at += (double)(rounds - 1) * (i < 2        ? sum + 1.5
+                                      : s.tm == 1  ? 0.9 * sum + 0.3
+                                      : s.tm == 2  ? 0.9 * sum + 1.0
+                                      : s.tm == 6  ? 0.5 * sum + 5.0
+                                      : rounds > 2 ? sum + 1.8
+                                                   : 0.35 * sum + 0.7);
+      }
+      const double stream = stream_us((long)G * ceil_div(N, 16 << i), 16 << i, K, cus, bytes, 60.0);
+      if (stream > 0.7 * at) at = stream + 0.3 * at;
+      if (at < us) {
+        us = at;
+        best = c;
+      }
+    }
+  }
+  return best;
+}
+
+// The shape whose tiles, in rounds over the compute units, take the least estimated
+// time; dense problems also try whole rounds of 256x256 tiles with the remaining
 // columns on 256x128, contiguous ones the run-following kernel.
 Choice choose(int layout, int M, int N, int K, int G, int cus) {
   Choice best;
-  if (layout != FG_LAYOUT_CONTIGUOUS) best = skinny(layout, M, N, K, G);
-  if (best.tile >= 0) return best;
   double cost = 0.0;
-  const double kb = (double)ceil_div(K, 128);
+  const double kb = (double)ceil_div(K, 128), bytes = (double)(layout == FG_LAYOUT_DENSE ? 1 : G) * N * K;
   for (int i = 0; i < kNumTiles; ++i) {
     const Tile& t = kTiles[i];
     if (layout == FG_LAYOUT_CONTIGUOUS && t.bm > 128) continue;   // a tile's rows are one expert's
     const long tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn) * (layout == FG_LAYOUT_MASKED ? G : 1);
     if (tiles > kMaxTiles) continue;
-    const double c = (double)ceil_div(tiles, cus) * tile_cycles(t, kb);
+    double c = tiles_us(t, tiles, cus, kb);
+    if (layout != FG_LAYOUT_CONTIGUOUS) {
+      const double stream = stream_us(tiles / ceil_div(M, t.bm), t.bn, K, cus, bytes, (t.bn == 256 ? 22.0 : 28.0) * (K % 128 ? 0.75 : 1.0));
+      if (stream > c) c = stream;
+    }
     if (best.tile < 0 || c < cost) {
       best.tile = i;
       best.grid = tiles;
@@ -109,7 +149,7 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
     // G runs, half of them odd (as many as leave whole pairs): full two-block tiles and single blocks per column
     const long nblk = ceil_div(M, 128), runs = G < nblk ? G : nblk, S = runs / 2 + ((nblk - runs / 2) & 1), F = (nblk - S) / 2;
     const long tn = ceil_div(N, 256), items = nblk * tn, grid = items < cus ? items : cus;
-    const double tf = tile_cycles(kTiles[kWide], kb), th = tile_cycles(kTiles[kHalf], kb);
+    const double tf = tiles_us(kTiles[kWide], cus, cus, kb), th = tiles_us(kTiles[kHalf], cus, cus, kb);
     const long full = F * tn, rest = full % grid;
     const double c = rest && 2 * rest + S * tn <= grid ? (double)(full / grid) * tf + th
                                                        : (double)ceil_div(full, grid) * tf + (double)ceil_div(S * tn, grid) * th;
@@ -126,7 +166,7 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
       if (a % cus) continue;
       if (nc == N) break;   // whole rounds on the wide tile alone
       const long b = tm * ceil_div(N - nc, 128);
-      const double c = (double)(a / cus) * tile_cycles(kTiles[kWide], kb) + (double)ceil_div(b, cus) * tile_cycles(kTiles[kNarrow], kb);
+      const double c = tiles_us(kTiles[kWide], a, cus, kb) + tiles_us(kTiles[kNarrow], b, cus, kb);
       if (c < cost) {
         best.tile = kSplit;
         best.n_split = (int)nc;
@@ -136,11 +176,19 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
       break;
     }
   }
+  if (layout != FG_LAYOUT_CONTIGUOUS) {
+    const long experts = layout == FG_LAYOUT_MASKED ? G : 1, w = ceil_div(M, kSkinnyRows) * ceil_div(N, 64) * experts;
+    if (w <= 4 * cus || M <= 16) {
+      double us;
+      const Choice c = skinny(M, N, K, (int)experts, cus, bytes, us);
+      if (us < 0.97 * (kLaunch + cost)) return c;
+    }
+  }
   return best;
 }
 
 #ifdef FG_TESTING
-bool forced(int layout, int M, int N, int K, int G, int cus, Choice& c) {
+bool forced(int layout, int M, int N, int G, int cus, Choice& c) {
   c = Choice();
   c.tile = t_tile;
   if (t_tile < kNumTiles) {
@@ -149,8 +197,13 @@ bool forced(int layout, int M, int N, int K, int G, int cus, Choice& c) {
     return layout != FG_LAYOUT_CONTIGUOUS || t.bm <= 128;
   }
   if (t_tile >= kSkinny) {
-    c = skinny(layout, M, N, K, G, t_tile - kSkinny);
-    return layout != FG_LAYOUT_CONTIGUOUS && !(M > 96 && t_tile == kSkinny + 2);
+    // 16 t_grid rows a workgroup, or all up to 128
+    int tm = t_grid ? t_grid : (int)ceil_div(M < kSkinnyRows ? M : kSkinnyRows, 16);
+    if (!t_grid && tm > 4) tm = tm <= 6 ? 6 : 8;
+    c = skinny_choice(M, N, layout == FG_LAYOUT_MASKED ? G : 1, tm, t_tile - kSkinny);
+    bool there = false;
+    for (const SkinnyTime& s : kSkinnyTimes) there |= s.tm == tm && s.least[t_tile - kSkinny] > 0.0;
+    return layout != FG_LAYOUT_CONTIGUOUS && there;
   }
   c.grid = t_grid > 0 ? t_grid : cus;
   if (t_tile == kRuns) return layout == FG_LAYOUT_CONTIGUOUS;
@@ -175,7 +228,7 @@ int run(int layout, const void* A, const float* sa, const void* B, const float* 
   if (st != FG_OK) return st;
   Choice c = choose(layout, M, N, K, G, cus);
 #ifdef FG_TESTING
-  if (t_tile >= 0 && (!forced(layout, M, N, K, G, cus, c) || c.grid > kMaxTiles)) return FG_EINVAL;
+  if (t_tile >= 0 && (!forced(layout, M, N, G, cus, c) || c.grid > kMaxTiles)) return FG_EINVAL;
 #endif
   const Tile& t = kTiles[c.tile < kNumTiles ? c.tile : kWide];
   Params p = {};

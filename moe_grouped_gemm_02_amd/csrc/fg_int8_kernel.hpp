@@ -469,8 +469,8 @@ __global__ __launch_bounds__(TF::THREADS) void int8_gemm_runs(Params p) {
   });
 }
 
-// Few rows: the product is a stream of the weights. A workgroup has 16 TN columns and 16 TM
-// rows, all of them where there are so few; its waves take 128-byte pieces of K in turn and add their sums up
+// Few rows or few columns: the product is a stream of its operands. A workgroup has 16 TN columns and
+// 16 TM rows, so few that all CUs have some; its waves take 128-byte pieces of K in turn and add their sums up
 // through LDS at the end -- exact in any order, so K needs no split over workgroups and no
 // workspace. Each wave moves its pieces through a ring of STAGES slots of its own in LDS
 // (whole 128-byte lines a load; straight into the matrix core's registers a load takes 16

@@ -1,6 +1,7 @@
 """Test-only choice of the integer product's kernel: the testing library's fgt_force_int8 puts this
 thread's calls inside a ``with`` block on one compiled tile, the two-shape dense kernel or the
-run-following contiguous one, with at most `grid` workgroups where these walk their tiles."""
+run-following contiguous one, with at most `grid` workgroups where these walk their tiles; "... columns" is the weight-streaming kernel, on
+blocks of 16 `grid` rows (0: of all rows up to 128)."""
 import contextlib
 import ctypes
 

@@ -244,6 +244,25 @@ def test_dense_streamed(M, N, K, columns):
     assert np.array_equal(d_bits(D), ref_product(*a))
 
 
+@pytest.mark.parametrize("columns,rows", [(c, r) for r in (1, 2, 3, 4, 6, 8) for c in ("16 columns", "32 columns", "64 columns")
+                                          if (c, r) != ("64 columns", 8)])
+def test_streamed_on_every_block_of_rows(columns, rows):
+    for M, N, K in [(5, 72, 48), (16 * rows, 264, 1040), (40 * rows + 3, 136, 2064), (300, 200, 7168)]:
+        print(f"gemm_int8_nt {M}x{N}x{K} streamed, {16 * rows} rows, {columns}", flush=True)
+        a = operands((M,), 0, N, K, M + N + K)
+        with forced_int8(columns, rows):
+            D = fg.gemm_int8_nt(*on_gpu(*a), new_out((M, N)))
+        assert np.array_equal(d_bits(D), ref_product(*a))
+    G, M_max, N, K, counts = 5, 70, 136, 528, [70, 0, 1, 33, -2]
+    A, sa, B, sb = operands((G, M_max), G, N, K, rows)
+    with forced_int8(columns, rows):
+        D = fg.grouped_masked_int8(*on_gpu(A, sa, B, sb), new_out((G, M_max, N)), to_dev(np.array(counts, np.int32)))
+    for g, n in enumerate(counts):
+        n = max(n, 0)
+        assert np.array_equal(d_bits(D[g, :n]), ref_product(A[g, :n], sa[g, :n], B[g], sb[g]))
+        assert bool((D[g, n:].cpu().view(torch.int16) == new_out((1,)).cpu().view(torch.int16)).all())
+
+
 def contiguous_rows(G, counts, seed, extra=128):
     """m_indices of experts with so many rows each, segments padded to 128, the tail all padding; a few rows
     inside the segments are padding too, and some padding ids are out of range."""
