@@ -85,22 +85,25 @@ Choice skinny_choice(int M, int N, int G, int tm, int i) {
   return c;
 }
 
-// The fastest of them and its estimated time in us (1e30: none); in 400 random problems the choice
-// among these and the tiles is 1.3% from the fastest measured.
-Choice skinny(int M, int N, int K, int G, int cus, double bytes, double& us) {
+// The fastest of them and its estimated time in us (1e30: none). Of 400 random dense and masked
+// problems the choice among these and the tiles is 1.3% from the fastest measured on average, of 190
+// contiguous ones, whose padding the host does not know, 6% (18% faster than the best tile).
+Choice skinny(int layout, int M, int N, int K, int G, int cus, double bytes, double& us) {
   Choice best;
+  const int experts = layout == FG_LAYOUT_MASKED ? G : 1;   // whose rows are apart
   us = 1e30;
-  // rows of parts of a 128-byte line take more loads
-  const double k = (double)K / 7168.0 * (K % 128 ? 1.25 : 1.0);
+  // rows that start within a 128-byte line take more loads, few waves feel it most
+  const double k[3] = {(double)K / 7168.0 * (K % 128 ? 1.25 : 1.0), k[0], (double)K / 7168.0 * (K % 64 ? 1.5 : K % 128 ? 1.25 : 1.0)};
   for (const SkinnyTime& s : kSkinnyTimes) {
     if (s.tm > 1 && 8 * s.tm >= M) break;   // half of the rows and more past M
+    if (layout == FG_LAYOUT_CONTIGUOUS && 8 % s.tm) continue;   // within a block of 128 rows
     for (int i = 0; i < 3; ++i) {
       if (s.least[i] == 0.0) continue;
-      const Choice c = skinny_choice(M, N, G, s.tm, i);
+      const Choice c = skinny_choice(M, N, experts, s.tm, i);
       if (c.grid > kMaxTiles) continue;
       // with two waves (64 columns, 48 rows and more) the loads' latency counts
       const bool two = s.tm >= 3 && i == 2, wide = s.tm == 8 && i == 1;
-      const double base = two ? 4.7 : wide ? 4.8 : 2.4, sum = (two ? 1.5 : wide ? 1.15 : 1.3) * (s.tm + (1 << i)) * k;
+      const double base = two ? 4.7 : wide ? 4.8 : 2.4, sum = (two ? 1.5 : wide ? 1.15 : 1.3) * (s.tm + (1 << i)) * k[i];
       double at = base + sum > s.least[i] ? base + sum : s.least[i];
       if (c.grid > cus) {   // a further round; workgroups of 64 columns are resident in twos
         const long rounds = ceil_div(c.grid, cus);
@@ -111,8 +114,9 @@ Choice skinny(int M, int N, int K, int G, int cus, double bytes, double& us) {
                                       : rounds > 2 ? sum + 1.8
                                                    : 0.35 * sum + 0.7);
       }
-      const double stream = stream_us((long)G * ceil_div(N, 16 << i), 16 << i, K, cus, bytes, 60.0);
-      if (stream > 0.7 * at) at = stream + 0.3 * at;
+      if (layout == FG_LAYOUT_CONTIGUOUS) at = 1.1 * at + 0.4;   // the look-up, experts that share less of the caches
+      const double stream = stream_us((long)experts * ceil_div(N, 16 << i), 16 << i, K, cus, bytes, 60.0);
+      if (stream > 0.85 * at) at = stream + 0.15 * at;
       if (at < us) {
         us = at;
         best = c;
@@ -129,14 +133,20 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
   Choice best;
   double cost = 0.0;
   const double kb = (double)ceil_div(K, 128), bytes = (double)(layout == FG_LAYOUT_DENSE ? 1 : G) * N * K;
+  // contiguous: the experts' look-up in each round; blocks of one expert that are apart in time fetch
+  // its weights again where no cache keeps them
+  const bool contiguous = layout == FG_LAYOUT_CONTIGUOUS;
+  const long blocks = ceil_div(M, 128);
+  const double lookup = contiguous ? 1.2 : 0.0;
+  const double again = contiguous && blocks > G && bytes >= 64.0e6 ? bytes / 5.2e6 * (1.0 - (double)G / (double)blocks) : 0.0;
   for (int i = 0; i < kNumTiles; ++i) {
     const Tile& t = kTiles[i];
     if (layout == FG_LAYOUT_CONTIGUOUS && t.bm > 128) continue;   // a tile's rows are one expert's
     const long tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn) * (layout == FG_LAYOUT_MASKED ? G : 1);
     if (tiles > kMaxTiles) continue;
-    double c = tiles_us(t, tiles, cus, kb);
-    if (layout != FG_LAYOUT_CONTIGUOUS) {
-      const double stream = stream_us(tiles / ceil_div(M, t.bm), t.bn, K, cus, bytes, (t.bn == 256 ? 22.0 : 28.0) * (K % 128 ? 0.75 : 1.0));
+    double c = tiles_us(t, tiles, cus, kb) + (double)ceil_div(tiles, cus) * lookup + again;
+    if (!contiguous) {
+      const double stream = stream_us(tiles / ceil_div(M, t.bm), t.bn, K, cus, bytes, t.bn == 256 ? 22.0 : 28.0) * (K % 128 ? 1.15 : 1.0);
       if (stream > c) c = stream;
     }
     if (best.tile < 0 || c < cost) {
@@ -151,8 +161,10 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
     const long tn = ceil_div(N, 256), items = nblk * tn, grid = items < cus ? items : cus;
     const double tf = tiles_us(kTiles[kWide], cus, cus, kb), th = tiles_us(kTiles[kHalf], cus, cus, kb);
     const long full = F * tn, rest = full % grid;
-    const double c = rest && 2 * rest + S * tn <= grid ? (double)(full / grid) * tf + th
-                                                       : (double)ceil_div(full, grid) * tf + (double)ceil_div(S * tn, grid) * th;
+    // a last partial round of full tiles leaves CUs for single blocks
+    const long left = S * tn - (rest ? grid - rest : 0);
+    const double c = (double)(full / grid) * tf + (rest && 2 * rest + S * tn <= grid ? th : rest ? tf : 0.0) +
+                     (left > 0 ? (double)ceil_div(left, grid) * th : 0.0) + lookup + 0.45 * again;
     if (c < cost) {
       best.tile = kRuns;
       best.grid = grid;
@@ -176,13 +188,11 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
       break;
     }
   }
-  if (layout != FG_LAYOUT_CONTIGUOUS) {
-    const long experts = layout == FG_LAYOUT_MASKED ? G : 1, w = ceil_div(M, kSkinnyRows) * ceil_div(N, 64) * experts;
-    if (w <= 4 * cus || M <= 16) {
-      double us;
-      const Choice c = skinny(M, N, K, (int)experts, cus, bytes, us);
-      if (us < 0.97 * (kLaunch + cost)) return c;
-    }
+  const long experts = layout == FG_LAYOUT_MASKED ? G : 1, w = ceil_div(M, kSkinnyRows) * ceil_div(N, 64) * experts;
+  if (w <= 4 * cus || M <= 16) {
+    double us;
+    const Choice c = skinny(layout, M, N, K, G, cus, contiguous ? 0.0 : bytes, us);
+    if (us < (contiguous ? 0.93 : 0.97) * (kLaunch + cost)) return c;
   }
   return best;
 }
@@ -203,7 +213,7 @@ bool forced(int layout, int M, int N, int G, int cus, Choice& c) {
     c = skinny_choice(M, N, layout == FG_LAYOUT_MASKED ? G : 1, tm, t_tile - kSkinny);
     bool there = false;
     for (const SkinnyTime& s : kSkinnyTimes) there |= s.tm == tm && s.least[t_tile - kSkinny] > 0.0;
-    return layout != FG_LAYOUT_CONTIGUOUS && there;
+    return there && (layout != FG_LAYOUT_CONTIGUOUS || 8 % tm == 0);
   }
   c.grid = t_grid > 0 ? t_grid : cus;
   if (t_tile == kRuns) return layout == FG_LAYOUT_CONTIGUOUS;

@@ -510,11 +510,22 @@ __global__ __launch_bounds__(64 * T::WAVES) void int8_skinny(Params p) {
   }
   rows = min(rows - m0, 16 * TM);
   const int K = p.K, cols = min(p.N - n0, 16 * TN);
+  if (LAYOUT == kContiguous) {   // the expert of these rows' block of 128; every wave looks it up for itself
+    static_assert(LAYOUT != kContiguous || 8 % TM == 0, "blocks of rows within one of 128");
+    int top = -1;
+#pragma unroll
+    for (int r = 0; r < 16 * TM; r += 64) {
+      const int id = r + lane < rows ? p.m_indices[m0 + r + lane] : -1;
+      if (id >= 0 && id < p.G) top = max(top, id);
+    }
+    g = (int)group_max_u32<64>((uint32_t)(top + 1)) - 1;
+    if (g < 0) return;   // padding only; uniform over the workgroup
+  }
   const size_t row0 = (LAYOUT == kMasked ? (size_t)g * p.M : 0) + m0;   // of A, sa and D
   const uint8_t* Ag = p.A + row0 * K;
-  const uint8_t* Bg = p.B + ((LAYOUT == kMasked ? (size_t)g * p.N : 0) + (size_t)n0) * K;
+  const uint8_t* Bg = p.B + ((LAYOUT != kDense ? (size_t)g * p.N : 0) + (size_t)n0) * K;
   const float* sag = p.sa + row0;
-  const float* sbg = p.sb + (LAYOUT == kMasked ? (size_t)g * p.N : 0);
+  const float* sbg = p.sb + (LAYOUT != kDense ? (size_t)g * p.N : 0);
   // the scales of the D that this lane finishes
   float sa[U], sb[U][4];
 #pragma unroll
@@ -532,11 +543,23 @@ __global__ __launch_bounds__(64 * T::WAVES) void int8_skinny(Params p) {
   // A load brings 8 rows: lane l chunk (l % 8) ^ (l / 8) of row l / 8, to 16-byte slot l.
   const uint32_t chunk16 = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16), row_off = (uint32_t)(lane >> 3) * (uint32_t)K + chunk16;
   const uint32_t ring = (uint32_t)(uintptr_t)lds + wave * T::RING;
+  uint32_t no_row[LAYOUT == kContiguous ? 2 * TM : 1] = {};   // kNoRow for rows of padding or of another expert
+  if (LAYOUT == kContiguous) {
+#pragma unroll
+    for (int q = 0; q < 2 * TM; ++q) {
+      const int row = 8 * q + (lane >> 3);
+      no_row[q] = row < rows && p.m_indices[m0 + row] == g ? 0u : kNoRow;
+      asm volatile("" : "+v"(no_row[q]));   // its load completes before the DMAs
+    }
+  }
   auto load = [&](uint32_t slot, int x) {
     const uint32_t k = (uint32_t)(x * W + wave) * 128u;
     const uint32_t off = row_off | (k + chunk16 < (uint32_t)K ? 0u : kNoRow), step = 8u * (uint32_t)K;
     const uint32_t at = min(k, (uint32_t)K);   // within the buffer, of at least one row
-    static_for<2 * TM>([&](auto q) { dma16<decltype(q)::value * 1024>(rsA, off + decltype(q)::value * step, at, ring + slot); });
+    static_for<2 * TM>([&](auto q) {
+      constexpr int n = decltype(q)::value;
+      dma16<n * 1024>(rsA, (off + n * step) | no_row[LAYOUT == kContiguous ? n : 0], at, ring + slot);
+    });
     static_for<2 * TN>([&](auto q) {
       dma16<(2 * TM + decltype(q)::value) * 1024>(rsB, off + decltype(q)::value * step, at, ring + slot);
     });
@@ -607,6 +630,7 @@ __global__ __launch_bounds__(64 * T::WAVES) void int8_skinny(Params p) {
 #pragma unroll
     for (int w = 1; w < W; ++w) v += sums[(w * TM * TN + u) * 64 + lane];
     if (m >= rows || n >= p.N) continue;
+    if (LAYOUT == kContiguous && p.m_indices[m0 + m] != g) continue;
     float f[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = (float)v[e] * sa[c] * sb[c][e];

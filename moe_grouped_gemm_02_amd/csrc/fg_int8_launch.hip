@@ -22,8 +22,8 @@ hipError_t launch_tile(const Params& p, int grid, hipStream_t s) {
 }
 template <int LAYOUT, class C>
 hipError_t launch_one_skinny(const Params& p, int grid, hipStream_t s) {
-  if constexpr (LAYOUT == kContiguous) {
-    return hipErrorInvalidValue;
+  if constexpr (LAYOUT == kContiguous && 8 % C::TM != 0) {
+    return hipErrorInvalidValue;   // a block of rows is within one of 128
   } else {
     hipLaunchKernelGGL((int8_skinny<LAYOUT, C>), dim3(grid), dim3(64 * C::WAVES), 0, s, p);
     return hipGetLastError();

@@ -305,6 +305,14 @@ def test_contiguous(G, N, K, counts):
                                        ("runs", 0)])
 
 
+@pytest.mark.parametrize("rows", [1, 2, 4, 8])
+@pytest.mark.parametrize("G,N,K,counts", [(1, 8, 16, [1]), (3, 136, 272, [5, 0, 200]), (4, 264, 1040, [130, 64, 1, 33]),
+                                          (5, 72, 3088, [0, 0, 257, 7, 128])])
+def test_contiguous_streamed(G, N, K, counts, rows):
+    print(f"grouped_contiguous_int8 G={G} {N}x{K} {counts} streamed, {16 * rows} rows", flush=True)
+    check_contiguous(G, N, K, counts, [(c, rows) for c in ("16 columns", "32 columns", "64 columns") if (c, rows) != ("64 columns", 8)])
+
+
 def test_contiguous_all_padding():
     A, sa, B, sb = operands((256,), 2, 64, 64, 1)
     D = new_out((256, 64))
