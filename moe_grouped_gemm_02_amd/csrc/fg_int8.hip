@@ -93,7 +93,7 @@ Choice skinny(int layout, int M, int N, int K, int G, int cus, double bytes, dou
   const int experts = layout == FG_LAYOUT_MASKED ? G : 1;   // whose rows are apart
   us = 1e30;
   // rows that start within a 128-byte line take more loads, few waves feel it most
-  const double k[3] = {(double)K / 7168.0 * (K % 128 ? 1.25 : 1.0), k[0], (double)K / 7168.0 * (K % 64 ? 1.5 : K % 128 ? 1.25 : 1.0)};
+  const double k = (double)K / 7168.0 * (K % 128 ? 1.25 : 1.0), k64 = (double)K / 7168.0 * (K % 64 ? 1.5 : K % 128 ? 1.25 : 1.0);
   for (const SkinnyTime& s : kSkinnyTimes) {
     if (s.tm > 1 && 8 * s.tm >= M) break;   // half of the rows and more past M
     if (layout == FG_LAYOUT_CONTIGUOUS && 8 % s.tm) continue;   // within a block of 128 rows
@@ -103,7 +103,7 @@ Choice skinny(int layout, int M, int N, int K, int G, int cus, double bytes, dou
       if (c.grid > kMaxTiles) continue;
       // with two waves (64 columns, 48 rows and more) the loads' latency counts
       const bool two = s.tm >= 3 && i == 2, wide = s.tm == 8 && i == 1;
-      const double base = two ? 4.7 : wide ? 4.8 : 2.4, sum = (two ? 1.5 : wide ? 1.15 : 1.3) * (s.tm + (1 << i)) * k[i];
+      const double base = two ? 4.7 : wide ? 4.8 : 2.4, sum = (two ? 1.5 : wide ? 1.15 : 1.3) * (s.tm + (1 << i)) * (i < 2 ? k : k64);
       double at = base + sum > s.least[i] ? base + sum : s.least[i];
       if (c.grid > cus) {   // a further round; workgroups of 64 columns are resident in twos
         const long rounds = ceil_div(c.grid, cus);
@@ -141,7 +141,7 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
   const double again = contiguous && blocks > G && bytes >= 64.0e6 ? bytes / 5.2e6 * (1.0 - (double)G / (double)blocks) : 0.0;
   for (int i = 0; i < kNumTiles; ++i) {
     const Tile& t = kTiles[i];
-    if (layout == FG_LAYOUT_CONTIGUOUS && t.bm > 128) continue;   // a tile's rows are one expert's
+    if (contiguous && t.bm > 128) continue;   // a tile's rows are one expert's
     const long tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn) * (layout == FG_LAYOUT_MASKED ? G : 1);
     if (tiles > kMaxTiles) continue;
     double c = tiles_us(t, tiles, cus, kb) + (double)ceil_div(tiles, cus) * lookup + again;
@@ -155,10 +155,10 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
       cost = c;
     }
   }
-  if (layout == FG_LAYOUT_CONTIGUOUS && ceil_div(M, 128) <= kRunMaxBlocks && G <= kRunMaxExperts) {
+  if (contiguous && blocks <= kRunMaxBlocks && G <= kRunMaxExperts) {
     // G runs, half of them odd (as many as leave whole pairs): full two-block tiles and single blocks per column
-    const long nblk = ceil_div(M, 128), runs = G < nblk ? G : nblk, S = runs / 2 + ((nblk - runs / 2) & 1), F = (nblk - S) / 2;
-    const long tn = ceil_div(N, 256), items = nblk * tn, grid = items < cus ? items : cus;
+    const long runs = G < blocks ? G : blocks, S = runs / 2 + ((blocks - runs / 2) & 1), F = (blocks - S) / 2;
+    const long tn = ceil_div(N, 256), items = blocks * tn, grid = items < cus ? items : cus;
     const double tf = tiles_us(kTiles[kWide], cus, cus, kb), th = tiles_us(kTiles[kHalf], cus, cus, kb);
     const long full = F * tn, rest = full % grid;
     // a last partial round of full tiles leaves CUs for single blocks
@@ -184,6 +184,7 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
         best.n_split = (int)nc;
         best.tiles_a = a;
         best.grid = (a > b ? a : b) < cus ? (a > b ? a : b) : cus;
+        cost = c;
       }
       break;
     }
@@ -232,7 +233,7 @@ int run(int layout, const void* A, const float* sa, const void* B, const float* 
     return FG_EINVAL;
   // the largest tiles, of which choose() always has one
   const Tile& top = kTiles[layout == FG_LAYOUT_CONTIGUOUS ? kHalf : kWide];
-  if ((layout == FG_LAYOUT_MASKED ? G : 1) * ceil_div(M, top.bm) * ceil_div(N, top.bn) > kMaxTiles) return FG_EINVAL;
+  if ((layout == FG_LAYOUT_MASKED ? (double)G : 1.0) * ceil_div(M, top.bm) * ceil_div(N, top.bn) > kMaxTiles) return FG_EINVAL;
   int cus = 0;
   const int st = current_device(&cus);
   if (st != FG_OK) return st;

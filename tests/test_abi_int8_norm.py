@@ -65,7 +65,9 @@ def test_bad_arguments_are_refused(name, good, changes):
 @pytest.mark.parametrize("name,good,changes", [
     ("fg_gemm_int8_nt", DENSE, dict(M=2147483647, N=8)), ("fg_gemm_int8_nt", DENSE, dict(M=1 << 30, N=1024)),
     ("fg_grouped_contiguous_int8", CONTIGUOUS, dict(M=1 << 30, N=8)),
-    ("fg_grouped_masked_int8", MASKED, dict(G=1 << 23, M_max=1, N=8)), ("fg_grouped_masked_int8", MASKED, dict(G=1 << 22, M_max=300, N=8))],
+    ("fg_grouped_masked_int8", MASKED, dict(G=1 << 23, M_max=1, N=8)), ("fg_grouped_masked_int8", MASKED, dict(G=1 << 22, M_max=300, N=8)),
+    ("fg_grouped_masked_int8", MASKED, dict(G=2147483647, M_max=2147483647, N=4194296)),
+    ("fg_grouped_masked_int8", MASKED, dict(G=1 << 29, M_max=1 << 30, N=1 << 21))],
     ids=lambda v: v if isinstance(v, str) else "")
 def test_products_of_more_tiles_than_a_grid_are_refused(name, good, changes):
     assert call(name, good, **changes) == EINVAL
