@@ -164,7 +164,8 @@ Choice choose(int layout, int M, int N, int K, int G, int cus) {
     // a last partial round of full tiles leaves CUs for single blocks
     const long left = S * tn - (rest ? grid - rest : 0);
     const double c = (double)(full / grid) * tf + (rest && 2 * rest + S * tn <= grid ? th : rest ? tf : 0.0) +
-                     (left > 0 ? (double)ceil_div(left, grid) * th : 0.0) + lookup + 0.45 * again;
+                     (left > 0 ? (double)ceil_div(left, grid) * th : 0.0) - (left > 0 && left % grid && 4 * (left % grid) <= grid ? 0.5 * th : 0.0) +
+                     lookup + 0.45 * again;   // a last round in quarters
     if (c < cost) {
       best.tile = kRuns;
       best.grid = grid;

@@ -21,7 +21,7 @@
 // PFLOP/s of operations; this instruction alone, on normal random codes in registers,
 // 4.2, on zeros 4.9: the matrix cores' switching power sets the clock, 74% of the cycles
 // are theirs at 1.9 GHz; the 32x32x32 form alone reaches 3.5). 8 experts contiguous (8192
-// rows, N 4096, K 7168) 227-235 us, the same bound in 2.5 rounds of tiles. 16 experts
+// rows, N 4096, K 7168) 224-228 us, the same bound in 2.3 rounds of tiles. 16 experts
 // masked (M_max 256, N 7168, K 2048) 67-70 us: the stream of the weights through a tile's
 // two barriers a K-block, 4 TB/s of them; 256x224 tiles 68, 128-row tiles 80-88.
 #pragma once
@@ -418,10 +418,14 @@ __global__ __launch_bounds__(TA::THREADS) void int8_gemm_split(Params p) {
   });
 }
 
-template <class TF, class TH>
+// Where the last round's single-block tiles leave three of four workgroups idle, it runs as quarters
+// of them (8192 rows of 8 experts, N 4096, K 7168: 233 to 226 us).
+template <class TF, class TH, class TQ>
 __global__ __launch_bounds__(TF::THREADS) void int8_gemm_runs(Params p) {
   static_assert(TF::BM == 256 && TH::BM == 128 && TF::BN == TH::BN && TF::THREADS == TH::THREADS,
                 "two-block tiles of 256 rows, single-block tiles of 128 rows, same columns and workgroup");
+  static_assert(TQ::BM == 64 && 2 * TQ::BN == TH::BN && TQ::THREADS == TH::THREADS, "quarters of a single-block tile");
+  static_assert(TQ::LDS_BYTES <= TH::LDS_BYTES, "LDS of the larger tiles");
   constexpr int LDS = TF::LDS_BYTES > TH::LDS_BYTES ? TF::LDS_BYTES : TH::LDS_BYTES;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS + kRunMaxBlocks * 4];
   __shared__ int s_count[2];
@@ -438,6 +442,8 @@ __global__ __launch_bounds__(TF::THREADS) void int8_gemm_runs(Params p) {
   }
   const long halves = 2 * (full_items - whole);
   const long items = whole + halves + (long)S * tn;
+  const long last = items % grid;
+  const long quartered = last <= items - whole && 4 * last <= grid ? last : 0;   // the last round's
   long w = xcd_position(blockIdx.x, gridDim.x);
   int8_tiles<kContiguous, TF>(p, lds, [&](TileDesc& d) {
     if (w >= whole) return false;
@@ -450,9 +456,7 @@ __global__ __launch_bounds__(TF::THREADS) void int8_gemm_runs(Params p) {
   });
   wait_lgkm0();
   block_barrier();   // no wave still reads LDS of the 256-row tiles when the 128-row ones start
-  int8_tiles<kContiguous, TH>(p, lds, [&](TileDesc& d) {
-    if (w >= items) return false;
-    const long h = w - whole;
+  auto single = [&](long h) {
     int mb, nbk, e, m0;
     if (h < halves) {   // one 128-row half of a two-block tile
       raster((int)(whole + h / 2), F, tn, mb, nbk);
@@ -463,9 +467,26 @@ __global__ __launch_bounds__(TF::THREADS) void int8_gemm_runs(Params p) {
       e = list[kRunMaxBlocks - 1 - mb];
       m0 = (e & 0xffff) * 128;
     }
-    d = TileDesc{e >> 16, m0, nbk * TH::BN, p.M};
+    return TileDesc{e >> 16, m0, nbk * TH::BN, p.M};
+  };
+  int8_tiles<kContiguous, TH>(p, lds, [&](TileDesc& d) {
+    if (w >= items - quartered) return false;
+    d = single(w - whole);
     w += grid;
     return true;
+  });
+  // items - quartered are whole rounds: what is left of w is this workgroup's quarter
+  long q = w - (items - quartered);
+  if (q >= 4 * quartered) return;   // uniform over the workgroup
+  wait_lgkm0();
+  block_barrier();
+  int8_tiles<kContiguous, TQ>(p, lds, [&](TileDesc& d) {
+    if (q < 0) return false;
+    d = single(items - quartered - whole + q / 4);
+    d.m0 += (int)(q & 1) * TQ::BM;
+    d.n0 += (int)(q >> 1 & 1) * TQ::BN;
+    q = -1;
+    return d.n0 < p.N && d.m0 < p.M;
   });
 }
 

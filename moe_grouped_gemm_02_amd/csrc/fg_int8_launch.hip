@@ -60,7 +60,7 @@ hipError_t launch_int8(int tile, const Params& p, int grid, hipStream_t s) {
       }
     case kRuns:
       if constexpr (LAYOUT == kContiguous) {
-        hipLaunchKernelGGL((int8_gemm_runs<Cfg0, Cfg2>), dim3(grid), dim3(Cfg0::THREADS), 0, s, p);
+        hipLaunchKernelGGL((int8_gemm_runs<Cfg0, Cfg2, CfgQ>), dim3(grid), dim3(Cfg0::THREADS), 0, s, p);
         return hipGetLastError();
       } else {
         return hipErrorInvalidValue;

@@ -15,8 +15,9 @@ using Cfg2 = Int8Cfg<128, 256, 2, 4, 3, 3>;
 using Cfg3 = Int8Cfg<128, 128, 2, 2, 4, 3>;
 using Cfg4 = Int8Cfg<64, 128, 2, 2, 3, 3>;
 using Cfg5 = Int8Cfg<128, 160, 4, 1, 3, 3>;
+using CfgQ = Int8Cfg<64, 128, 2, 4, 4, 1>;   // quarters of Cfg2's tiles
 constexpr int kSplit = 6;   // dense: int8_gemm_split<Cfg0, Cfg1>
-constexpr int kRuns = 7;    // contiguous: int8_gemm_runs<Cfg0, Cfg2>
+constexpr int kRuns = 7;    // contiguous: int8_gemm_runs<Cfg0, Cfg2, CfgQ>
 // row blocks of 16 TM rows (contiguous: TM 1, 2, 4, 8): int8_skinny on kSkinny + 3 * (TM - 1) + i, i for 16, 32 or 64 columns.
 // LDS up to 160 KB where there is one workgroup a CU at most, 80 KB or less where two are resident (64 columns).
 constexpr int kSkinny = 8, kSkinnyRows = 128;

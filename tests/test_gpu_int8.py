@@ -305,6 +305,13 @@ def test_contiguous(G, N, K, counts):
                                        ("runs", 0)])
 
 
+def test_contiguous_last_round_in_quarters():
+    """A whole round of two-block tiles on 256 units, then 64 single blocks; the last columns' quarters are partly or
+    wholly past N, the last rows' past the experts'."""
+    for N, counts in [(2040, [1147, 1030, 1152, 1088, 1089, 1025, 1100, 1150]), (1800, [1147] * 8)]:
+        check_contiguous(8, N, 144, counts, [("runs", 256)])
+
+
 @pytest.mark.parametrize("rows", [1, 2, 4, 8])
 @pytest.mark.parametrize("G,N,K,counts", [(1, 8, 16, [1]), (3, 136, 272, [5, 0, 200]), (4, 264, 1040, [130, 64, 1, 33]),
                                           (5, 72, 3088, [0, 0, 257, 7, 128])])
