@@ -387,8 +387,11 @@ def run_own(s):
             out["s"] = sc
             out["h"] = h.view(torch.float8_e4m3fn) if quant == "e4m3" else h.to(torch.bfloat16)
         return out
-    dx, dy, dgate, dpre, dpost = fg.block_norm_grad(s["x"], dh=s["dh"], dr=s["dr"], y=s["y"], **how)
-    out = dict(dx=dx, dy=dy, dgate=dgate, dpre=dpre, dpost=dpost)
+    # alpha is the factor of a stream that a block's output is added to (alpha x + beta y): where the case has no such
+    # output the call gets the stream in its place, whose gradient dy is not asked for
+    y = s["y"] if c["y"] else s["x"]
+    dx, dy, dgate, dpre, dpost = fg.block_norm_grad(s["x"], dh=s["dh"], dr=s["dr"], y=y, **how)
+    out = dict(dx=dx, dy=dy if c["y"] else None, dgate=dgate, dpre=dpre, dpost=dpost)
     return {name: v for name, v in out.items() if v is not None}
 
 
