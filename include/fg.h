@@ -423,7 +423,8 @@ int fg_swiglu_quant_int8(const void* h, int dtype, const int32_t* slots, void* Q
 /*
  * Norms around a block, with the block's gate and the residual scales, in one pass:
  *   u = y / sqrt(mean(y^2) + eps) * post       (y itself where post is NULL)
- *   r = alpha * x + beta * gate * u            (x itself where y is NULL: r is not written)
+ *   r = alpha * x + beta * gate * u            (x itself where y is NULL: r is not written, alpha and beta
+ *                                              are not used)
  *   h = r / sqrt(mean(r^2) + eps) * pre        (pre NULL: no h), of r before its rounding
  * x (the residual stream), y (a block's output), r [T][N], bf16 or fp32 (dtype), 16-byte aligned; pre,
  * post [N] fp32; gate fp32, [N] (FG_GATE_CHANNEL) or [T] (FG_GATE_TOKEN), NULL for FG_GATE_NONE.
@@ -442,8 +443,9 @@ int fg_block_norm(const void* x, const void* y, int dtype, const float* pre, con
 /*
  * Its gradient, at r as it was stored (an 8-bit h's rounding is passed over). dh: gradient
  * of h (with pre; NULL without), dr: of r from what else reads it (NULL: none); one of them
- * at least. dx [T][N], and with y: dy [T][N], in r's type; fp32: dpre [N] (with pre), dpost [N]
- * (with post), dgate [N] or [T] (with gate). Outputs of parts that are not there may be NULL.
+ * at least. dx [T][N] (of x, which is r without y: alpha and beta are not used then), and with
+ * y: dy [T][N], in r's type; fp32: dpre [N] (with pre), dpost [N] (with post), dgate [N] or [T]
+ * (with gate). Outputs of parts that are not there may be NULL.
  * dx may be dr or dh; dy may be y. T == 0 writes zeros to dpre, dpost and a channel's dgate.
  * ws: fg_block_norm_grad_workspace bytes, 16-byte aligned. The sums over tokens are
  * fp32 in an order that depends on T and N alone.

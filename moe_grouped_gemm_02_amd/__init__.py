@@ -957,7 +957,7 @@ def block_norm(x, y=None, pre=None, post=None, gate=None, alpha=1.0, beta=1.0, e
     output (both bf16 or both fp32):
 
         u = y / sqrt(mean y^2 + eps) * post       (y itself without post [N] fp32)
-        r = alpha x + beta gate u                 (x itself without y; gate fp32 [N] or [T, 1], or none)
+        r = alpha x + beta gate u                 (x itself without y, whatever alpha; gate fp32 [N] or [T, 1], or none)
         h = r / sqrt(mean r^2 + eps) * pre        (None without pre [N] fp32), of r before its rounding
 
     Returns (r, h, s). quant None: h in x's type, s None; "e4m3" or "e4m3_pow2": h the E4M3 product's
@@ -1010,7 +1010,7 @@ def block_norm_grad(r, dh=None, dr=None, y=None, pre=None, post=None, gate=None,
     """Gradient of block_norm at the stream r it returned: dh the gradient of h (with pre), dr that of r from
     what else reads it (None: none), the other arguments as in the forward call (pre None if h was not used).
     Returns (dx, dy, dgate, dpre, dpost): dx and dy in r's type, the vectors fp32; None where the forward call
-    had no such input. dx may be dr or dh, dy may be y (in place)."""
+    had no such input. Without y, r is x: alpha and beta are not used. dx may be dr or dh, dy may be y (in place)."""
     torch = _torch()
     if (dh is None) != (pre is None):
         raise ValueError("dh and pre belong together")

@@ -8,7 +8,7 @@
 // operand (1x128 scales) or as the 8-bit integer product's (one scale per row). And the
 // gradient: with rh = r rx, yh = y ry (rx, ry the reciprocal roots), g the gate,
 //
-//     dR = dr + rx (z - rh mean(z rh)),  z = dh pre;          dx = alpha dR
+//     dR = dr + rx (z - rh mean(z rh)),  z = dh pre;          dx = alpha dR (dR without y)
 //     dy = ry (v - yh mean(v yh)),       v = beta g post dR   (dy = v without post)
 //     dpre = sum_t dh rh,   S = sum_t dR yh (times the token's gate)
 //     dpost = beta g S,     dgate = beta post S  per channel, beta sum_n dR yh post per token
@@ -626,7 +626,7 @@ int fg_block_norm_grad(const void* r, const void* dh, const void* dr, const void
   if (st != FG_OK) return st;
   if (T > 0) {
     const GradArgs a = {r, dh, dr, y, pre, post, gate, dx, dy, dgate, static_cast<float*>(ws), T, N, 1, gate_kind,
-                        alpha, beta, eps, 1.0f / (float)N};
+                        y ? alpha : 1.0f, beta, eps, 1.0f / (float)N};   // without y the stream is x itself
     const int rc = dtype == FG_BF16 ? launch_grad_of<RowBf16>(a, stream) : launch_grad_of<RowF32>(a, stream);
     if (rc != FG_OK) return rc;
   }

@@ -34,7 +34,10 @@ def forward(x, y, pre, post, gate, alpha, beta, eps):
 
 
 def backward(r, dh, dr, y, pre, post, gate, alpha, beta, eps):
-    """dict of (value, bound): dx, dy, dgate, dpre, dpost, as far as they exist."""
+    """dict of (value, bound): dx, dy, dgate, dpre, dpost, as far as they exist. Without y the stream r is x itself, as
+    in forward, and alpha has no part in it."""
+    if y is None:
+        alpha = 1.0
     T, N = r.shape
     out = {}
     dR = np.zeros((T, N)) if dr is None else dr
