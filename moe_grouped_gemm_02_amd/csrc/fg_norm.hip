@@ -444,8 +444,8 @@ __global__ __launch_bounds__(NTH) void block_norm_grad(GradArgs a) {
     for (int c = 0; c < C; ++c) {
       float f[8], o[8];
       y[c].unpack(f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = k * fmaf(-f[e] * ry, m, d[c][e]);
+#pragma unroll   // without post m is 0, and an infinite y would make NaN of it
+      for (int e = 0; e < 8; ++e) o[e] = k * (a.post ? fmaf(-f[e] * ry, m, d[c][e]) : d[c][e]);
       store8<R, STREAM>(rows_at(a.dy, t), unit(c), o);
     }
   }
