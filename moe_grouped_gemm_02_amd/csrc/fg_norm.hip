@@ -495,8 +495,9 @@ __global__ __launch_bounds__(kSumCols * kSumParts) void block_norm_sums(SumArgs 
   s += __shfl_xor(s, 32);
   if (p != 0 || n >= a.N) return;
   if (!of_s) a.dpre[n] = s;
-  if (of_s && a.dpost) a.dpost[n] = a.beta * (a.gate ? a.gate[n] : 1.0f) * s;
-  if (of_s && a.dgate) a.dgate[n] = a.beta * (a.post ? a.post[n] : 1.0f) * s;
+  const bool rows = a.groups > 0;   // without rows zeros, infinite weights or not
+  if (of_s && a.dpost) a.dpost[n] = rows ? a.beta * (a.gate ? a.gate[n] : 1.0f) * s : 0.0f;
+  if (of_s && a.dgate) a.dgate[n] = rows ? a.beta * (a.post ? a.post[n] : 1.0f) * s : 0.0f;
 }
 
 // Threads of a workgroup and rows it takes one after another, for T rows of N columns: as
