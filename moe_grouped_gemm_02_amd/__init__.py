@@ -30,6 +30,7 @@ their output in the row's type or as either product's operand.
 """
 import ctypes
 import functools
+import math
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -789,6 +790,14 @@ def _is(t, dtype, shape, index):
     return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _too_large(*sizes):
+    """Raised by the calls below for sizes past a C int, of which ctypes would pass on the low 32 bits."""
+    raise ValueError(f"every size must be below 2^31, got {max(sizes)}")
+
+
 def _int8_product(fn, A, sa, B, sb, D, lead, N, K, index, *sizes):
     """Checks and makes the call of an integer product; lead: the leading dimensions of A and D, index: the
     layout's tensor with its name and shape (None: dense), sizes: the call's."""
@@ -808,6 +817,8 @@ def _int8_product(fn, A, sa, B, sb, D, lead, N, K, index, *sizes):
             _dev(index[0], index[1], index[2], torch.int32, dev)
     if K % 16 or not 16 <= K <= 131056 or N % 8:
         raise ValueError("K must be a multiple of 16 from 16 to 131056 and N of 8")
+    if max(sizes) > _INT_MAX:
+        _too_large(*sizes)
     stream = _raw_stream(d) if _raw_stream is not None else _stream(A)
     if index is None:
         _call(fn, A.device, A.data_ptr(), sa.data_ptr(), B.data_ptr(), sb.data_ptr(), D.data_ptr(), *sizes, stream)
@@ -854,6 +865,9 @@ def _int8_rows(x, lead, K, q, s):
     torch = _torch()
     if K % 16 or not 16 <= K <= 65536:
         raise ValueError("rows must be a multiple of 16 long, from 16 to 65536")
+    rows = math.prod(lead)
+    if rows > _INT_MAX:
+        _too_large(rows)
     shape = tuple(lead) + (K,)
     if q is None:
         q = torch.empty_like(x, dtype=torch.int8) if x.shape == shape else torch.empty(shape, dtype=torch.int8, device=x.device)
@@ -885,6 +899,8 @@ def dispatch_quant_int8(x, plan, w=None, Q=None, s=None):
         raise ValueError(f"x has shape {tuple(x.shape)}, expected [{T}, columns]")
     H = x.shape[1]
     _dev(x, "x", (T, H), None, dev)
+    if T > _INT_MAX or k > _INT_MAX:
+        _too_large(T, k)
     if w is not None:
         _dev(w, "w", (T, k), _torch().float32, dev)
     Q, s = _int8_rows(x, plan.lead, H, Q, s)
@@ -931,6 +947,8 @@ def _norm_args(x, name, y, pre, post, gate, eps):
     T, N = shape
     if not (d >= 0 and x.is_contiguous()):
         _dev(x, name, shape)
+    if T > _INT_MAX:
+        _too_large(T)
     if N % 8 or not 8 <= N <= 16384:
         raise ValueError("N must be a multiple of 8 from 8 to 16384")
     if not eps > 0:
