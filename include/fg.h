@@ -428,7 +428,8 @@ int fg_swiglu_quant_int8(const void* h, int dtype, const int32_t* slots, void* Q
  *   h = r / sqrt(mean(r^2) + eps) * pre        (pre NULL: no h), of r before its rounding
  * x (the residual stream), y (a block's output), r [T][N], bf16 or fp32 (dtype), 16-byte aligned; pre,
  * post [N] fp32; gate fp32, [N] (FG_GATE_CHANNEL) or [T] (FG_GATE_TOKEN), NULL for FG_GATE_NONE.
- * r may be x or y, and h may be either where it has their type, but not both the same.
+ * r may be x or y, and h may be either where it has their type (8-bit codes there are refused), but not
+ * both the same.
  *   out: FG_OUT_SAME: h [T][N] in x's type, s unused. FG_OUT_E4M3 / FG_OUT_E4M3_POW2: codes
  *   h [T][N] and scales s [N/128][T] as fg_quant_act_1x128(_pow2) makes them (N % 128 == 0; r finite).
  *   FG_OUT_INT8: codes h [T][N] and s [T] as fg_quant_int8 (N % 16 == 0).

@@ -593,6 +593,7 @@ int fg_block_norm(const void* x, const void* y, int dtype, const float* pre, con
   if (!x || (!y && !pre) || (y && !r) || (!y && (post || gate_kind != FG_GATE_NONE))) return FG_EINVAL;
   if ((gate_kind != FG_GATE_NONE) != (gate != nullptr) || (pre && (!h || (out != FG_OUT_SAME && !s)))) return FG_EINVAL;
   if (y && pre && r == h) return FG_EINVAL;   // two outputs
+  if (pre && out != FG_OUT_SAME && (h == x || h == y)) return FG_EINVAL;   // codes lie over other rows
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(r, 16) || !aligned(h, 16) || !aligned(pre, 4) || !aligned(post, 4) ||
       !aligned(gate, 4) || !aligned(s, 4))
     return FG_EINVAL;
