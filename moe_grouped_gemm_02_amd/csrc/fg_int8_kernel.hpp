@@ -32,11 +32,10 @@
 namespace fg {
 
 // Compile-time tile configuration: as TileCfg, without scales in the rings.
-template <int BM_, int BN_, int WGM_, int WGN_, int STAGES_, int PD_ = 2, bool FA2_ = false, int ASTAGES_ = STAGES_>
+template <int BM_, int BN_, int WGM_, int WGN_, int STAGES_, int PD_>
 struct Int8Cfg {
-  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, STAGES = STAGES_, ASTAGES = ASTAGES_;
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, STAGES = STAGES_;
   static constexpr int PD = PD_, RING = PD_ + 1;
-  static constexpr bool FA2 = FA2_;
   static constexpr int W = WGM * WGN, THREADS = 64 * W;
   static constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
   static constexpr int A_INSTR = (BM * 8 + 64 * W - 1) / (64 * W);
@@ -47,12 +46,12 @@ struct Int8Cfg {
   static constexpr int SC_LOADS = BM / 64 + (BN + 63) / 64;   // 64 scales a load
   static constexpr int SC_BYTES = SC_LOADS * 256;
   static constexpr int A_BASE = 2 * SC_BYTES;
-  static constexpr int B_BASE = A_BASE + ASTAGES * A_BYTES;
+  static constexpr int B_BASE = A_BASE + STAGES * A_BYTES;
   static constexpr int LDS_BYTES = B_BASE + STAGES * B_BYTES;
-  static constexpr int UNROLL = lcm_c(lcm_c(lcm_c(STAGES, ASTAGES), RING / gcd_c(TN, RING)), FA2 ? 2 : 1);
+  static constexpr int UNROLL = lcm_c(STAGES, RING / gcd_c(TN, RING));
   static_assert(WM % 16 == 0 && WN % 32 == 0 && BM % 64 == 0, "whole sub-tile pairs, scales 64 at a time");
   static_assert(BM % WGM == 0 && BN % WGN == 0, "waves must split the tile evenly");
-  static_assert(ASTAGES >= 2 && ASTAGES <= STAGES && (STAGES != 2 || ASTAGES == 2), "ring depths");
+  static_assert(STAGES >= 2, "ring depth");
   static_assert(STAGES * DMA_PER_STAGE <= 63, "too many DMA instructions in flight per wave");
   static_assert(LDS_BYTES <= 160 * 1024, "LDS exceeds 160 KB");
   static_assert(PD >= 1 && PD <= TN - 1, "prefetch distance must leave the barrier inside the K-block");
@@ -154,19 +153,19 @@ __device__ __forceinline__ void int8_tiles(const Params& p, lds_u8* const lds, N
       else if (i < T::SC_LOADS) dma4<0>(rsSB, (uint32_t)((i - BM / 64) * 64 + lane) * 4u, 0u, at + i * 256);
     }
   };
-  // Scalar offsets of one DMA group, A of K-block ka and B of K-block kbb, and what
-  // puts a lane's chunk past the buffer where it lies past K.
+  // Scalar offset of the DMAs of K-block kb (or of the last one), and what puts a lane's
+  // chunk past the buffer where it lies past K.
   struct Soff {
-    uint32_t a, b, past_a, past_b;
+    uint32_t at, past;
   };
-  auto soff_of = [&](int ka, int kbb) {
-    const uint32_t a = (uint32_t)ka * (uint32_t)kKBlock, b = (uint32_t)kbb * (uint32_t)kKBlock;
-    return Soff{a, b, a + chunk16 >= (uint32_t)K ? kNoRow : 0u, b + chunk16 >= (uint32_t)K ? kNoRow : 0u};
+  auto soff_of = [&](int kb) {
+    const uint32_t at = (uint32_t)min(kb, nkb - 1) * (uint32_t)kKBlock;
+    return Soff{at, at + chunk16 >= (uint32_t)K ? kNoRow : 0u};
   };
-  auto issue = [&](auto d_c, auto ast_c, auto bst_c, const Soff& o) {
-    constexpr int d = decltype(d_c)::value, AST = decltype(ast_c)::value, BST = decltype(bst_c)::value;
-    if constexpr (d < NA) dma16<T::A_BASE + AST * T::A_BYTES + d * W * 1024>(rsA, a_off[d] | o.past_a, o.a, wave_at);
-    else dma16<T::B_BASE + BST * T::B_BYTES + (d - NA) * W * 1024>(rsB, b_off[d - NA] | o.past_b, o.b, wave_at);
+  auto issue = [&](auto d_c, auto st_c, const Soff& o) {
+    constexpr int d = decltype(d_c)::value, ST = decltype(st_c)::value;
+    if constexpr (d < NA) dma16<T::A_BASE + ST * T::A_BYTES + d * W * 1024>(rsA, a_off[d] | o.past, o.at, wave_at);
+    else dma16<T::B_BASE + ST * T::B_BYTES + (d - NA) * W * 1024>(rsB, b_off[d - NA] | o.past, o.at, wave_at);
   };
   auto fragA = [&](auto st_c, auto i_c) {
     return frag_at<T::A_BASE + decltype(st_c)::value * T::A_BYTES + decltype(i_c)::value * 2048>(aLo, aHi);
@@ -179,29 +178,19 @@ __device__ __forceinline__ void int8_tiles(const Params& p, lds_u8* const lds, N
   using SCH = Sched<T>;
   constexpr int STEPS = SCH::STEPS, PRE = SCH::PRE, POST = SCH::POST, D = SCH::D;
   constexpr bool SPLIT = SCH::SPLIT;
-  constexpr int SA = T::ASTAGES, SB = T::STAGES;
-  constexpr int B_AFTER_A = SA == SB ? 0 : NB;
-  constexpr int WAIT_LOOP = SPLIT ? SCH::n_early() : B_AFTER_A + (SA - 2) * D;
-  constexpr int WAIT_PRO = SPLIT ? D : B_AFTER_A + (SA - 2) * D + SCH::n_head();
+  constexpr int S = T::STAGES;
+  constexpr int WAIT_LOOP = SPLIT ? SCH::n_early() : (S - 2) * D;
+  constexpr int WAIT_PRO = SPLIT ? D : (S - 2) * D + SCH::n_head();
   constexpr int NST = TM * (TN / 2);   // output stores per wave and tile
   static_assert(WAIT_PRO + NST < 64 && WAIT_LOOP < 64, "vmcnt counter range");
   auto prologue = [&]() {
-    if constexpr (SPLIT) {
-      static_for<2>([&](auto x_c) {
-        const Soff o = soff_of(min((int)decltype(x_c)::value, nkb - 1), min((int)decltype(x_c)::value, nkb - 1));
-        static_for<D>([&](auto d_c) { issue(d_c, x_c, x_c, o); });
+    static_for<S>([&](auto x_c) {
+      constexpr int x = decltype(x_c)::value;
+      const Soff o = soff_of(x);
+      static_for<D>([&](auto d_c) {   // S >= 3: the rest of the last stage comes with the first K-block
+        if constexpr (SPLIT || x != S - 1 || SCH::slot(decltype(d_c)::value) < POST) issue(d_c, x_c, o);
       });
-    } else {
-      static_for<SB>([&](auto x_c) {
-        constexpr int x = decltype(x_c)::value, ka = x - SB + SA;
-        const Soff o = soff_of(min(ka < 0 ? 0 : ka, nkb - 1), min(x, nkb - 1));
-        static_for<D>([&](auto d_c) {
-          constexpr int d = decltype(d_c)::value;
-          if constexpr (!(d < NA && ka < 0) && !(x == SB - 1 && SCH::slot(d) >= POST))
-            issue(d_c, std::integral_constant<int, (ka < 0 ? 0 : ka)>{}, x_c, o);
-        });
-      });
-    }
+    });
   };
   int par = 0;
   setup(cur, par);
@@ -217,36 +206,25 @@ __device__ __forceinline__ void int8_tiles(const Params& p, lds_u8* const lds, N
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    i32x8 fbr[R], fa[T::FA2 ? 2 : 1][TM];
+    i32x8 fbr[R], fa[TM];
     {
       using Z = std::integral_constant<int, 0>;
-      if constexpr (T::FA2)
-        static_for<TM>([&](auto i_c) {
-          fa[0][decltype(i_c)::value] = fragA(Z{}, i_c);
-          __builtin_amdgcn_sched_barrier(0);
-        });
       static_for<PD>([&](auto c_c) {
         fbr[decltype(c_c)::value] = fragB(Z{}, c_c);
         __builtin_amdgcn_sched_barrier(0);
       });
-      if constexpr (!T::FA2)
-        static_for<TM>([&](auto i_c) {
-          fa[0][decltype(i_c)::value] = fragA(Z{}, i_c);
-          __builtin_amdgcn_sched_barrier(0);
-        });
+      static_for<TM>([&](auto i_c) {
+        fa[decltype(i_c)::value] = fragA(Z{}, i_c);
+        __builtin_amdgcn_sched_barrier(0);
+      });
     }
     int kb = 0;
     auto kblock = [&](auto ph_c) -> bool {
       constexpr int PH = decltype(ph_c)::value, U = T::UNROLL;
-      constexpr int CA = PH % SA, NXA = (PH + 1) % SA, TA = (PH + U - 1) % SA;
-      constexpr int CB = PH % SB, NXB = (PH + 1) % SB, TB = (PH + U - 1) % SB;
-      constexpr int FSET = T::FA2 ? (PH & 1) : 0, NFSET = T::FA2 ? ((PH + 1) & 1) : 0;
-      using NxtA = std::integral_constant<int, NXA>;
-      using CurA = std::integral_constant<int, CA>;
-      using CurB = std::integral_constant<int, CB>;
-      using NxtB = std::integral_constant<int, NXB>;
-      const Soff head = soff_of(min(kb + SA, nkb - 1), min(kb + SB, nkb - 1));
-      const Soff tail = soff_of(min(kb - 1 + SA, nkb - 1), min(kb - 1 + SB, nkb - 1));
+      using Cur = std::integral_constant<int, PH % S>;
+      using Nxt = std::integral_constant<int, (PH + 1) % S>;
+      using Tail = std::integral_constant<int, (PH + U - 1) % S>;
+      const Soff head = soff_of(kb + S), tail = soff_of(kb - 1 + S);
       (void)tail;
       static_for<STEPS>([&](auto u_c) {
         constexpr int u = decltype(u_c)::value, j = u / TM, i = u % TM;
@@ -255,25 +233,22 @@ __device__ __forceinline__ void int8_tiles(const Params& p, lds_u8* const lds, N
           wait_lgkm0();
           wait_vm<WAIT_LOOP>();
           block_barrier();
-          if constexpr (T::FA2)
-            static_for<TM>([&](auto ii_c) { fa[NFSET][decltype(ii_c)::value] = fragA(NxtA{}, ii_c); });
         }
-        acc[i][j] = mfma_i8_lo(fbr[(PH * TN + j) % R], fa[FSET][i], acc[i][j]);
-        acc[i][j] = mfma_i8_hi(fbr[(PH * TN + j) % R], fa[FSET][i], acc[i][j]);
+        acc[i][j] = mfma_i8_lo(fbr[(PH * TN + j) % R], fa[i], acc[i][j]);
+        acc[i][j] = mfma_i8_hi(fbr[(PH * TN + j) % R], fa[i], acc[i][j]);
         if constexpr (i == 0) {
           constexpr int jn = j + PD, slot = (PH * TN + jn) % R;
-          if constexpr (jn < TN) fbr[slot] = fragB(CurB{}, std::integral_constant<int, jn>{});
-          else fbr[slot] = fragB(NxtB{}, std::integral_constant<int, jn - TN>{});
+          if constexpr (jn < TN) fbr[slot] = fragB(Cur{}, std::integral_constant<int, jn>{});
+          else fbr[slot] = fragB(Nxt{}, std::integral_constant<int, jn - TN>{});
         }
-        if constexpr (!T::FA2 && j == TN - 1) fa[0][i] = fragA(NxtA{}, std::integral_constant<int, i>{});
+        if constexpr (j == TN - 1) fa[i] = fragA(Nxt{}, std::integral_constant<int, i>{});
         static_for<D>([&](auto d_c) {
           constexpr int d = decltype(d_c)::value;
           if constexpr (SPLIT) {
-            if constexpr (SCH::slot(d) == u) issue(d_c, CurA{}, CurB{}, head);
+            if constexpr (SCH::slot(d) == u) issue(d_c, Cur{}, head);
           } else {
-            if constexpr (u >= PRE && SCH::slot(d) == u - PRE) issue(d_c, CurA{}, CurB{}, head);
-            if constexpr (u < PRE && SCH::slot(d) == POST + u)
-              issue(d_c, std::integral_constant<int, TA>{}, std::integral_constant<int, TB>{}, tail);
+            if constexpr (u >= PRE && SCH::slot(d) == u - PRE) issue(d_c, Cur{}, head);
+            if constexpr (u < PRE && SCH::slot(d) == POST + u) issue(d_c, Tail{}, tail);
           }
         });
         int8_step_fence();
