@@ -13,8 +13,8 @@ namespace {
 using namespace fg;
 using namespace fg::int8_cfg;
 
-// A round of a tile over the compute units takes fixed + kblocks * kblock us, measured (200 dense
-// problems of 200 to 8192 rows; the fastest by these times is 0.2% from the fastest measured).
+// A round of a tile over the compute units takes fixed + kblocks * kblock us, fitted to the times of
+// 200 dense problems of 200 to 8192 rows.
 struct Tile {
   int bm, bn;
   double fixed, kblock;
@@ -85,9 +85,10 @@ Choice skinny_choice(int M, int N, int G, int tm, int i) {
   return c;
 }
 
-// The fastest of them and its estimated time in us (1e30: none). Of 400 random dense and masked
-// problems the choice among these and the tiles is 1.3% from the fastest measured on average, of 190
-// contiguous ones, whose padding the host does not know, 6% (18% faster than the best tile).
+// The fastest of them and its estimated time in us (1e30: none). Of 220 random dense and masked
+// problems the choice among these and the tiles is 1.4% from the fastest measured on average and 24%
+// at most, of 90 contiguous ones, whose padding the host does not know, 6% and 47% (12% faster than
+// the best tile on average, 24% slower at most).
 Choice skinny(int layout, int M, int N, int K, int G, int cus, double bytes, double& us) {
   Choice best;
   const int experts = layout == FG_LAYOUT_MASKED ? G : 1;   // whose rows are apart

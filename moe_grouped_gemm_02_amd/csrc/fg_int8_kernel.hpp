@@ -18,12 +18,12 @@
 // offsets past the buffer and read as zeros.
 //
 // What bounds it, measured on one MI355X: 8192 x 7168 x 18432 takes 726-750 us (2.9-3.0
-// PFLOP/s of operations; this instruction alone, on normal random codes in registers,
-// 4.2, on zeros 4.9: the matrix cores' switching power sets the clock, 74% of the cycles
-// are theirs at 1.9 GHz; the 32x32x32 form alone reaches 3.5). 8 experts contiguous (8192
-// rows, N 4096, K 7168) 224-228 us, the same bound in 2.3 rounds of tiles. 16 experts
-// masked (M_max 256, N 7168, K 2048) 67-70 us: the stream of the weights through a tile's
-// two barriers a K-block, 4 TB/s of them; 256x224 tiles 68, 128-row tiles 80-88.
+// POP/s; this instruction alone, on normal random codes in registers, 4.2, on zeros 4.9, the
+// 32x32x32 form 3.5). The matrix cores are busy 74-78% of the cycles -- the rest are a K-block's
+// two barriers and the tiles' ends -- and the clock is 1.8-1.9 GHz, where the instruction alone
+// has 2.0. 8 experts contiguous (8192 rows, N 4096, K 7168) 220-228 us, the same in 2.3 rounds of
+// tiles. 16 experts masked (M_max 256, N 7168, K 2048) 67-70 us: the stream of the weights through
+// those barriers, 3.4 TB/s of them (3.9 of all that moves); 256x224 tiles 68, 128-row tiles 80-88.
 #pragma once
 
 #include "fg_kernel.hpp"

@@ -12,10 +12,11 @@
 // its largest value and its codes. A lane holds units of 16 elements, 16 bytes of
 // codes; a workgroup (or a wave, for rows of up to 1024) has one row, and a wave 8, 4 or 2 rows
 // of up to 128, 256 or 512 side by side (65536 rows of 128 bf16 5.5 us, one a wave 15.6). Measured: 8192 rows
-// of 7168 bf16 31 us (5.7 TB/s; fp32 51 us), dispatch of 8192 tokens, k 4, H 7168 62 us
-// (weighted 64), of 128 tokens, k 8 4.6 us (latency; 8.9 with a load of each choice's row
-// in turn), silu(gate) up of 2000 rows of 2048 in 5120 7.2 us (14.4 with expf, the IEEE
-// division and half of the threads idle).
+// of 7168 bf16 31 us (5.7 TB/s; fp32 51 us), dispatch of 8192 tokens, 4 of 64 experts, H 7168 67 us
+// (weighted 72), of 128 tokens, k 8 4.3-4.6 us (latency; 8.9 with a load of each choice's row
+// in turn), silu(gate) up of 2000 rows of 2048 in 5120 7.5 us (14.4 with expf, the IEEE
+// division and half of the threads idle), of 8192 rows of 2048 15.6 us (5.4 TB/s; fp32 28), of
+// 128 rows 3.2.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

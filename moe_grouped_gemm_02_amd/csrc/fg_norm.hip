@@ -20,8 +20,8 @@
 // gradient's column sums S and sum dh rh stay in registers until a workgroup's rows are
 // done; a second kernel adds the workgroups' sums in a fixed order. The next row is on its
 // way while this one goes through its barriers. Measured, T 8192, N 7168, bf16: forward to
-// E4M3 84-86 us (4.9 TB/s; a row a workgroup at a time 108), in bf16 92, without y 40;
-// gradient 140 + 6.5 us (4.8 TB/s; without the row ahead, rows as floats 200 + 27). T 32
+// E4M3 84-86 us (4.9 TB/s; a row a workgroup at a time 108), as integers 83, in bf16 92-94, without y
+// 41, 37 and 47; gradient 140 + 6.5 us (4.8 TB/s; without the row ahead, rows as floats 200 + 27). T 32
 // forward 4.2 us, latency. T 1001, N 2048, fp32, gradient 12.8 + 3.9.
 #include <hip/hip_runtime.h>
 

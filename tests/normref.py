@@ -3,8 +3,8 @@
 import numpy as np
 
 U32 = 2.0 ** -24
-# A thread adds up to 32 squares in turn, then 6 steps of lanes, then up to 16 waves: 54 roundings of
-# terms of one sign. The mean's product, the sum with eps, the root and the division: 4 more.
+# A thread adds up to 16 squares in turn, then 6 steps of lanes, then up to 16 waves: 38 roundings of
+# terms of one sign (54 are allowed for). The mean's product, the sum with eps, the root and the division: 4 more.
 SUM = 58
 
 
